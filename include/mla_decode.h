@@ -23,7 +23,7 @@
  *  - Device work is enqueued on `stream` (a cudaStream_t passed as void*;
  *    NULL = the legacy default stream) and is asynchronous. mla_decode,
  *    mla_combine, mla_combine_v_up, mla_combine_inv_rope, mla_kv_write,
- *    mla_kv_write_norm_rope and mla_kv_gather perform no host synchronisation and
+ *    mla_kv_write_norm_rope, mla_qkv_norm_rope, mla_kv_read and mla_kv_gather perform no host synchronisation and
  *    no device allocation.
  *  - bf16 = IEEE bfloat16 bit patterns (uint16); all row-major, contiguous.
  *
@@ -39,6 +39,18 @@
  *                       page_bytes = page_size*648 rounded up to a multiple of 640.
  *                       K = [dequantised 512 | RoPE 64], V = K[0:512].
  *  A NoPE value is e4m3(byte) * 2^(scale_byte - 127).
+ *  MLA_KV_FP4_448_UE8M0 row = [448 e2m1 NoPE, two per byte | 64 bf16 RoPE] (352 B); element 2i
+ *                       is the low nibble of byte i, 2i + 1 the high one. After the rows,
+ *                       page_size 16-byte scale slots (14 ue8m0 bytes, one per 32 NoPE
+ *                       elements, + 2 zero bytes); page_bytes = page_size*368 rounded up to
+ *                       a multiple of 352. K = V = the 512-wide row.
+ *  MLA_KV_FP4_512_UE8M0 the same with 512 e2m1 NoPE (384 B rows, 16 scale bytes);
+ *                       page_bytes = page_size*400 rounded up to a multiple of 384.
+ *                       K = [dequantised 512 | RoPE 64], V = K[0:512].
+ *  A 4-bit NoPE value is e2m1(code) * 2^(scale_byte - 127); e2m1 = {0, 0.5, 1, 1.5, 2, 3, 4, 6}
+ *  for codes 0-7, and their negatives for 8-15; scale byte 255 is NaN (OCP MX formats).
+ *  Reading 4-bit rows, the decode passes the softmax weights to the value product as one
+ *  bf16 each (as it does for bf16 rows; the fp8 layouts pass a pair).
  */
 #ifndef MLA_DECODE_H_
 #define MLA_DECODE_H_
@@ -67,7 +79,9 @@ extern "C" {
 typedef enum {
   MLA_KV_BF16_576 = 0,
   MLA_KV_FP8_448_UE8M0 = 1,
-  MLA_KV_FP8_512_UE8M0 = 2
+  MLA_KV_FP8_512_UE8M0 = 2,
+  MLA_KV_FP4_448_UE8M0 = 3,
+  MLA_KV_FP4_512_UE8M0 = 4
 } mla_kv_layout;
 
 /* Sizes the kernels are built for. */
@@ -141,7 +155,7 @@ int mla_decode_plan(const int32_t* cache_seqlens, int32_t batch, int32_t q_token
  * "Data-Movement Friendly Approach"; "Implementation:Sgl project Sglang Flash
  * MLA", I/O Contract).
  *  q            device bf16 [T = batch*q_tokens_per_req, num_heads, Dqk]
- *               (Dqk = 576, or 512 for MLA_KV_FP8_448_UE8M0), 16-byte aligned.
+ *               (Dqk = 576, or 512 for the 448-NoPE layouts), 16-byte aligned.
  *  kv_cache     device uint8 [num_pages, page_bytes(layout, page_size)], 16-B aligned.
  *  block_table  device int32 [batch, max_pages]: page of each page-sized block.
  *  cache_seqlens device int32 [batch]: L_b, context rows including the query
@@ -328,7 +342,7 @@ int mla_combine_inv_rope(const float* part_out, const float* part_lse, const int
  * KV-row write (device): scatter n new rows into their pages ("MLA" API page of
  * HALOps, mla_attention: its cache-write step and kv_cache parameter).
  *  rows   device bf16 [n, row_elems], already RMSNorm'd (and RoPE'd);
- *         row_elems = 576 (layouts 0 and 2) or 512 (layout 1: 448 NoPE | 64 RoPE).
+ *         row_elems = 576 (layouts 0, 2, 4) or 512 (layouts 1, 3: 448 NoPE | 64 RoPE).
  *  slots  device int32 [n]: page * page_size + offset; negative slots are skipped.
  * Layout 0 copies the bits. fp8 layouts: per 64-element NoPE group,
  * amax = max(max|x|, 1e-10f), e = the smallest integer with 448 * 2^e >= amax,
@@ -336,7 +350,10 @@ int mla_combine_inv_rope(const float* part_out, const float* part_lse, const int
  * x * 2^-e; the RoPE part is copied as bf16. A NaN element takes no part in its
  * group's amax (the maximum is taken over the numbers) and is stored as the
  * E4M3 NaN code 0x7F; an infinite one makes amax infinite (scale byte 254) and
- * is stored as +-448.
+ * is stored as +-448. 4-bit layouts: the same per 32-element group with 6 in the place
+ * of 448 and e2m1 round-to-nearest-even codes; e2m1 has no NaN, so a group that holds one
+ * is written as scale byte 255 with zero codes (all 32 elements read back as NaN), and
+ * an infinite element gives scale byte 254 and is stored as +-6.
  *  status device uint32 or NULL: a row whose slot's page is >= num_pages is not
  *         written and ORs MLA_STATUS_BAD_SLOT into *status.
  */
@@ -349,7 +366,7 @@ int mla_kv_write(const void* rows, const int32_t* slots, int32_t n, void* kv_cac
  * of HALOps, mla_attention: the step that normalises and rotates q and kv before the
  * cache write; its kv_norm_weight, kv_eps, positions and freqs_real parameters).
  *  raw     device bf16 [n, row_elems], the un-normalised rows; row_elems = 576
- *          for layouts 0 and 2 ([kv_c 512 | k_pe 64]) and 512 for layout 1 (the
+ *          for layouts 0, 2, 4 ([kv_c 512 | k_pe 64]) and 512 for layouts 1, 3 (the
  *          DSV4 row: 448 NoPE | 64 RoPE).
  *  slots   device int32 [n] as for mla_kv_write (negative slots are skipped).
  *  positions device int32 [n]: the token position that selects the RoPE row;
@@ -361,8 +378,8 @@ int mla_kv_write(const void* rows, const int32_t* slots, int32_t n, void* kv_cac
  *    y = x * (1 / sqrt(sum(x^2) / 512 + eps)) * w;
  *  - RoPE of the 64 RoPE elements, pair i = (x[2i], x[2i+1]) of that part, with
  *    (c, s) = (freqs[pos, 2i], freqs[pos, 2i+1]): (x0 c - x1 s, x0 s + x1 c).
- *    Layouts 0 and 2 rotate the raw k_pe (elements 512..575, not normalised);
- *    layout 1 rotates elements 448..511 after the normalisation;
+ *    Layouts 0, 2, 4 rotate the raw k_pe (elements 512..575, not normalised);
+ *    layouts 1, 3 rotate elements 448..511 after the normalisation;
  *  - the row is rounded to bf16 (nearest even) and written exactly as
  *    mla_kv_write writes that bf16 row.
  * status (device uint32, or NULL) is OR-ed with MLA_STATUS_BAD_POSITION for a
@@ -373,6 +390,56 @@ int mla_kv_write_norm_rope(const void* raw, const int32_t* slots, const int32_t*
                            float eps, const float* freqs, int32_t max_pos, int32_t n, void* kv_cache,
                            mla_kv_layout layout, int64_t num_pages, int32_t page_size, uint32_t* status,
                            void* stream);
+
+/*
+ * Prepare queries and append KV rows (device): the step before a decode, in one launch ("MLA"
+ * API page of HALOps, mla_attention: "q / kv RMSNorm + RoPE + KV cache write"). For every token t of
+ * num_tokens and head n, the row [q_nope | q_pe] is normalised (if asked), rotated and
+ * written to q_out, contiguous as mla_decode reads it; and the token's raw KV row goes through
+ * the same steps into its page slot, exactly as mla_kv_write_norm_rope writes it.
+ *  q_nope  device bf16, NoPE elements of row (t, n) at q_nope + t * q_nope_token_stride +
+ *          n * q_nope_head_stride (strides in elements): 512 of them for layouts 0, 2, 4 and 448
+ *          for layouts 1, 3. q_pe: the 64 RoPE elements, by strides of its own (for a 512-wide
+ *          query row, q_nope + 448 with the same strides).
+ *  q_norm  nonzero: RMSNorm of the row's first 512 elements (layouts 0, 2, 4: q_nope; layouts
+ *          1, 3: q_nope and q_pe), y = x * (1 / sqrt(sum(x^2) / 512 + q_eps)) * w, with w =
+ *          q_norm_weight, device bf16 [512], or 1 if it is NULL. Zero: rotation only, and
+ *          q_norm_weight must be NULL.
+ *          The RoPE elements are then rotated as mla_kv_write_norm_rope rotates k_pe; arithmetic
+ *          is fp32, rounded once to bf16.
+ *  kv_raw  device bf16 rows [num_tokens, row_elems], kv_row_stride elements apart; kv_norm_weight,
+ *          kv_eps, freqs, max_pos, kv_cache, layout, num_pages, page_size as for
+ *          mla_kv_write_norm_rope.
+ *  slots, positions  device int32 [num_tokens]: a negative slot writes no KV row (the
+ *          query rows are still prepared). Slots that are written must be distinct. A token
+ *          whose position is outside [0, max_pos) writes neither its query rows nor its KV row
+ *          and is reported, unless slot and position are both negative (padding).
+ *  q_out   device bf16 [num_tokens, num_heads, row_elems]. It may be the queries' own memory row for
+ *          row (q_nope == q_out, q_pe == q_out + its offset, strides those of q_out); any other
+ *          overlap with an input is refused.
+ * Strides are multiples of 8 elements >= 0 and every pointer is 16-byte aligned (status, slots
+ * and positions 4-byte). status (device uint32 or NULL) is OR-ed with MLA_STATUS_BAD_SLOT and
+ * MLA_STATUS_BAD_POSITION.
+ */
+int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
+                      int64_t q_pe_token_stride, int64_t q_pe_head_stride, int32_t q_norm, const void* q_norm_weight,
+                      float q_eps, const void* kv_raw, int64_t kv_row_stride, const int32_t* slots,
+                      const int32_t* positions, const void* kv_norm_weight, float kv_eps, const float* freqs,
+                      int32_t max_pos, int32_t num_tokens, int32_t num_heads, void* q_out, void* kv_cache,
+                      mla_kv_layout layout, int64_t num_pages, int32_t page_size, uint32_t* status, void* stream);
+
+/*
+ * Read cached rows back (device): rows[i] = the cached row at slots[i] as bf16 [n, row_elems]
+ * (row_elems as for mla_kv_write), for steps that need the rows unpaged, such as
+ * mla_sparse_prefill over a quantised cache. bf16 rows are copied; fp8 and 4-bit values are
+ * code * 2^(scale - 127), rounded to bf16 (exact inside its range).
+ *  slots  device int32 [n]: page * page_size + offset, in any order, repeats allowed. A
+ *         negative slot leaves its row of `rows` as it was; a slot whose page is >= num_pages
+ *         does too and ORs MLA_STATUS_BAD_SLOT into *status (device uint32 or NULL).
+ *  kv_cache and rows are 16-byte aligned and do not overlap.
+ */
+int mla_kv_read(const void* kv_cache, mla_kv_layout layout, int64_t num_pages, int32_t page_size, const int32_t* slots,
+                int32_t n, void* rows, uint32_t* status, void* stream);
 
 /*
  * Page gather (device, a test export): out[j, :] = decoded K row j of one

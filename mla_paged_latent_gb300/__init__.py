@@ -24,8 +24,10 @@ LIB_PATH = _build.LIB
 MLA_KV_BF16_576 = 0
 MLA_KV_FP8_448_UE8M0 = 1
 MLA_KV_FP8_512_UE8M0 = 2
-DQK = {0: 576, 1: 512, 2: 576}
-ROW_ELEMS = {0: 576, 1: 512, 2: 576}
+MLA_KV_FP4_448_UE8M0 = 3
+MLA_KV_FP4_512_UE8M0 = 4
+DQK = {0: 576, 1: 512, 2: 576, 3: 512, 4: 576}
+ROW_ELEMS = {0: 576, 1: 512, 2: 576, 3: 512, 4: 576}
 DV = 512
 WORKSPACE_HEADER = 256
 
@@ -50,7 +52,8 @@ class _PlanInfo(ctypes.Structure):
 
 EXPORTS = ["mla_page_bytes", "mla_decode_plan", "mla_decode", "mla_decode_runs", "mla_sparse_prefill", "mla_swa_plan",
            "mla_decode_static_workspace", "mla_combine",
-           "mla_combine_v_up", "mla_combine_inv_rope", "mla_kv_write", "mla_kv_write_norm_rope", "mla_kv_gather", "mla_workspace_init", "mla_read_status",
+           "mla_combine_v_up", "mla_combine_inv_rope", "mla_kv_write", "mla_kv_write_norm_rope", "mla_qkv_norm_rope",
+           "mla_kv_read", "mla_kv_gather", "mla_workspace_init", "mla_read_status",
            "mla_last_error"]
 STATIC_WORKSPACE_BYTES = 64 << 20
 
@@ -84,6 +87,9 @@ def load(path: str | None = None):
         lib.mla_combine_inv_rope.argtypes = [V, V, V, I32, I32, I32, V, V, V, I32, I32, V, V, V]
         lib.mla_kv_write.argtypes = [V, V, I32, V, I32, I64, I32, V, V]
         lib.mla_kv_write_norm_rope.argtypes = [V, V, V, V, F32, V, I32, I32, V, I32, I64, I32, V, V]
+        lib.mla_qkv_norm_rope.argtypes = [V, I64, I64, V, I64, I64, I32, V, F32, V, I64, V, V, V, F32, V, I32, I32, I32,
+                                          V, V, I32, I64, I32, V, V]
+        lib.mla_kv_read.argtypes = [V, I32, I64, I32, V, I32, V, V, V]
         lib.mla_kv_gather.argtypes = [V, I32, I64, I32, V, I32, I32, V, V]
         lib.mla_workspace_init.argtypes = [V, V]
         lib.mla_read_status.argtypes = [V, ctypes.POINTER(ctypes.c_uint32), I32, V]
@@ -115,6 +121,25 @@ def _require_cuda(*tensors):
     for t in tensors:
         if t is not None and not t.is_cuda:
             raise ValueError("all tensors passed to the device entry points must live on the GPU")
+
+
+def _require(name: str, t, dtype: str, *shape, contiguous: bool = True):
+    """One tensor's type, shape (None: any size) and layout; raises ValueError."""
+    if str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have the shape {list(shape)}, not {list(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _require_cache(kv_cache, layout: int, page_size: int):
+    _require("kv_cache", kv_cache, "uint8", None, mla_page_bytes(layout, page_size))
+
+
+def _require_status(status):
+    if status is not None and (status.element_size() != 4 or status.numel() < 1):
+        raise ValueError("status must hold a 32-bit word")
 
 
 def mla_page_bytes(layout: int, page_size: int) -> int:
@@ -298,6 +323,53 @@ def mla_kv_write_norm_rope(raw, slots, positions, norm_weight, eps: float, freqs
     _check(load().mla_kv_write_norm_rope(_ptr(raw), _ptr(slots), _ptr(positions), _ptr(norm_weight), float(eps),
                                          _ptr(freqs), freqs.shape[0], slots.shape[0], _ptr(kv_cache), layout,
                                          kv_cache.shape[0], page_size, _ptr(status), _stream(stream)))
+
+
+def mla_qkv_norm_rope(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, kv_eps: float, freqs, q_out, kv_cache,
+                      layout: int, page_size: int, q_norm_weight=None, q_eps: float | None = None, status=None,
+                      stream=None):
+    """Queries normalised (if q_eps is given) and rotated into q_out, and the same tokens' KV rows
+    normalised, rotated and written into their slots, in one launch. q_nope bf16 [T, N, 512] (layouts 0,
+    2, 4) or [T, N, 448] (1, 3) and q_pe bf16 [T, N, 64] by their strides; kv_raw bf16 [T, ROW_ELEMS], rows
+    apart by their stride; slots and positions int32 [T]; kv_norm_weight and q_norm_weight bf16 [512];
+    freqs float32 [max_pos, 64]; q_out bf16 [T, N, ROW_ELEMS] (or the queries' own memory, row for row).
+    status: optional device uint32 [1] receiving MLA_STATUS_BAD_SLOT (4) / MLA_STATUS_BAD_POSITION (8)."""
+    _require_cuda(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, freqs, q_out, kv_cache, q_norm_weight, status)
+    _require_cache(kv_cache, layout, page_size)
+    width = ROW_ELEMS[layout]
+    T, N = q_nope.shape[:2]
+    _require("q_nope", q_nope, "bfloat16", T, N, 448 if width == 512 else 512, contiguous=False)
+    _require("q_pe", q_pe, "bfloat16", T, N, 64, contiguous=False)
+    _require("kv_raw", kv_raw, "bfloat16", T, width, contiguous=False)
+    if T > 0 and any(t.stride(-1) != 1 for t in (q_nope, q_pe, kv_raw)):
+        raise ValueError("q_nope, q_pe and kv_raw must have their last elements adjacent")
+    _require("slots", slots, "int32", T)
+    _require("positions", positions, "int32", T)
+    _require("kv_norm_weight", kv_norm_weight, "bfloat16", 512)
+    _require("freqs", freqs, "float32", None, 64)
+    _require("q_out", q_out, "bfloat16", T, N, width)
+    if q_norm_weight is not None:
+        _require("q_norm_weight", q_norm_weight, "bfloat16", 512)
+    _require_status(status)
+    _check(load().mla_qkv_norm_rope(_ptr(q_nope), q_nope.stride(0), q_nope.stride(1), _ptr(q_pe), q_pe.stride(0),
+                                    q_pe.stride(1), int(q_eps is not None), _ptr(q_norm_weight),
+                                    0.0 if q_eps is None else float(q_eps), _ptr(kv_raw), kv_raw.stride(0), _ptr(slots),
+                                    _ptr(positions), _ptr(kv_norm_weight), float(kv_eps), _ptr(freqs), freqs.shape[0],
+                                    T, N, _ptr(q_out), _ptr(kv_cache), layout, kv_cache.shape[0], page_size,
+                                    _ptr(status), _stream(stream)))
+
+
+def mla_kv_read(kv_cache, layout: int, page_size: int, slots, rows, status=None, stream=None):
+    """Cached rows decoded to bf16: rows [n, ROW_ELEMS] receives the rows at slots int32 [n] (negative:
+    left as it was). status: optional device uint32 [1] receiving MLA_STATUS_BAD_SLOT (4) for a slot past
+    the cache."""
+    _require_cuda(kv_cache, slots, rows, status)
+    _require_cache(kv_cache, layout, page_size)
+    _require("slots", slots, "int32", None)
+    _require("rows", rows, "bfloat16", slots.shape[0], ROW_ELEMS[layout])
+    _require_status(status)
+    _check(load().mla_kv_read(_ptr(kv_cache), layout, kv_cache.shape[0], page_size, _ptr(slots), slots.shape[0],
+                              _ptr(rows), _ptr(status), _stream(stream)))
 
 
 def mla_kv_gather(kv_cache, layout: int, page_size: int, block_table_row, length: int, out, stream=None):

@@ -19,8 +19,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmla_decode_gb300.so")
 
 SOURCES = ["api.cpp", "plan.cpp", "decode_sm103.cu", "decode_pair_sm103.cu", "aux_sm103.cu", "vup_sm103.cu",
-           "noalloc_sm103.cu"]
-HEADERS = ["mla_kernels.h", "ptx_sm103.cuh", "decode_common.cuh", "combine_row.cuh"]
+           "qkv_sm103.cu", "noalloc_sm103.cu"]
+HEADERS = ["mla_kernels.h", "ptx_sm103.cuh", "decode_common.cuh", "combine_row.cuh", "fp4_row.cuh", "kv_row.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

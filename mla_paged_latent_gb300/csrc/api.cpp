@@ -57,6 +57,16 @@ int layout_geometry(int layout, int page_size, int64_t* row_bytes, int64_t* page
       *page_bytes = ((static_cast<int64_t>(page_size) * 648 + 639) / 640) * 640;
       *dqk = 576;
       return 0;
+    case MLA_KV_FP4_448_UE8M0:
+      *row_bytes = 352;
+      *page_bytes = ((static_cast<int64_t>(page_size) * 368 + 351) / 352) * 352;
+      *dqk = 512;
+      return 0;
+    case MLA_KV_FP4_512_UE8M0:
+      *row_bytes = 384;
+      *page_bytes = ((static_cast<int64_t>(page_size) * 400 + 383) / 384) * 384;
+      *dqk = 576;
+      return 0;
     default:
       return -1;
   }
@@ -341,7 +351,9 @@ int decode_impl(const void* q, const void* kv_cache, mla_kv_layout layout, int64
     mla::DecodeVariant v;
     if (layout == MLA_KV_BF16_576) v = tma_kv ? mla::DecodeVariant::kBf16Tma : mla::DecodeVariant::kBf16Gather;
     else if (layout == MLA_KV_FP8_448_UE8M0) v = mla::DecodeVariant::kFp8_448;
-    else v = mla::DecodeVariant::kFp8_512;
+    else if (layout == MLA_KV_FP8_512_UE8M0) v = mla::DecodeVariant::kFp8_512;
+    else if (layout == MLA_KV_FP4_448_UE8M0) v = mla::DecodeVariant::kFp4_448;
+    else v = mla::DecodeVariant::kFp4_512;
     const int grid = p.num_work < num_sms ? p.num_work : num_sms;
     e = mla::launch_decode(v, p, q_map, kv_map, grid, s);
     if (e != cudaSuccess) return cuda_fail(e, "mla_decode: decode launch");
@@ -535,6 +547,113 @@ int mla_kv_write_norm_rope(const void* raw, const int32_t* slots, const int32_t*
       max_pos, n, static_cast<uint8_t*>(kv_cache), static_cast<int>(layout), num_pages, page_size, pb, status,
       static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "mla_kv_write_norm_rope: launch");
+  return MLA_OK;
+}
+
+// Byte range [lo, hi) that rows by strides (elements of 2 bytes) cover.
+struct ByteRange {
+  uintptr_t lo, hi;
+};
+static ByteRange strided_range(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t elems) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + 2 * static_cast<uintptr_t>((n0 - 1) * s0 + (n1 - 1) * s1 + elems)};
+}
+static bool overlap(const ByteRange& a, const ByteRange& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
+                      int64_t q_pe_token_stride, int64_t q_pe_head_stride, int32_t q_norm, const void* q_norm_weight,
+                      float q_eps, const void* kv_raw, int64_t kv_row_stride, const int32_t* slots,
+                      const int32_t* positions, const void* kv_norm_weight, float kv_eps, const float* freqs,
+                      int32_t max_pos, int32_t num_tokens, int32_t num_heads, void* q_out, void* kv_cache,
+                      mla_kv_layout layout, int64_t num_pages, int32_t page_size, uint32_t* status, void* stream) {
+  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: num_tokens < 0");
+  if (num_tokens == 0) return MLA_OK;
+  if (!q_nope || !q_pe || !kv_raw || !slots || !positions || !kv_norm_weight || !freqs || !q_out || !kv_cache)
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: NULL pointer");
+  int64_t rb, pb;
+  int dqk;
+  if (layout_geometry(layout, page_size, &rb, &pb, &dqk) != 0)
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: unknown layout %d", static_cast<int>(layout));
+  if (!pow2(page_size))
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: page_size %d not a power of two", page_size);
+  if (num_heads < 1 || num_pages < 1 || max_pos < 1)
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: num_heads, num_pages and max_pos must be >= 1");
+  if (static_cast<int64_t>(num_tokens) * num_heads >= (1ll << 31))
+    return fail(MLA_ERR_UNSUPPORTED, "mla_qkv_norm_rope: too many query rows");
+  if (!(kv_eps >= 0.f) || !(kv_eps < 1e30f) || (q_norm && (!(q_eps >= 0.f) || !(q_eps < 1e30f))))
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: eps must be a finite number >= 0");
+  if (!q_norm && q_norm_weight != nullptr)
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: q_norm_weight given without q_norm");
+  const int64_t strides[5] = {q_nope_token_stride, q_nope_head_stride, q_pe_token_stride, q_pe_head_stride,
+                              kv_row_stride};
+  for (int64_t s : strides)
+    if (s < 0 || s % 8 != 0 || s >= (1ll << 40))
+      return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: stride %lld must be a multiple of 8 elements >= 0",
+                  static_cast<long long>(s));
+  if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(q_norm_weight) || !aligned16(kv_raw) ||
+      !aligned16(kv_norm_weight) || !aligned16(freqs) || !aligned16(q_out) || !aligned16(kv_cache))
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: pointers must be 16-byte aligned");
+  // q_out may be the queries' own memory, row for row; any other overlap would race
+  const int nope = dqk == 512 ? 448 : 512;
+  const int64_t T = num_tokens, N = num_heads;
+  const ByteRange out = strided_range(q_out, T, N * dqk, N, dqk, dqk);
+  const uint16_t* qo = static_cast<const uint16_t*>(q_out);
+  const bool nope_here = q_nope == qo && q_nope_token_stride == N * dqk && q_nope_head_stride == dqk;
+  const bool pe_here = q_pe == qo + nope && q_pe_token_stride == N * dqk && q_pe_head_stride == dqk;
+  if ((!nope_here && overlap(out, strided_range(q_nope, T, q_nope_token_stride, N, q_nope_head_stride, nope))) ||
+      (!pe_here && overlap(out, strided_range(q_pe, T, q_pe_token_stride, N, q_pe_head_stride, 64))) ||
+      overlap(out, strided_range(kv_raw, T, kv_row_stride, 1, 0, dqk)))
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: q_out overlaps an input other than row for row");
+  mla::QkvParams p;
+  std::memset(&p, 0, sizeof p);
+  p.q_nope = static_cast<const uint16_t*>(q_nope);
+  p.q_pe = static_cast<const uint16_t*>(q_pe);
+  p.nope_token_stride = q_nope_token_stride;
+  p.nope_head_stride = q_nope_head_stride;
+  p.pe_token_stride = q_pe_token_stride;
+  p.pe_head_stride = q_pe_head_stride;
+  p.q_weight = static_cast<const uint16_t*>(q_norm_weight);
+  p.kv_raw = static_cast<const uint16_t*>(kv_raw);
+  p.kv_row_stride = kv_row_stride;
+  p.slots = slots;
+  p.positions = positions;
+  p.kv_weight = static_cast<const uint16_t*>(kv_norm_weight);
+  p.freqs = freqs;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.kv = static_cast<uint8_t*>(kv_cache);
+  p.status = status;
+  p.num_pages = num_pages;
+  p.page_bytes = pb;
+  p.q_eps = q_eps;
+  p.kv_eps = kv_eps;
+  p.q_norm = q_norm ? 1 : 0;
+  p.max_pos = max_pos;
+  p.tokens = num_tokens;
+  p.heads = num_heads;
+  p.layout = static_cast<int>(layout);
+  p.page_size = page_size;
+  cudaError_t e = mla::launch_qkv_norm_rope(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mla_qkv_norm_rope: launch");
+  return MLA_OK;
+}
+
+int mla_kv_read(const void* kv_cache, mla_kv_layout layout, int64_t num_pages, int32_t page_size, const int32_t* slots,
+                int32_t n, void* rows, uint32_t* status, void* stream) {
+  if (n < 0) return fail(MLA_ERR_INVALID_ARG, "mla_kv_read: n < 0");
+  if (n == 0) return MLA_OK;
+  if (!kv_cache || !slots || !rows) return fail(MLA_ERR_INVALID_ARG, "mla_kv_read: NULL pointer");
+  int64_t rb, pb;
+  int dqk;
+  if (layout_geometry(layout, page_size, &rb, &pb, &dqk) != 0)
+    return fail(MLA_ERR_INVALID_ARG, "mla_kv_read: unknown layout %d", static_cast<int>(layout));
+  if (!pow2(page_size)) return fail(MLA_ERR_INVALID_ARG, "mla_kv_read: page_size %d not a power of two", page_size);
+  if (num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "mla_kv_read: num_pages < 1");
+  if (!aligned16(rows) || !aligned16(kv_cache))
+    return fail(MLA_ERR_INVALID_ARG, "mla_kv_read: rows and kv_cache must be 16-byte aligned");
+  cudaError_t e = mla::launch_kv_read(static_cast<const uint8_t*>(kv_cache), static_cast<int>(layout), num_pages,
+                                      page_size, pb, slots, n, static_cast<uint16_t*>(rows), status,
+                                      static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mla_kv_read: launch");
   return MLA_OK;
 }
 

@@ -3,16 +3,12 @@
 #include <cuda_runtime.h>
 
 #include "combine_row.cuh"
+#include "kv_row.cuh"
 #include "mla_kernels.h"
 #include "ptx_sm103.cuh"
 
 namespace mla {
 namespace {
-
-__device__ __forceinline__ uint16_t f32_to_bf16(float x) {
-  return static_cast<uint16_t>(f32x2_to_bf16x2(x, 0.f) & 0xFFFFu);
-}
-__device__ __forceinline__ float bf16_to_f32(uint32_t h) { return __uint_as_float(h << 16); }
 
 // ----------------------------------------------------------------------------- combine
 // One warp per query row of a request that the plan split into >= 2 pieces (the merge
@@ -158,103 +154,6 @@ __global__ void __launch_bounds__(128) swa_plan_kernel(const int32_t* __restrict
 }
 
 // ----------------------------------------------------------------------------- kv write
-// 448 * 2^e as fp32 (exact; +inf once it exceeds the fp32 range).
-__device__ __forceinline__ float pow2x448(int e) {
-  const int E = e + 8 + 127;  // 448 = 1.75 * 2^8
-  if (E >= 255) return __uint_as_float(0x7F800000u);
-  if (E <= 0) return 0.f;
-  return __uint_as_float((static_cast<uint32_t>(E) << 23) | 0x600000u);
-}
-// Smallest e with 448 * 2^e >= a (a >= 1e-10), clamped to [-127, 127]; decided by
-// exact comparisons of powers of two.
-__device__ __forceinline__ int group_exponent(float a) {
-  if (!(a <= 3.4028235e38f)) return 127;
-  int e = static_cast<int>((__float_as_uint(a) >> 23) & 0xFFu) - 127 - 8;
-  while (e < 127 && !(pow2x448(e) >= a)) ++e;
-  while (e > -127 && pow2x448(e - 1) >= a) --e;
-  return e;
-}
-// 2^-e as fp32 (exact for e in [-127, 126]).
-__device__ __forceinline__ float pow2neg(int e) {
-  const int E = 127 - e;
-  if (E >= 255) return __uint_as_float(0x7F800000u);
-  if (E <= 0) return __uint_as_float(0x00400000u >> (-E));
-  return __uint_as_float(static_cast<uint32_t>(E) << 23);
-}
-
-// Write one bf16 row (generic pointer x, 16-byte aligned, row_elems values) into its
-// page slot; all 32 lanes of the warp take part ("MLA" API page of HALOps,
-// mla_attention: KV cache write of the RMSNorm'd row; kv_cache parameter for the layout).
-__device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* __restrict__ kv, int layout,
-                                          int64_t page, int off, int page_size, int64_t page_bytes) {
-  if (layout == 0) {
-    const uint4* src = reinterpret_cast<const uint4*>(x);
-    uint4* dst = reinterpret_cast<uint4*>(kv + page * page_bytes + (int64_t)off * 1152);
-    for (int c = lane; c < 72; c += 32) dst[c] = src[c];
-    return;
-  }
-  const int nope = layout == 1 ? 448 : 512;
-  const int row_bytes = layout == 1 ? 576 : 640;
-  uint8_t* dst = kv + page * page_bytes + (int64_t)off * row_bytes;
-  // lane l holds elements [16 l, 16 l + 16), loaded at once; NoPE group g is lanes 4g .. 4g+3
-  // (in the 512-wide DSV4 row, lanes 28-31 hold the RoPE part)
-  float v[16];
-  {
-    const uint4 a = reinterpret_cast<const uint4*>(x)[2 * lane];
-    const uint4 b = reinterpret_cast<const uint4*>(x)[2 * lane + 1];
-    const uint32_t h[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[2 * k] = bf16_to_f32(h[k] & 0xFFFFu);
-      v[2 * k + 1] = bf16_to_f32(h[k] >> 16);
-    }
-  }
-  const bool in_nope = lane * 16 < nope;
-  float a = 0.f;  // fmaxf returns the number when one operand is NaN: NaN elements do not count
-#pragma unroll
-  for (int k = 0; k < 16; ++k) a = fmaxf(a, fabsf(v[k]));
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  a = fmaxf(a, 1e-10f);
-  const int e = group_exponent(a);
-  if (in_nope) {
-    const float sc = pow2neg(e);
-    uint32_t w4[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint16_t c0, c1;
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c0) : "f"(v[4 * k + 1] * sc), "f"(v[4 * k] * sc));
-      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c1) : "f"(v[4 * k + 3] * sc), "f"(v[4 * k + 2] * sc));
-      w4[k] = static_cast<uint32_t>(c0) | (static_cast<uint32_t>(c1) << 16);
-      // a NaN element (left out of the amax above) is stored as the NaN code 0x7F, whatever its sign
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-        if (v[4 * k + b] != v[4 * k + b]) w4[k] = (w4[k] & ~(0xFFu << (8 * b))) | (0x7Fu << (8 * b));
-    }
-    reinterpret_cast<uint4*>(dst)[lane] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-  } else {
-    // DSV4 row: its 64 RoPE elements stay bf16, after the 448 code bytes
-    const uint4* src = reinterpret_cast<const uint4*>(x) + 2 * lane;
-    uint4* d2 = reinterpret_cast<uint4*>(dst + nope + (lane * 16 - nope) * 2);
-    d2[0] = src[0];
-    d2[1] = src[1];
-  }
-  // scale bytes: group g's exponent sits in lane 4g; lane 0 assembles the 8-byte slot
-  uint32_t sbytes[2] = {0u, 0u};
-#pragma unroll
-  for (int g = 0; g < 8; ++g) {
-    const int eg = __shfl_sync(0xffffffffu, e, 4 * g);
-    if (g < nope / 64) sbytes[g >> 2] |= static_cast<uint32_t>(eg + 127) << (8 * (g & 3));
-  }
-  // the 576-wide row's RoPE part: 64 bf16 copied
-  if (layout != 1 && lane < 8)
-    reinterpret_cast<uint4*>(dst + nope)[lane] = reinterpret_cast<const uint4*>(x + nope)[lane];
-  if (lane == 0) {
-    uint2* sp = reinterpret_cast<uint2*>(kv + page * page_bytes + (int64_t)page_size * row_bytes + off * 8);
-    *sp = make_uint2(sbytes[0], sbytes[1]);
-  }
-}
-
 // One warp per new row, already normalised.
 __global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* __restrict__ rows,
                                                        const int32_t* __restrict__ slots, int n,
@@ -272,7 +171,7 @@ __global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* __restric
     if (lane == 0 && status != nullptr) atomicOr(status, 4u);
     return;
   }
-  const int row_elems = layout == 1 ? 512 : 576;
+  const int row_elems = row_width(layout);
   write_row(rows + (int64_t)r * row_elems, lane, kv, layout, page, static_cast<int>(slot % page_size), page_size,
             page_bytes);
 }
@@ -280,8 +179,7 @@ __global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* __restric
 // One warp per raw row: RMSNorm of the 512 latent elements and RoPE of the 64 RoPE
 // elements in fp32 ("MLA" API page of HALOps, mla_attention: its normalise-and-rotate
 // step before the cache write, kv_norm_weight / kv_eps / positions / freqs_real), the row
-// rounded to bf16 in shared memory, then written as write_row writes it. Lane l
-// holds latent elements [16 l, 16 l + 16) and RoPE pair l of the 576-wide layouts.
+// rounded to bf16 in shared memory (norm_rope_row), then written as write_row writes it.
 __global__ void __launch_bounds__(128) kv_write_norm_rope_kernel(
     const uint16_t* __restrict__ raw, const int32_t* __restrict__ slots, const int32_t* __restrict__ positions,
     const uint16_t* __restrict__ w, float eps, const float* __restrict__ freqs, int max_pos, int n,
@@ -302,60 +200,10 @@ __global__ void __launch_bounds__(128) kv_write_norm_rope_kernel(
     if (lane == 0 && status != nullptr) atomicOr(status, bad);
     return;
   }
-  const int row_elems = layout == 1 ? 512 : 576;
+  const int row_elems = row_width(layout);
   const uint16_t* x = raw + (int64_t)r * row_elems;
   const float* f = freqs + (int64_t)pos * 64;
-  float v[16];
-  {
-    const uint4 a = reinterpret_cast<const uint4*>(x)[2 * lane];
-    const uint4 b = reinterpret_cast<const uint4*>(x)[2 * lane + 1];
-    const uint32_t h[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[2 * k] = bf16_to_f32(h[k] & 0xFFFFu);
-      v[2 * k + 1] = bf16_to_f32(h[k] >> 16);
-    }
-  }
-  float ss = 0.f;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) ss = fmaf(v[k], v[k], ss);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float rinv = 1.0f / sqrtf(ss * (1.0f / 512.0f) + eps);
-  {
-    const uint4 a = reinterpret_cast<const uint4*>(w)[2 * lane];
-    const uint4 b = reinterpret_cast<const uint4*>(w)[2 * lane + 1];
-    const uint32_t h[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[2 * k] = v[2 * k] * rinv * bf16_to_f32(h[k] & 0xFFFFu);
-      v[2 * k + 1] = v[2 * k + 1] * rinv * bf16_to_f32(h[k] >> 16);
-    }
-  }
-  if (layout == 1 && lane >= 28) {
-    // DSV4 row: elements 448..511 (lanes 28-31) are the RoPE part, rotated after the norm
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int i = 8 * (lane - 28) + k;
-      const float c = f[2 * i], s = f[2 * i + 1];
-      const float x0 = v[2 * k], x1 = v[2 * k + 1];
-      v[2 * k] = x0 * c - x1 * s;
-      v[2 * k + 1] = x0 * s + x1 * c;
-    }
-  }
-  uint32_t o[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) o[k] = f32x2_to_bf16x2(v[2 * k], v[2 * k + 1]);
-  reinterpret_cast<uint4*>(srow[wi])[2 * lane] = make_uint4(o[0], o[1], o[2], o[3]);
-  reinterpret_cast<uint4*>(srow[wi])[2 * lane + 1] = make_uint4(o[4], o[5], o[6], o[7]);
-  if (layout != 1) {
-    // k_pe (elements 512..575) is rotated as it comes, without the norm
-    const uint32_t two = reinterpret_cast<const uint32_t*>(x + 512)[lane];
-    const float x0 = bf16_to_f32(two & 0xFFFFu), x1 = bf16_to_f32(two >> 16);
-    const float c = f[2 * lane], s = f[2 * lane + 1];
-    reinterpret_cast<uint32_t*>(srow[wi] + 512)[lane] = f32x2_to_bf16x2(x0 * c - x1 * s, x0 * s + x1 * c);
-  }
-  __syncwarp();
+  norm_rope_row(x, w, eps, f, row_elems, lane, srow[wi]);
   write_row(srow[wi], lane, kv, layout, page, static_cast<int>(slot % page_size), page_size, page_bytes);
 }
 
@@ -369,7 +217,7 @@ __global__ void __launch_bounds__(128) kv_gather_kernel(const uint8_t* __restric
   const int j = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (j >= length) return;
-  const int dqk = layout == 1 ? 512 : 576;
+  const int dqk = row_width(layout);
   float* o = out + (int64_t)j * dqk;
   const int pi = j / page_size;
   const int64_t page = pi < max_pages ? bt_row[pi] : -1;
@@ -383,10 +231,24 @@ __global__ void __launch_bounds__(128) kv_gather_kernel(const uint8_t* __restric
     for (int d = lane; d < 576; d += 32) o[d] = bf16_to_f32(src[d]);
     return;
   }
-  const int nope = layout == 1 ? 448 : 512;
-  const int row_bytes = layout == 1 ? 576 : 640;
+  const int nope = row_nope(layout);
+  const int row_bytes = row_stored_bytes(layout);
   const uint8_t* src = kv + page * page_bytes + (int64_t)off * row_bytes;
-  const uint8_t* sc = kv + page * page_bytes + (int64_t)page_size * row_bytes + off * 8;
+  const uint8_t* sc = kv + page * page_bytes + (int64_t)page_size * row_bytes + off * row_scale_slot(layout);
+  if (layout >= 3) {
+    for (int i = lane; i < nope / 8; i += 32) {
+      uint32_t o4[4];
+      fp4x8_to_bf16(reinterpret_cast<const uint32_t*>(src)[i], ue8m0_to_bf16x2(sc[i >> 2]), o4);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        o[8 * i + 2 * k] = bf16_to_f32(o4[k] & 0xFFFFu);
+        o[8 * i + 2 * k + 1] = bf16_to_f32(o4[k] >> 16);
+      }
+    }
+    const uint16_t* pe = reinterpret_cast<const uint16_t*>(src + nope / 2);
+    for (int d = lane; d < 64; d += 32) o[nope + d] = bf16_to_f32(pe[d]);
+    return;
+  }
   for (int d = 2 * lane; d < nope; d += 64) {
     const uint32_t two = *reinterpret_cast<const uint16_t*>(src + d);
     const float2 v = e4m3x2_to_f32x2(two);

@@ -33,6 +33,7 @@
 #include <cuda_runtime.h>
 
 #include "decode_common.cuh"
+#include "kv_row.cuh"
 #include "mla_kernels.h"
 #include "ptx_sm103.cuh"
 
@@ -84,8 +85,10 @@ struct Misc {
 
 template <int LAYOUT, bool TMA_KV>
 struct Cfg {
-  static constexpr int kNslab = (LAYOUT == 1) ? 8 : 9;
-  static constexpr int kNope = (LAYOUT == 1) ? 448 : 512;
+  static constexpr int kNslab = row_width(LAYOUT) / 64;
+  static constexpr int kNope = row_nope(LAYOUT);
+  static constexpr bool kFp4 = LAYOUT >= 3;
+  static constexpr int kScaleSlot = row_scale_slot(LAYOUT);
   static constexpr uint32_t kQBytes = kNslab * kSlab;
   static constexpr uint32_t kStageBytes = kNslab * kSlab;
   static constexpr uint32_t kOffStage = kQBytes;
@@ -97,15 +100,17 @@ struct Cfg {
   // pair P = P_hi + P_lo (P_lo = bf16(P - P_hi)) in extra 8 KB buffers: one per stage
   // where shared memory allows (8-slab rows), else one shared by both stages, whose
   // writer then waits for the previous tile's PV to finish.
-  static constexpr bool kPSplit = (LAYOUT != 0);
+  // 4-bit rows keep one bf16 P: its rounding (2^-9 of each term) is far inside their own (2^-3).
+  static constexpr bool kPSplit = LAYOUT == 1 || LAYOUT == 2;
   static constexpr uint32_t kOffPLo = kOffP + (kPInStage ? 0 : 2 * kSlab);
   static constexpr int kPLoBufs =
       !kPSplit ? 0 : (kOffPLo + 2 * kSlab + sizeof(Misc) + 1024 <= 232448 ? 2 : 1);
   static constexpr uint32_t kOffMisc = kOffPLo + kPLoBufs * kSlab;
   static constexpr uint32_t kSmem = kOffMisc + sizeof(Misc) + 1024;
   static_assert(kSmem <= 232448, "shared memory budget of one CTA");
-  static constexpr int kChunks = (LAYOUT == 0) ? 72 : (kNope / 16 + 8);  // 16-B chunks per stored row
-  static constexpr int kChunksPerThread = kChunks / 4;
+  static constexpr int kChunks = row_stored_bytes(LAYOUT) / 16;  // 16-B chunks per stored row
+  static constexpr int kChunksPerThread = (kChunks + 3) / 4;
+  static constexpr int kCodeChunks = kFp4 ? kNope / 32 : kNope / 16;
   __device__ static uint32_t stage(uint32_t base, int st) { return base + kOffStage + st * kStageBytes; }
   __device__ static uint32_t parea(uint32_t base, int st) {
     return kPInStage ? stage(base, st) + 8 * kSlab : base + kOffP + st * kSlab;
@@ -125,8 +130,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // and 5: DSV4-shaped decode 3 % faster, DSV3-shaped 0.5 %, verify 1.3 %). The sparse
   // variants keep the PV issuer on warp 1: their prefetch warp does per-row work and they
   // were 3 % slower.
-  constexpr int kPvWarp = (LAYOUT == 1 || TMA_KV) ? 3 : 1;
-  constexpr int kPrefetchWarp = (LAYOUT == 1 || TMA_KV) ? 1 : 3;
+  constexpr int kPvWarp = (LAYOUT == 1 || LAYOUT == 3 || TMA_KV) ? 3 : 1;
+  constexpr int kPrefetchWarp = (LAYOUT == 1 || LAYOUT == 3 || TMA_KV) ? 1 : 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_addr(smem);
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     // Streams the Q rows and KV rows of upcoming tiles from HBM into L2 so that
     // the stage fills (TMA or converters) find them there. It runs ahead of the
     // fills by about kPrefetchBytes and never blocks them: a prefetch is a hint.
-    const int64_t tile_bytes = static_cast<int64_t>(kBlockRows) * (P.row_bytes + (LAYOUT != 0 ? 8 : 0));
+    const int64_t tile_bytes = static_cast<int64_t>(kBlockRows) * (P.row_bytes + C::kScaleSlot);
     int ahead = static_cast<int>(kPrefetchBytes / tile_bytes);
     ahead = ahead < 2 ? 2 : ahead;
     const int box_rows = P.page_size < kBlockRows ? P.page_size : kBlockRows;
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
               prefetch_l2_bulk(pg + static_cast<int64_t>(off) * P.row_bytes, P.row_bytes);
               if (LAYOUT != 0) {
                 const uintptr_t sa = reinterpret_cast<uintptr_t>(pg + static_cast<int64_t>(P.page_size) * P.row_bytes +
-                                                                 off * 8);
+                                                                 off * C::kScaleSlot);
                 prefetch_l2_bulk(reinterpret_cast<const void*>(sa & ~uintptr_t(15)), 16);
               }
             }
@@ -439,8 +444,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
                 prefetch_l2_bulk(pg + static_cast<int64_t>(off) * P.row_bytes,
                                  static_cast<uint32_t>(((rows * P.row_bytes) + 15) & ~15));
                 if (LAYOUT != 0)
-                  prefetch_l2_bulk(pg + static_cast<int64_t>(P.page_size) * P.row_bytes + off * 8,
-                                   static_cast<uint32_t>((rows * 8 + 15) & ~15));
+                  prefetch_l2_bulk(pg + static_cast<int64_t>(P.page_size) * P.row_bytes + off * C::kScaleSlot,
+                                   static_cast<uint32_t>((rows * C::kScaleSlot + 15) & ~15));
               }
             }
           }
@@ -519,7 +524,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             if (!sparse) {
               int nv = lim - j * kBlockRows;
               nv = nv < 0 ? 0 : (nv > 64 ? 64 : nv);
-              vmask = nv == 64 ? ~0ull : ((1ull << nv) - 1ull);
+              const uint64_t reach = nv == 64 ? ~0ull : ((1ull << nv) - 1ull);
+              vmask = C::kFp4 ? vmask & reach : reach;  // (4-bit: a row of a bad page is left out)
             }
             if (!valid_row || dead) vmask = 0;
             const uint32_t hmask = static_cast<uint32_t>(vmask >> (32 * half));
@@ -625,7 +631,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
         l_run += __shfl_xor_sync(0xffffffffu, l_run, 16);  // the row's sum over both halves
         if (half == 0) {
           float inv = 0.f, lse2 = -INFINITY;
-          if (l_run > 0.f) {
+          // (4-bit rows: a NaN sum, from a NaN group, is passed on instead of counting as empty)
+          if (C::kFp4 ? !(l_run <= 0.f) : l_run > 0.f) {
             float denom = l_run;
             if (nsplit == 1 && P.sink != nullptr) {
               const int n = grow % P.heads;
@@ -758,7 +765,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             const uint8_t* pgn = P.kv + (int64_t)page_a * P.page_bytes;
             const uint8_t* rn = pgn + (int64_t)offn * P.row_bytes;
             for (int l = part4; l * 128 < P.row_bytes; l += 4) prefetch_l2_line(rn + l * 128);
-            if (part4 == 3) prefetch_l2_line(pgn + (int64_t)P.page_size * P.row_bytes + offn * 8);
+            if (part4 == 3) prefetch_l2_line(pgn + (int64_t)P.page_size * P.row_bytes + offn * C::kScaleSlot);
           }
           bool valid = page >= 0;
           if (page == -2 && part4 == 0) atomicOr(P.status, 2u);
@@ -767,7 +774,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
           if (valid) {
             const int off = pos & (P.page_size - 1);
             rowp = P.kv + (int64_t)page * P.page_bytes + (int64_t)off * P.row_bytes;
-            scp = P.kv + (int64_t)page * P.page_bytes + (int64_t)P.page_size * P.row_bytes + off * 8;
+            scp = P.kv + (int64_t)page * P.page_bytes + (int64_t)P.page_size * P.row_bytes + off * C::kScaleSlot;
           }
           const unsigned bal = __ballot_sync(0xffffffffu, valid && part4 == 0);
           // issue this tile's global loads first, then wait for the stage to be free
@@ -776,10 +783,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
           for (int i = 0; i < CPT; ++i) {
             const int c = part4 + 4 * i;
-            v[i] = valid ? ld_nc_v4(rowp + c * 16) : make_uint4(0, 0, 0, 0);
+            v[i] = valid && c < C::kChunks ? ld_nc_v4(rowp + c * 16) : make_uint4(0, 0, 0, 0);
           }
           uint2 sc = make_uint2(0, 0);
-          if (LAYOUT != 0 && valid) sc = ld_nc_v2(scp);
+          uint4 sc4 = make_uint4(0, 0, 0, 0);
+          if (C::kFp4) {
+            if (valid) sc4 = ld_nc_v4(scp);
+          } else if (LAYOUT != 0 && valid) {
+            sc = ld_nc_v2(scp);
+          }
           // dequantise in registers before waiting for the stage, so that only the stores
           // remain once the PV two tiles back has released it: an fp8 chunk (16 e4m3 codes of
           // group c/4) becomes 16 bf16 in lo/hi; a bf16 (RoPE) chunk stays in lo
@@ -789,7 +801,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             const int c = part4 + 4 * i;
             lo[i] = v[i];
             hi[i] = make_uint4(0, 0, 0, 0);
-            if (LAYOUT != 0 && c < C::kNope / 16) {
+            if (!C::kFp4 && LAYOUT != 0 && c < C::kNope / 16) {
               const int grp = c >> 2;
               const uint32_t sbyte = (grp < 4 ? (sc.x >> (8 * grp)) : (sc.y >> (8 * (grp - 4)))) & 0xFFu;
               const float scale = valid ? ue8m0_to_f32(sbyte) : 0.f;
@@ -818,7 +830,24 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
           for (int i = 0; i < CPT; ++i) {
             const int c = part4 + 4 * i;
-            if (LAYOUT == 0) {
+            if (C::kFp4) {
+              if (c < C::kCodeChunks) {
+                // 32 codes of group c: dims [32c, 32c + 32) of slab c / 2
+                const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                const uint32_t sw[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
+                const uint32_t s2 = ue8m0_to_bf16x2((sw[i & 3] >> (8 * part4)) & 0xFFu);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t o[4];
+                  fp4x8_to_bf16(w4[q], s2, o);
+                  st_shared_v4(dst + (c >> 1) * kSlab + sw128_offset(crow, (c & 1) * 32 + 8 * q),
+                               make_uint4(o[0], o[1], o[2], o[3]));
+                }
+              } else if (c < C::kChunks) {
+                const int dim = C::kNope + 8 * (c - C::kCodeChunks);
+                st_shared_v4(dst + (dim >> 6) * kSlab + sw128_offset(crow, dim & 63), v[i]);
+              }
+            } else if (LAYOUT == 0) {
               // bf16 copy: chunk c = dims [8c, 8c + 8)
               st_shared_v4(dst + (c >> 3) * kSlab + sw128_offset(crow, (c & 7) * 8), lo[i]);
             } else if (c < C::kNope / 16) {
@@ -855,6 +884,8 @@ size_t decode_smem_bytes(DecodeVariant v) {
     case DecodeVariant::kBf16Gather: return Cfg<0, false>::kSmem;
     case DecodeVariant::kFp8_448: return Cfg<1, false>::kSmem;
     case DecodeVariant::kFp8_512: return Cfg<2, false>::kSmem;
+    case DecodeVariant::kFp4_448: return Cfg<3, false>::kSmem;
+    case DecodeVariant::kFp4_512: return Cfg<4, false>::kSmem;
   }
   return 0;
 }
@@ -876,6 +907,8 @@ cudaError_t launch_decode(DecodeVariant v, const DecodeParams& p, const CUtensor
     case DecodeVariant::kBf16Gather: return launch_variant<0, false>(p, q_map, kv_map, grid, stream);
     case DecodeVariant::kFp8_448: return launch_variant<1, false>(p, q_map, kv_map, grid, stream);
     case DecodeVariant::kFp8_512: return launch_variant<2, false>(p, q_map, kv_map, grid, stream);
+    case DecodeVariant::kFp4_448: return launch_variant<3, false>(p, q_map, kv_map, grid, stream);
+    case DecodeVariant::kFp4_512: return launch_variant<4, false>(p, q_map, kv_map, grid, stream);
   }
   return cudaErrorInvalidValue;
 }

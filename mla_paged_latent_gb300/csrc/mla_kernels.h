@@ -63,8 +63,9 @@ struct WideMaps {
 };
 
 // Kernel variants: layout 0 with TMA page loads (dense), layout 0 gathered by
-// the converter warps (sparse), layouts 1 and 2 (fp8, dense or sparse).
-enum class DecodeVariant { kBf16Tma = 0, kBf16Gather = 1, kFp8_448 = 2, kFp8_512 = 3 };
+// the converter warps (sparse), layouts 1 and 2 (fp8, dense or sparse), layouts 3 and 4 (4-bit,
+// dense or sparse).
+enum class DecodeVariant { kBf16Tma = 0, kBf16Gather = 1, kFp8_448 = 2, kFp8_512 = 3, kFp4_448 = 4, kFp4_512 = 5 };
 
 size_t decode_smem_bytes(DecodeVariant v);
 
@@ -89,6 +90,32 @@ cudaError_t launch_kv_write_norm_rope(const uint16_t* raw, const int32_t* slots,
                                      const uint16_t* norm_weight, float eps, const float* freqs, int max_pos, int n,
                                      uint8_t* kv, int layout, int64_t num_pages, int page_size, int64_t page_bytes,
                                      uint32_t* status, cudaStream_t stream);
+
+// Queries prepared and KV rows appended in one launch (mla_qkv_norm_rope).
+struct QkvParams {
+  const uint16_t* q_nope;         // bf16 [T, heads, 448 or 512] by strides (elements)
+  const uint16_t* q_pe;           // bf16 [T, heads, 64] by strides
+  int64_t nope_token_stride, nope_head_stride, pe_token_stride, pe_head_stride;
+  const uint16_t* q_weight;       // bf16 [512] or null (gain 1)
+  const uint16_t* kv_raw;         // bf16 [T, width], kv_row_stride elements apart
+  int64_t kv_row_stride;
+  const int32_t* slots;           // [T]
+  const int32_t* positions;       // [T]
+  const uint16_t* kv_weight;      // bf16 [512]
+  const float* freqs;             // [max_pos, 64]
+  uint16_t* q_out;                // bf16 [T, heads, width]
+  uint8_t* kv;
+  uint32_t* status;               // or null
+  int64_t num_pages, page_bytes;
+  float q_eps, kv_eps;
+  int32_t q_norm;                 // normalise the queries
+  int32_t max_pos, tokens, heads, layout, page_size;
+  int32_t kv_blocks;              // blocks that take KV rows (set at launch)
+};
+cudaError_t launch_qkv_norm_rope(const QkvParams& p, cudaStream_t stream);
+
+cudaError_t launch_kv_read(const uint8_t* kv, int layout, int64_t num_pages, int page_size, int64_t page_bytes,
+                           const int32_t* slots, int n, uint16_t* out, uint32_t* status, cudaStream_t stream);
 
 cudaError_t launch_swa_plan(const int32_t* kv_indices, const int32_t* topk_lengths, int num_tokens, int topk,
                             int page_size, int kv_run_step, int32_t* runs, cudaStream_t stream);

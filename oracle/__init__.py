@@ -33,6 +33,8 @@ _lib = None
 LAYOUT_BF16 = 0
 LAYOUT_FP8_448 = 1
 LAYOUT_FP8_512 = 2
+LAYOUT_FP4_448 = 3
+LAYOUT_FP4_512 = 4
 
 
 def build(force: bool = False) -> str:
@@ -67,6 +69,14 @@ def _load():
         lib.mo_e4m3_encode.restype = ctypes.c_uint8
         lib.mo_ue8m0_decode.argtypes = [ctypes.c_uint8]
         lib.mo_ue8m0_decode.restype = f64
+        lib.mo_e2m1_decode.argtypes = [ctypes.c_uint8]
+        lib.mo_e2m1_decode.restype = f64
+        lib.mo_e2m1_encode.argtypes = [f64]
+        lib.mo_e2m1_encode.restype = ctypes.c_uint8
+        lib.mo_group_exponent_fp4.argtypes = [f64]
+        lib.mo_group_exponent_fp4.restype = i32
+        lib.mo_q_norm_rope.argtypes = [P, P, i32, P, f64, P, i32, i32, i32, P]
+        lib.mo_q_norm_rope.restype = None
         lib.mo_group_exponent.argtypes = [f64]
         lib.mo_group_exponent.restype = i32
         lib.mo_layout_info.argtypes = [i32, i32, P, P, P, P, P]
@@ -131,6 +141,22 @@ def ue8m0_decode(codes) -> np.ndarray:
     lib = _load()
     c = np.asarray(codes, dtype=np.uint8)
     return np.array([lib.mo_ue8m0_decode(int(x)) for x in c.ravel()], dtype=np.float64).reshape(c.shape)
+
+
+def e2m1_decode(codes) -> np.ndarray:
+    lib = _load()
+    c = np.asarray(codes, dtype=np.uint8)
+    return np.array([lib.mo_e2m1_decode(int(x)) for x in c.ravel()], dtype=np.float64).reshape(c.shape)
+
+
+def e2m1_encode(values) -> np.ndarray:
+    lib = _load()
+    v = np.asarray(values, dtype=np.float64)
+    return np.array([lib.mo_e2m1_encode(float(x)) for x in v.ravel()], dtype=np.uint8).reshape(v.shape)
+
+
+def group_exponent_fp4(amax: float) -> int:
+    return int(_load().mo_group_exponent_fp4(float(amax)))
 
 
 def group_exponent(amax: float) -> int:
@@ -265,6 +291,20 @@ def kv_write_norm_rope(raw_bits, slots, positions, weight_bits, eps, freqs, kv_c
     p = np.asarray(positions)
     s[(p < 0) | (p >= np.asarray(freqs).shape[0])] = -1
     return kv_write(rows, s, kv_cache, layout, page_size)
+
+
+def q_norm_rope(x_bits, positions, freqs, eps=None, weight_bits=None, out=None) -> np.ndarray:
+    """Query rows (uint16 bf16 bits [n, 576 or 512], one position a row) normalised (if eps is given, with
+    the gain weight_bits) and rotated -> bf16 bits; rows outside the table are left as `out` has them."""
+    lib = _load()
+    x = _c(x_bits, np.uint16)
+    pos = _c(positions, np.int32)
+    w = _c(weight_bits, np.uint16)
+    f = _c(freqs, np.float32)
+    o = np.zeros_like(x) if out is None else np.array(out, dtype=np.uint16, copy=True, order="C")
+    lib.mo_q_norm_rope(_ptr(x), _ptr(pos), int(eps is not None), _ptr(w), float(np.float32(eps or 0.0)), _ptr(f),
+                       f.shape[0], x.shape[0], x.shape[1], _ptr(o))
+    return o
 
 
 def v_up(x_bits, w_bits) -> np.ndarray:

@@ -33,7 +33,8 @@
  *              indices -> out, softmax_lse).
  *  OCP 8-bit floating point specification (E4M3: bias 7, no infinities,
  *  S.1111.111 is NaN, largest finite 448) and the OCP MX specification
- *  (E8M0 scale: 2^(b-127), 0xFF is NaN).
+ *  (E8M0 scale: 2^(b-127), 0xFF is NaN; E2M1: bias 1, no infinities and no NaN,
+ *  largest 6; a block is 32 elements with one E8M0 scale).
  *
  * Readings where the pages are silent:
  *  - lse is natural-log and covers keys only; the sink enters only the output
@@ -44,7 +45,9 @@
  *  - Sparse indices are request-local token positions; entries outside [0, L)
  *    are skipped; duplicates count as often as they appear.
  *  - The fp8 group exponent is the smallest e with 448 * 2^e >= max(amax, 1e-10),
- *    the eps being the fp32 value of 1e-10 (the kernel's precision).
+ *    the eps being the fp32 value of 1e-10 (the kernel's precision); the 4-bit
+ *    one the same with 6 in the place of 448, per 32 elements. A 4-bit group that
+ *    holds a NaN has the scale byte 255 and zero codes.
  *  - RMSNorm covers the 512 latent elements with the mean of squares over 512;
  *    RoPE pairs are adjacent elements (interleaved), rotated by the table's
  *    (cos, sin); k_pe of the 576-wide rows is rotated but not normalised; the
@@ -109,6 +112,28 @@ uint8_t mo_e4m3_encode(double x) {
   return (uint8_t)(sign | ((lo & 1) ? lo + 1 : lo));
 }
 
+/* OCP MX E2M1: sign, 2-bit exponent (bias 1), 1-bit mantissa; E = 0 is subnormal
+ * (M/2 * 2^0). Codes 0-7 are 0, 0.5, 1, 1.5, 2, 3, 4, 6. */
+double mo_e2m1_decode(uint8_t b) {
+  int s = (b >> 3) & 1, E = (b >> 1) & 3, M = b & 1;
+  double v = E == 0 ? 0.5 * M : ldexp(1.0 + 0.5 * M, E - 1);
+  return s ? -v : v;
+}
+
+/* Round-to-nearest-even onto the E2M1 grid, saturating to +-6: the nearest of the
+ * eight magnitudes, a tie going to the even code. x is not NaN. */
+uint8_t mo_e2m1_encode(double x) {
+  const uint8_t sign = signbit(x) ? 8 : 0;
+  const double a = fabs(x);
+  int best = 0, c;
+  if (a >= 6.0) return (uint8_t)(sign | 7);
+  for (c = 1; c < 8; ++c) {
+    const double dc = fabs(mo_e2m1_decode((uint8_t)c) - a), db = fabs(mo_e2m1_decode((uint8_t)best) - a);
+    if (dc < db || (dc == db && (c & 1) == 0)) best = c;
+  }
+  return (uint8_t)(sign | best);
+}
+
 /* OCP MX E8M0 scale: 2^(b-127); 0xFF is NaN. */
 double mo_ue8m0_decode(uint8_t b) {
   if (b == 0xFF) return NAN;
@@ -124,7 +149,13 @@ double mo_ue8m0_decode(uint8_t b) {
  *           page_bytes = page_size * 584 rounded up to a multiple of 576.
  * layout 2: the same with 512 e4m3 NoPE (640 B rows, 8 scale bytes);
  *           page_bytes = page_size * 648 rounded up to a multiple of 640.
- * K has 576 (layouts 0, 2) or 512 (layout 1) elements; V is K[0:512]. */
+ * layout 3: 4-bit row [448 e2m1 NoPE, element 2i in the low nibble of byte i | 64 bf16
+ *           RoPE] = 352 B; after the rows, page_size 16-byte scale slots (14 ue8m0
+ *           bytes, one per 32 elements, + 2 zero bytes); page_bytes = page_size * 368
+ *           rounded up to a multiple of 352.
+ * layout 4: the same with 512 e2m1 NoPE (384 B rows, 16 scale bytes);
+ *           page_bytes = page_size * 400 rounded up to a multiple of 384.
+ * K has 576 (layouts 0, 2, 4) or 512 (layouts 1, 3) elements; V is K[0:512]. */
 int mo_layout_info(int layout, int page_size, int64_t* row_bytes, int64_t* page_bytes, int* dqk, int* nope,
                    int* n_scales) {
   int64_t rb, pb;
@@ -133,6 +164,8 @@ int mo_layout_info(int layout, int page_size, int64_t* row_bytes, int64_t* page_
     case 0: rb = 1152; pb = (int64_t)page_size * 1152; *dqk = 576; *nope = 512; *n_scales = 0; break;
     case 1: rb = 576; pb = (((int64_t)page_size * 584 + 575) / 576) * 576; *dqk = 512; *nope = 448; *n_scales = 7; break;
     case 2: rb = 640; pb = (((int64_t)page_size * 648 + 639) / 640) * 640; *dqk = 576; *nope = 512; *n_scales = 8; break;
+    case 3: rb = 352; pb = (((int64_t)page_size * 368 + 351) / 352) * 352; *dqk = 512; *nope = 448; *n_scales = 14; break;
+    case 4: rb = 384; pb = (((int64_t)page_size * 400 + 383) / 384) * 384; *dqk = 576; *nope = 512; *n_scales = 16; break;
     default: return -1;
   }
   *row_bytes = rb;
@@ -152,6 +185,15 @@ int mo_decode_row(const uint8_t* kv, int layout, int page_size, int64_t page, in
     for (d = 0; d < 576; ++d) {
       memcpy(&h, row + 2 * d, 2);
       k[d] = mo_bf16_decode(h);
+    }
+    return dqk;
+  }
+  if (layout >= 3) {
+    sc = kv + page * pb + (int64_t)page_size * rb + (int64_t)offset * 16;
+    for (d = 0; d < nope; ++d) k[d] = mo_e2m1_decode((row[d / 2] >> (4 * (d % 2))) & 15) * mo_ue8m0_decode(sc[d / 32]);
+    for (d = 0; d < 64; ++d) {
+      memcpy(&h, row + nope / 2 + 2 * d, 2);
+      k[nope + d] = mo_bf16_decode(h);
     }
     return dqk;
   }
@@ -339,6 +381,40 @@ int mo_group_exponent(double a) {
   return e;
 }
 
+/* The same with 6 in the place of 448 (e2m1's largest). */
+int mo_group_exponent_fp4(double a) {
+  int e;
+  if (!(a <= 1e300)) return 127;
+  e = 0;
+  while (e < 127 && ldexp(6.0, e) < a) ++e;
+  while (e > -127 && ldexp(6.0, e - 1) >= a) --e;
+  return e;
+}
+
+/* The NoPE part of a 4-bit row: per 32 elements amax over the numbers, the exponent above, codes
+ * E2M1 RNE-satfinite of x * 2^-e; a group with a NaN: scale byte 255, zero codes. */
+static void write_fp4(const uint16_t* x, int nope, uint8_t* dst, uint8_t* sc) {
+  int g, d;
+  memset(sc, 0, 16);
+  memset(dst, 0, (size_t)nope / 2);
+  for (g = 0; g < nope / 32; ++g) {
+    double amax = (double)(float)1e-10;
+    int e, nan = 0;
+    for (d = 0; d < 32; ++d) {
+      const double v = fabs(mo_bf16_decode(x[g * 32 + d]));
+      if (isnan(v)) nan = 1;
+      else if (v > amax) amax = v;
+    }
+    e = mo_group_exponent_fp4(amax);
+    sc[g] = nan ? 255 : (uint8_t)(e + 127);
+    if (nan) continue;
+    for (d = 0; d < 32; ++d) {
+      const uint8_t c = mo_e2m1_encode(ldexp(mo_bf16_decode(x[g * 32 + d]), -e));
+      dst[(g * 32 + d) / 2] |= (uint8_t)(c << (4 * (d % 2)));
+    }
+  }
+}
+
 /* Write n rows (bf16 bits, [n, row_elems]) into the pages at slots[n]
  * (slot = page * page_size + offset; negative slots are skipped).
  * Layout 0: bit copy of 576 bf16. Layouts 1, 2: for each 64-element NoPE group,
@@ -347,7 +423,8 @@ int mo_group_exponent(double a) {
  * the 64 RoPE values are copied as bf16; the unused scale byte of layout 1 is 0.
  * A NaN element takes no part in amax and is stored as the NaN code 0x7F (what
  * mo_e4m3_encode gives for NaN); an infinite one makes amax infinite (e = 127).
- * Row elements: layout 0 -> 576, layout 1 -> 512 (448 | 64), layout 2 -> 576.
+ * Layouts 3, 4: write_fp4, then the 64 RoPE values copied as bf16.
+ * Row elements: layouts 0, 2, 4 -> 576, layouts 1, 3 -> 512 (448 | 64).
  * Returns 0, or -1 on an out-of-range slot. */
 int mo_kv_write(const uint16_t* rows, const int32_t* slots, int n, uint8_t* kv, int layout, int64_t num_pages,
                 int page_size) {
@@ -366,6 +443,11 @@ int mo_kv_write(const uint16_t* rows, const int32_t* slots, int n, uint8_t* kv, 
     dst = kv + page * pb + (int64_t)off * rb;
     if (layout == 0) {
       memcpy(dst, x, 1152);
+      continue;
+    }
+    if (layout >= 3) {
+      write_fp4(x, nope, dst, kv + page * pb + (int64_t)page_size * rb + (int64_t)off * 16);
+      memcpy(dst + nope / 2, x + nope, 128);
       continue;
     }
     sc = kv + page * pb + (int64_t)page_size * rb + (int64_t)off * 8;
@@ -411,17 +493,17 @@ uint16_t mo_bf16_encode(double x) {
 /* RMSNorm + RoPE of new KV rows ([HALOps-MLA] mla_attention: the kv RMSNorm +
  * RoPE before the KV cache write; kv_norm_weight (gain of the 512 latent
  * elements), kv_eps, positions, and freqs_real: per position 32 interleaved
- * (cos, sin) pairs). Row i (bf16 bits, row_elems = 576 for layouts 0 and 2,
- * 512 for layout 1):
+ * (cos, sin) pairs). Row i (bf16 bits, row_elems = 576 for layouts 0, 2, 4,
+ * 512 for layouts 1, 3):
  *   y[d] = x[d] / sqrt(sum_{e<512} x[e]^2 / 512 + eps) * w[d]   for d < 512;
  *   RoPE pair i of the 64 RoPE elements, (c, s) = freqs[pos, 2i], freqs[pos, 2i+1]:
- *   (u, v) -> (u c - v s, u s + v c); layouts 0 and 2 rotate the raw elements
- *   512..575 (k_pe is not normalised), layout 1 rotates y[448..511];
+ *   (u, v) -> (u c - v s, u s + v c); layouts 0, 2, 4 rotate the raw
+ *   elements 512..575 (k_pe is not normalised), layouts 1, 3 rotate y[448..511];
  * the row is then rounded to bfloat16. Rows whose position lies outside
  * [0, max_pos) are left as zeros and return a count of them. */
 int mo_kv_norm_rope(const uint16_t* raw, const int32_t* positions, const uint16_t* w, double eps, const float* freqs,
                     int max_pos, int n, int layout, uint16_t* out) {
-  const int row_elems = layout == 1 ? 512 : 576;
+  const int row_elems = layout == 1 || layout == 3 ? 512 : 576;
   int bad = 0;
   for (int i = 0; i < n; ++i) {
     const uint16_t* x = raw + (size_t)i * row_elems;
@@ -440,9 +522,9 @@ int mo_kv_norm_rope(const uint16_t* raw, const int32_t* positions, const uint16_
     }
     const double r = 1.0 / sqrt(ss / 512.0 + eps);
     for (int d = 0; d < 512; ++d) y[d] = mo_bf16_decode(x[d]) * r * mo_bf16_decode(w[d]);
-    if (layout != 1)
+    if (row_elems != 512)
       for (int d = 512; d < 576; ++d) y[d] = mo_bf16_decode(x[d]);
-    const int rope0 = layout == 1 ? 448 : 512;
+    const int rope0 = row_elems == 512 ? 448 : 512;
     const float* f = freqs + (size_t)pos * 64;
     for (int p = 0; p < 32; ++p) {
       const double c = f[2 * p], sn = f[2 * p + 1];
@@ -453,6 +535,31 @@ int mo_kv_norm_rope(const uint16_t* raw, const int32_t* positions, const uint16_
     for (int d = 0; d < row_elems; ++d) o[d] = mo_bf16_encode(y[d]);
   }
   return bad;
+}
+
+/* The queries' step of the same launch ([HALOps-MLA] mla_attention: q RMSNorm + RoPE): row i (bf16 bits,
+ * width 576 or 512) of position positions[i]. norm != 0: the first 512 elements are normalised as above
+ * with the gain w (NULL: 1); the last 64 elements are rotated as above; rounded to bfloat16. A row
+ * whose position lies outside [0, max_pos) is left as out has it. */
+void mo_q_norm_rope(const uint16_t* x, const int32_t* positions, int norm, const uint16_t* w, double eps,
+                    const float* freqs, int max_pos, int n, int width, uint16_t* out) {
+  for (int i = 0; i < n; ++i) {
+    const int pos = positions[i];
+    double y[576], ss = 0.0;
+    if (pos < 0 || pos >= max_pos) continue;
+    for (int d = 0; d < width; ++d) y[d] = mo_bf16_decode(x[(size_t)i * width + d]);
+    for (int d = 0; d < 512; ++d) ss += y[d] * y[d];
+    if (norm)
+      for (int d = 0; d < 512; ++d) y[d] = y[d] / sqrt(ss / 512.0 + eps) * (w ? mo_bf16_decode(w[d]) : 1.0);
+    for (int p = 0; p < 32; ++p) {
+      const double c = freqs[(size_t)pos * 64 + 2 * p], sn = freqs[(size_t)pos * 64 + 2 * p + 1];
+      double* z = y + width - 64 + 2 * p;
+      const double u = z[0], v = z[1];
+      z[0] = u * c - v * sn;
+      z[1] = u * sn + v * c;
+    }
+    for (int d = 0; d < width; ++d) out[(size_t)i * width + d] = mo_bf16_encode(y[d]);
+  }
 }
 
 /* Value up-projection ([vLLM-MLA] _v_up_proj: the (N, B, L) latent output times

@@ -20,7 +20,8 @@ bf16 values are float32 normal draws rounded to nearest-even by torch's bf16
 conversion. fp8 NoPE codes are drawn from 256 equiprobable quantiles of N(0,1),
 each rounded to E4M3 by torch's float8_e4m3fn conversion (a discrete stand-in
 for "N(0,1) quantized to e4m3" that generates gigabytes quickly); scale bytes
-are 127 + U{-4..4}.
+are 127 + U{-4..4}. 4-bit rows (a workload's `layout` set to 3 or 4) draw every e2m1
+code alike, with scale bytes 127 + U{-3..0}.
 """
 from __future__ import annotations
 
@@ -32,10 +33,12 @@ import numpy as np
 LAYOUT_BF16 = 0
 LAYOUT_FP8_448 = 1
 LAYOUT_FP8_512 = 2
+LAYOUT_FP4_448 = 3
+LAYOUT_FP4_512 = 4
 
-_ROW_BYTES = {LAYOUT_BF16: 1152, LAYOUT_FP8_448: 576, LAYOUT_FP8_512: 640}
-_NOPE = {LAYOUT_BF16: 512, LAYOUT_FP8_448: 448, LAYOUT_FP8_512: 512}
-_DQK = {LAYOUT_BF16: 576, LAYOUT_FP8_448: 512, LAYOUT_FP8_512: 576}
+_ROW_BYTES = {LAYOUT_BF16: 1152, LAYOUT_FP8_448: 576, LAYOUT_FP8_512: 640, LAYOUT_FP4_448: 352, LAYOUT_FP4_512: 384}
+_NOPE = {LAYOUT_BF16: 512, LAYOUT_FP8_448: 448, LAYOUT_FP8_512: 512, LAYOUT_FP4_448: 448, LAYOUT_FP4_512: 512}
+_DQK = {LAYOUT_BF16: 576, LAYOUT_FP8_448: 512, LAYOUT_FP8_512: 576, LAYOUT_FP4_448: 512, LAYOUT_FP4_512: 576}
 
 
 def page_bytes(layout: int, page_size: int) -> int:
@@ -45,7 +48,8 @@ def page_bytes(layout: int, page_size: int) -> int:
     rb = _ROW_BYTES[layout]
     if layout == LAYOUT_BF16:
         return page_size * rb
-    return -(-(page_size * (rb + 8)) // rb) * rb
+    slot = 8 if layout <= LAYOUT_FP8_512 else 16  # 4-bit rows: one scale byte per 32 elements
+    return -(-(page_size * (rb + slot)) // rb) * rb
 
 
 def row_elems(layout: int) -> int:
@@ -192,6 +196,17 @@ def generate(cfg: Config) -> Workload:
         vals = rng.standard_normal((nrows, 576), dtype=np.float32) * np.float32(cfg.value_scale)
         bits = _bf16_bits(vals).reshape(total_pages, ps * 576)
         kv[:, :ps * rb] = bits.view(np.uint8).reshape(total_pages, ps * rb)
+    elif layout >= LAYOUT_FP4_448:
+        # every e2m1 code alike (rms 2.9), one scale of 2^-3 .. 2^0 per 32 elements
+        nope = _NOPE[layout]
+        rows = kv[:, :ps * rb].reshape(total_pages, ps, rb)
+        rows[:, :, :nope // 2] = rng.integers(0, 256, size=(total_pages, ps, nope // 2), dtype=np.uint8)
+        rope = rng.standard_normal((total_pages, ps, 64), dtype=np.float32) * np.float32(cfg.value_scale)
+        rows[:, :, nope // 2:] = _bf16_bits(rope).view(np.uint8).reshape(total_pages, ps, 128)
+        kv[:, :ps * rb] = rows.reshape(total_pages, ps * rb)
+        scales = np.zeros((total_pages, ps, 16), np.uint8)
+        scales[:, :, :nope // 32] = rng.integers(124, 128, size=(total_pages, ps, nope // 32), dtype=np.uint8)
+        kv[:, ps * rb:ps * (rb + 16)] = scales.reshape(total_pages, ps * 16)
     else:
         nope = _NOPE[layout]
         table = _fp8_quantile_table()
@@ -217,6 +232,10 @@ def generate(cfg: Config) -> Workload:
                 nan16 = np.frombuffer(np.full(rb // 2, 0x7FC1, dtype=np.uint16).tobytes(), np.uint8)
                 if layout == LAYOUT_BF16:
                     kv[page, r0:r0 + rb] = nan16
+                elif layout >= LAYOUT_FP4_448:
+                    s0 = ps * rb + (j % ps) * 16
+                    kv[page, s0:s0 + 16] = 255  # NaN scales
+                    kv[page, r0 + rb - 128:r0 + rb] = nan16[:128]
                 else:
                     nope = _NOPE[layout]
                     kv[page, r0:r0 + nope] = 0x7F
