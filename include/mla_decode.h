@@ -156,7 +156,8 @@ int mla_decode_plan(const int32_t* cache_seqlens, int32_t batch, int32_t q_token
  * MLA", I/O Contract).
  *  q            device bf16 [T = batch*q_tokens_per_req, num_heads, Dqk]
  *               (Dqk = 576, or 512 for the 448-NoPE layouts), 16-byte aligned.
- *  kv_cache     device uint8 [num_pages, page_bytes(layout, page_size)], 16-B aligned.
+ *  kv_cache     device uint8 [num_pages, page_bytes(layout, page_size)], 16-B aligned (4-bit
+ *               layouts: 32-B aligned).
  *  block_table  device int32 [batch, max_pages]: page of each page-sized block.
  *  cache_seqlens device int32 [batch]: L_b, context rows including the query
  *               tokens' own new rows (seq_len = context_len + query_len,

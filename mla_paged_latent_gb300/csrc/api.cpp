@@ -231,6 +231,10 @@ int decode_impl(const void* q, const void* kv_cache, mla_kv_layout layout, int64
     return fail(MLA_ERR_INVALID_ARG, "mla_decode: sm_scale must be a positive finite number");
   if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out))
     return fail(MLA_ERR_INVALID_ARG, "mla_decode: q, kv_cache and out must be 16-byte aligned");
+  if (layout >= MLA_KV_FP4_448_UE8M0 && (reinterpret_cast<uintptr_t>(kv_cache) & 31u) != 0)
+    return fail(MLA_ERR_INVALID_ARG, "mla_decode: a 4-bit kv_cache must be 32-byte aligned");
+  if (layout >= MLA_KV_FP4_448_UE8M0 && num_pages >= ((1ll << 32) - 1) / page_size)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_decode: more than 2^32 cache slots");
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(MLA_ERR_INVALID_ARG, "mla_decode: workspace must be 256-byte aligned");
   const size_t need = workspace_bytes_for(total_splits, R);

@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(128) kv_gather_kernel(const uint8_t* __restric
   if (layout >= 3) {
     for (int i = lane; i < nope / 8; i += 32) {
       uint32_t o4[4];
-      fp4x8_to_bf16(reinterpret_cast<const uint32_t*>(src)[i], ue8m0_to_bf16x2(sc[i >> 2]), o4);
+      fp4x8_to_bf16(reinterpret_cast<const uint32_t*>(src)[i], fp4_scale(sc[i >> 2]), o4);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         o[8 * i + 2 * k] = bf16_to_f32(o4[k] & 0xFFFFu);

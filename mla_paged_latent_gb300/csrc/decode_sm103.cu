@@ -83,6 +83,11 @@ struct Misc {
   uint8_t mask[2][8];  // sparse / gathered row validity per stage, one byte per 8 rows
 };
 
+template <bool B>
+struct Bool {
+  static constexpr bool value = B;
+};
+
 template <int LAYOUT, bool TMA_KV>
 struct Cfg {
   static constexpr int kNslab = row_width(LAYOUT) / 64;
@@ -818,6 +823,37 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
               hi[i] = make_uint4(o[4], o[5], o[6], o[7]);
             }
           }
+          // 4-bit rows: code chunk c holds the 32 codes of group c, dims [32c, 32c + 32) of slab c / 2. Eight lanes
+          // store two rows' halves of two slabs at a time: the odd slab's take their words in the order 2, 3, 0, 1,
+          // so that the eight 16-byte stores fall on different banks.
+          uint4 e4[C::kFp4 ? 4 : 1][4];
+          if (C::kFp4) {
+            const uint32_t sw[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
+            uint32_t sb4[4];
+            bool plain = true;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              sb4[i] = (sw[i] >> (8 * part4)) & 0xFFu;
+              plain = plain && (fp4_scale_plain(sb4[i]) || part4 + 4 * i >= C::kCodeChunks);
+            }
+            auto expand = [&](auto p) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const Fp4Scale s = fp4_scale(sb4[i]);
+                const bool odd = part4 & 2;
+                const uint32_t w4[4] = {odd ? v[i].z : v[i].x, odd ? v[i].w : v[i].y, odd ? v[i].x : v[i].z,
+                                        odd ? v[i].y : v[i].w};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  uint32_t o[4];
+                  fp4x8_to_bf16<decltype(p)::value>(w4[q], s, o);
+                  e4[i][q] = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+              }
+            };
+            if (__all_sync(0xffffffffu, plain || !valid)) expand(Bool<true>{});
+            else expand(Bool<false>{});
+          }
           if (it >= 2 && !mbar_wait(bar(kv_empty(st, 4)), ((it >> 1) - 1) & 1, abort_flag, P.status)) return;
           fence_proxy_async_smem();
           if (lane == 0) {
@@ -832,17 +868,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             const int c = part4 + 4 * i;
             if (C::kFp4) {
               if (c < C::kCodeChunks) {
-                // 32 codes of group c: dims [32c, 32c + 32) of slab c / 2
-                const uint32_t w4[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                const uint32_t sw[4] = {sc4.x, sc4.y, sc4.z, sc4.w};
-                const uint32_t s2 = ue8m0_to_bf16x2((sw[i & 3] >> (8 * part4)) & 0xFFu);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  uint32_t o[4];
-                  fp4x8_to_bf16(w4[q], s2, o);
-                  st_shared_v4(dst + (c >> 1) * kSlab + sw128_offset(crow, (c & 1) * 32 + 8 * q),
-                               make_uint4(o[0], o[1], o[2], o[3]));
-                }
+                for (int q = 0; q < 4; ++q)
+                  st_shared_v4(dst + (c >> 1) * kSlab + sw128_offset(crow, (c & 1) * 32 + 8 * (q ^ (part4 & 2))), e4[i][q]);
               } else if (c < C::kChunks) {
                 const int dim = C::kNope + 8 * (c - C::kCodeChunks);
                 st_shared_v4(dst + (dim >> 6) * kSlab + sw128_offset(crow, dim & 63), v[i]);

@@ -15,10 +15,11 @@ namespace mla {
 constexpr int kFp4Group = 32;         // elements that share a scale
 constexpr int kFp4ScaleSlot = 16;     // bytes of a row's scale slot
 
-// ue8m0 byte -> the bf16 pair (2^(b - 127), 2^(b - 127)); 0 is the subnormal 2^-127, 255 NaN.
-__device__ __forceinline__ uint32_t ue8m0_to_bf16x2(uint32_t b) {
-  const uint32_t h = b == 0u ? 0x0040u : (b == 255u ? 0x7FC0u : b << 7);
-  return h * 0x00010001u;
+// Byte permute; every selector nibble is 0-7.
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+  return r;
 }
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -26,23 +27,45 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Eight codes (element 0 in bits 0-3) times the scale pair -> four bf16 pairs in element order.
-// The magnitudes' high and low bytes come from two 8-entry tables, four codes a byte permute (the
-// codes' own nibbles are the selectors), the sign bits are spread into the high bytes, and two more
-// permutes interleave them: 2.6 instructions an element pair with the exact product, against 4 for
-// a conversion through f16 and fp32.
-__device__ __forceinline__ void fp4x8_to_bf16(uint32_t w, uint32_t scale2, uint32_t (&o)[4]) {
+// A group's scale 2^(b - 127) in two factors: f16 bits, which hold 2^-14 .. 2^15, and a bf16 pair with the
+// rest (one for the scales of ordinary rows; NaN for b = 255).
+struct Fp4Scale {
+  uint16_t h;
+  uint32_t rest;
+};
+__device__ __forceinline__ bool fp4_scale_plain(uint32_t b) { return b - 113u <= 29u; }  // rest is one
+__device__ __forceinline__ Fp4Scale fp4_scale(uint32_t b) {
+  const uint32_t c = b < 113u ? 113u : (b > 142u ? 142u : b);
+  Fp4Scale s;
+  s.h = static_cast<uint16_t>((c - 112u) << 10);
+  s.rest = b == 255u ? 0x7FC07FC0u : ((b + 127u - c) << 7) * 0x00010001u;
+  return s;
+}
+// Eight codes (element 0 in bits 0-3) times the scale -> four bf16 pairs in element order, exactly: e2m1 to f16,
+// an fp32 product with the f16 factor, two of them rounded (that is, cut) to a bf16 pair. Measured for a group
+// of 32 a lane, on all four sub-partitions, with the 64 bytes stored: 93 cycles; with the magnitudes taken from
+// byte-permute tables and the signs joined on, which all runs in one pipe, 130; a plain f16 product, which loses
+// scales, 74, where the stores are the bound. (The -0.0 addend keeps the sign of a zero.) PLAIN: the caller has seen
+// that the rest is one.
+template <bool PLAIN = false>
+__device__ __forceinline__ void fp4x8_to_bf16(uint32_t w, const Fp4Scale& s, uint32_t (&o)[4]) {
+  uint32_t h[4];
+  asm("{\n .reg .b8 t0, t1, t2, t3;\n mov.b32 {t0, t1, t2, t3}, %4;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, t0;\n cvt.rn.f16x2.e2m1x2 %1, t1;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, t2;\n cvt.rn.f16x2.e2m1x2 %3, t3;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t v = h ? w >> 16 : w;
-    const uint32_t sel = v & 0x7777u;
-    const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
-    uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel);
-    const uint32_t s = __byte_perm(v, 0u, 0x1100);  // bytes 0, 0, 1, 1: two codes in each
-    hi |= s & 0x80008000u;
-    hi |= (s << 4) & 0x00800080u;
-    o[2 * h] = mul_bf16x2(__byte_perm(lo, hi, 0x5140), scale2);
-    o[2 * h + 1] = mul_bf16x2(__byte_perm(lo, hi, 0x7362), scale2);
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    asm("{\n .reg .b16 l, u;\n mov.b32 {l, u}, %2;\n fma.rn.f32.f16 %0, l, %3, %4;\n fma.rn.f32.f16 %1, u, %3, %4;\n}\n"
+        : "=f"(a), "=f"(b)
+        : "r"(h[i]), "h"(s.h), "f"(-0.0f));
+    o[i] = f32x2_to_bf16x2(a, b);
+  }
+  if (!PLAIN) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = mul_bf16x2(o[i], s.rest);
   }
 }
 

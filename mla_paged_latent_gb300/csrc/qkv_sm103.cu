@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_read_kernel(const uint8_t* 
                           f32x2_to_bf16x2(d.x * s, d.y * s), f32x2_to_bf16x2(e.x * s, e.y * s));
     } else {
       uint32_t o[4];
-      fp4x8_to_bf16(reinterpret_cast<const uint32_t*>(src)[c], ue8m0_to_bf16x2(sc[c >> 2]), o);
+      fp4x8_to_bf16(reinterpret_cast<const uint32_t*>(src)[c], fp4_scale(sc[c >> 2]), o);
       dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
