@@ -90,9 +90,10 @@ typedef enum {
 #define MLA_GROUP_ROWS 64       /* query rows (token x head) per CTA work item */
 #define MLA_WORKSPACE_HEADER 256
 #define MLA_DECODE_SKIP_COMBINE 1u  /* mla_decode flag: leave split partials in the workspace */
-/* A dense bf16 decode whose query rows per request (q_tokens_per_req x num_heads) come in
- * groups of 128 (for example 128 heads) runs on the CTA-pair kernel: two SMs per group of
- * 128 query rows share each KV tile through one tensor-core pair. mla_decode flag: run it on
+/* A decode whose query rows per request (q_tokens_per_req x num_heads) come in groups of 128
+ * (for example 128 heads) runs on a CTA-pair kernel: two SMs per group of 128 query rows share
+ * each KV tile through one tensor-core pair. That is so for a dense decode of bf16 rows, and for
+ * 4-bit rows dense or, where num_heads is a multiple of 128, listed. mla_decode flag: run it on
  * the single-SM kernel instead (same results within the stated tolerances; for comparison
  * and testing). Ignored for other decodes. */
 #define MLA_DECODE_SINGLE_SM 2u

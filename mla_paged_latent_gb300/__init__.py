@@ -193,8 +193,8 @@ def mla_decode(q, kv_cache, layout: int, page_size: int, block_table, cache_seql
     q bf16 [T, N, Dqk]; kv_cache uint8 [num_pages, page_bytes]; block_table int32 [B, max_pages];
     cache_seqlens int32 [B]; sched int32 [P, 8]; num_splits int32 [B+1]; workspace uint8;
     out bf16 [T, N, 512]; lse float32 [T, N]; sink float32 [N] or None; indices int32 [T, topk] or None.
-    single_sm: run a dense bf16 decode whose query rows come in groups of 128 on the single-SM
-    kernel instead of the CTA-pair kernel."""
+    single_sm: run a decode whose query rows come in groups of 128 (dense over bf16 rows, or over
+    4-bit rows) on the single-SM kernel instead of the CTA-pair kernel."""
     _require_cuda(q, kv_cache, block_table, cache_seqlens, sched, num_splits, workspace, out, lse, sink, indices)
     T, N, D = q.shape
     B = cache_seqlens.shape[0]

@@ -106,11 +106,13 @@ EncodeTiledFn get_encode_fn(int* err) {
   return fn;
 }
 
-// Most 2-CTA clusters of the pair decode kernel resident at once on the current device
-// (looked up once per device).
-int pair_cluster_capacity(int* n) {
+// Most 2-CTA clusters of the layout's pair decode kernel resident at once on the current device
+// (looked up once per device and kernel).
+int pair_cluster_capacity(mla_kv_layout layout, int* n) {
   static std::mutex mu;
-  static int cache[64] = {};
+  static int caches[3][64] = {};
+  const int kernel = layout == MLA_KV_FP4_448_UE8M0 ? 1 : layout == MLA_KV_FP4_512_UE8M0 ? 2 : 0;
+  int* const cache = caches[kernel];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
@@ -118,7 +120,7 @@ int pair_cluster_capacity(int* n) {
   if (dev < 0 || dev >= 64) return fail(MLA_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
   if (cache[dev] == 0) {
     int c = 0;
-    e = mla::decode_pair_max_clusters(&c);
+    e = kernel == 0 ? mla::decode_pair_max_clusters(&c) : mla::decode_pair_fp4_max_clusters(static_cast<int>(layout), &c);
     if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters (pair decode kernel)");
     if (c < 1) return fail(MLA_ERR_UNSUPPORTED, "no 2-CTA cluster of the pair decode kernel fits on this device");
     cache[dev] = c;
@@ -344,10 +346,18 @@ int decode_impl(const void* q, const void* kv_cache, mla_kv_layout layout, int64
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (tma_kv && R % 128 == 0 && !(flags & MLA_DECODE_SINGLE_SM)) {
+  const bool fp4 = layout == MLA_KV_FP4_448_UE8M0 || layout == MLA_KV_FP4_512_UE8M0;
+  const bool one_token = (indices == nullptr && runs == nullptr) || num_heads % 128 == 0;  // of a group's listed rows
+  if (fp4 && R % 128 == 0 && one_token && !(flags & MLA_DECODE_SINGLE_SM)) {
+    int cap = 0;
+    if (int rc = pair_cluster_capacity(layout, &cap)) return rc;
+    const int work = num_partitions * static_cast<int>(R / 128);
+    e = mla::launch_decode_pair_fp4(static_cast<int>(layout), p, q_map, work < cap ? work : cap, s);
+    if (e != cudaSuccess) return cuda_fail(e, "mla_decode: 4-bit pair decode launch");
+  } else if (tma_kv && R % 128 == 0 && !(flags & MLA_DECODE_SINGLE_SM)) {
     // query rows in groups of 128: one CTA pair per (partition, group of 128 rows)
     int cap = 0;
-    if (int rc = pair_cluster_capacity(&cap)) return rc;
+    if (int rc = pair_cluster_capacity(layout, &cap)) return rc;
     const int work = num_partitions * static_cast<int>(R / 128);
     e = mla::launch_decode_pair(p, q_map, kv_map, wide, work < cap ? work : cap, s);
     if (e != cudaSuccess) return cuda_fail(e, "mla_decode: pair decode launch");

@@ -15,12 +15,6 @@ namespace mla {
 constexpr int kFp4Group = 32;         // elements that share a scale
 constexpr int kFp4ScaleSlot = 16;     // bytes of a row's scale slot
 
-// Byte permute; every selector nibble is 0-7.
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-  uint32_t r;
-  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
-  return r;
-}
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));

@@ -75,6 +75,11 @@ size_t decode_pair_smem_bytes();
 cudaError_t launch_decode_pair(const DecodeParams& p, const CUtensorMap& q_map, const CUtensorMap& kv_map,
                                const WideMaps& wide, int clusters, cudaStream_t stream);
 cudaError_t decode_pair_max_clusters(int* clusters);
+// The same for 4-bit rows (decode_pair_fp4_sm103.cu): layout 3 or 4, dense, or listed rows with a group of 128
+// query rows inside one token (heads % 128 == 0).
+cudaError_t launch_decode_pair_fp4(int layout, const DecodeParams& p, const CUtensorMap& q_map, int clusters,
+                                   cudaStream_t stream);
+cudaError_t decode_pair_fp4_max_clusters(int layout, int* clusters);
 cudaError_t launch_decode(DecodeVariant v, const DecodeParams& p, const CUtensorMap& q_map,
                           const CUtensorMap& kv_map, int grid, cudaStream_t stream);
 

@@ -576,6 +576,92 @@ def test_timed_out_wait_is_reported(layout):
     assert_decode(out, lse, decode(w, w.kv_cache, dense_slots(w)), "after a timed-out call")
 
 
+# ----------------------------------------------------------------------------- 128 query rows a request: CTA pairs
+@pytest.mark.parametrize("layout", FP4)
+@pytest.mark.parametrize("sq,heads,splits", [(1, 128, 1), (1, 256, 3), (3, 128, 1), (2, 192, 2)])
+def test_pairs_and_single_sms_agree(layout, sq, heads, splits):
+    """Query rows in groups of 128, on CTA pairs and, by the flag, on single SMs."""
+    w = workloads.generate(workloads.verify(batch=3, sq=sq, heads=heads, seqlens=(1, 700, 66), len_dist="fixed",
+                                            layout=layout, new_rows=False, tail_fill="nan"))
+    d = DeviceWorkload(w)
+    p = d.make_plan(min_splits=splits)
+    ref = decode(w, w.kv_cache, dense_slots(w))
+    for single in (False, True):
+        d.out.fill_(7)
+        mla.mla_decode(d.q, d.kv, layout, 64, d.bt, d.sl, sq, w.cfg.sm_scale, d.sched, d.ns, p.num_partitions,
+                       p.total_splits, d.ws, d.out, d.lse, sink=d.sink, causal=True, single_sm=single)
+        assert mla.mla_read_status(d.ws) == 0
+        assert_decode(bf16_to_f64(d.out), d.lse.cpu().numpy().astype(np.float64), ref, f"single_sm {single}")
+
+
+@pytest.mark.parametrize("layout", FP4)
+@pytest.mark.parametrize("topk,heads,sq", [(300, 256, 1), (65, 128, 3)])
+def test_pairs_listed_rows(layout, topk, heads, sq):
+    """Several groups of 128 query rows over one token's list, and several tokens with lists of their own."""
+    w = workloads.generate(workloads.sparse(batch=2, sq=sq, heads=heads, seqlens=(1000, 90), layout=layout, topk=topk,
+                                            page_size=16, new_rows=False))
+    w.indices[0, ::7] = -1
+    w.indices[-1] = -1
+    w.indices[-1, topk - 1] = 3                   # a single row, listed last
+    _, out, lse = _run(w)
+    assert_decode(out, lse, decode(w, w.kv_cache, listed_slots(w)), f"top {topk}")
+
+
+@pytest.mark.parametrize("layout", FP4)
+def test_pairs_wide_scales(layout):
+    """Scale bytes from 20 to 140 in one cache, one magnitude per column group (as for single SMs above)."""
+    w = workloads.generate(workloads.dsv3(batch=2, seqlens=(300, 77), len_dist="fixed", heads=128, layout=layout,
+                                          new_rows=False, seed=9))
+    ps, rb, nope = 64, workloads._ROW_BYTES[layout], workloads._NOPE[layout]
+    sc = w.kv_cache[:, ps * rb:ps * (rb + 16)].reshape(-1, ps, 16)
+    sc[..., :nope // 32] = np.clip(np.arange(nope // 32) * 8 + 20 + np.arange(ps)[:, None] % 4, 20, 140)
+    w.kv_cache[:, ps * rb:ps * (rb + 16)] = sc.reshape(-1, ps * 16)
+    q = bf16_f64(w.q)
+    q[..., :nope] = 0
+    w.q[:] = _bits(q)
+    _, out, lse = _run(w)
+    assert_decode(out, lse, decode(w, w.kv_cache, dense_slots(w)), "wide scales")
+
+
+@pytest.mark.parametrize("layout", FP4)
+def test_pairs_nan_group_and_bad_page(layout):
+    """A NaN group reaches its own request only; a bad page's rows are left out and reported; and a timed-out wait
+    ends the call, after which the next is whole."""
+    w = workloads.generate(workloads.dsv4(batch=3, seqlens=(200, 100, 400), len_dist="fixed", heads=128, layout=layout,
+                                          new_rows=False))
+    held = w.kv_cache.copy()
+    w.kv_cache[w.block_table[1, 0], 64 * workloads._ROW_BYTES[layout] + 5] = 255
+    good = w.block_table.copy()
+    w.block_table[0, 1] = w.kv_cache.shape[0] + 7
+    d = DeviceWorkload(w)
+    p = d.make_plan()
+    d.decode()
+    with pytest.raises(mla.MlaError) as e:
+        mla.mla_read_status(d.ws)
+    assert e.value.code == -5
+    assert d.out[1].isnan().all() and d.lse[1].isnan().all()
+    w.block_table[:] = good
+    w.kv_cache[:] = held
+
+    def rows(t):
+        s = dense_slots(w)(t)
+        return s[(np.arange(s.size) < 64) | (np.arange(s.size) >= 128)] if t == 0 else s
+
+    out, lse = bf16_to_f64(d.out), d.lse.cpu().numpy().astype(np.float64)
+    ref = decode(w, held, rows)
+    keep = [0, 2]
+    assert_decode(out[keep], lse[keep], tuple(x[keep] if isinstance(x, np.ndarray) and x.ndim else x for x in ref),
+                  "the other requests")
+    d = DeviceWorkload(w)
+    p = d.make_plan()
+    mla.mla_decode(d.q, d.kv, layout, 64, d.bt, d.sl, 1, w.cfg.sm_scale, d.sched, d.ns, p.num_partitions, p.total_splits,
+                   d.ws, d.out, d.lse, sink=d.sink, _test_withhold_signal=True)
+    with pytest.raises(mla.MlaError):
+        mla.mla_read_status(d.ws)
+    out, lse = d.run(write=False)
+    assert_decode(out, lse, decode(w, w.kv_cache, dense_slots(w)), "after a timed-out call")
+
+
 # ----------------------------------------------------------------------------- a step as a whole
 @pytest.mark.parametrize("layout,heads,sq", [(3, 64, 1), (4, 128, 1), (4, 64, 3)])
 def test_serving_steps(layout, heads, sq):
