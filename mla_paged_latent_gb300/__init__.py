@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 import threading
 
@@ -110,11 +111,22 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_torch_c = None
+
+
 def _stream(stream):
-    if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+    """The stream's handle; None: the current stream of the current device. (Asking torch for a Stream object takes
+    3 us on the host, its handle a tenth of that: small calls are bound by the host.)"""
+    global _torch_c
+    if stream is not None:
+        return stream.cuda_stream
+    if _torch_c is not None:
+        return _torch_c._cuda_getCurrentRawStream(_torch_c._cuda_getDevice())
+    import torch
+    handle = torch.cuda.current_stream().cuda_stream
+    if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+        _torch_c = torch._C
+    return handle
 
 
 def _require_cuda(*tensors):
@@ -123,18 +135,40 @@ def _require_cuda(*tensors):
             raise ValueError("all tensors passed to the device entry points must live on the GPU")
 
 
+def _require_one_device(*tensors):
+    """All on one GPU, the one that the call launches on."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"all tensors must live on one device, not on {tensors[0].device} and {t.device}")
+    if device >= 0:
+        import torch
+        current = torch.cuda.current_device() if _torch_c is None else _torch_c._cuda_getDevice()
+        if device != current:
+            raise ValueError(f"the tensors live on cuda:{device}, the current device is cuda:{current}")
+
+
+_dtypes = {}  # name -> torch dtype
+
+
 def _require(name: str, t, dtype: str, *shape, contiguous: bool = True):
     """One tensor's type, shape (None: any size) and layout; raises ValueError."""
-    if str(t.dtype) != "torch." + dtype:
+    want = _dtypes.get(dtype)
+    if want is None:
+        import torch
+        want = _dtypes[dtype] = getattr(torch, dtype)
+    if t.dtype is not want:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have the shape {list(shape)}, not {list(t.shape)}")
+    have = t.shape
+    if have != shape and (len(have) != len(shape) or
+                          any(w is not None and h != w for h, w in zip(have, shape))):
+        raise ValueError(f"{name} must have the shape {list(shape)}, not {list(have)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _require_cache(kv_cache, layout: int, page_size: int):
-    _require("kv_cache", kv_cache, "uint8", None, mla_page_bytes(layout, page_size))
+    _require("kv_cache", kv_cache, "uint8", None, _page_bytes(layout, page_size))
 
 
 def _require_status(status):
@@ -146,6 +180,9 @@ def mla_page_bytes(layout: int, page_size: int) -> int:
     out = ctypes.c_int64()
     _check(load().mla_page_bytes(layout, page_size, ctypes.byref(out)))
     return out.value
+
+
+_page_bytes = functools.lru_cache(maxsize=None)(mla_page_bytes)
 
 
 @dataclasses.dataclass
@@ -334,14 +371,17 @@ def mla_qkv_norm_rope(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, kv
     apart by their stride; slots and positions int32 [T]; kv_norm_weight and q_norm_weight bf16 [512];
     freqs float32 [max_pos, 64]; q_out bf16 [T, N, ROW_ELEMS] (or the queries' own memory, row for row).
     status: optional device uint32 [1] receiving MLA_STATUS_BAD_SLOT (4) / MLA_STATUS_BAD_POSITION (8)."""
-    _require_cuda(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, freqs, q_out, kv_cache, q_norm_weight, status)
+    tensors = q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, freqs, q_out, kv_cache, q_norm_weight, status
+    _require_cuda(*tensors)
+    _require_one_device(*tensors)
     _require_cache(kv_cache, layout, page_size)
     width = ROW_ELEMS[layout]
     T, N = q_nope.shape[:2]
     _require("q_nope", q_nope, "bfloat16", T, N, 448 if width == 512 else 512, contiguous=False)
     _require("q_pe", q_pe, "bfloat16", T, N, 64, contiguous=False)
     _require("kv_raw", kv_raw, "bfloat16", T, width, contiguous=False)
-    if T > 0 and any(t.stride(-1) != 1 for t in (q_nope, q_pe, kv_raw)):
+    (qs, qh, q1), (ps, ph, p1), (rs, r1) = q_nope.stride(), q_pe.stride(), kv_raw.stride()
+    if T > 0 and not (q1 == p1 == r1 == 1):
         raise ValueError("q_nope, q_pe and kv_raw must have their last elements adjacent")
     _require("slots", slots, "int32", T)
     _require("positions", positions, "int32", T)
@@ -351,12 +391,11 @@ def mla_qkv_norm_rope(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, kv
     if q_norm_weight is not None:
         _require("q_norm_weight", q_norm_weight, "bfloat16", 512)
     _require_status(status)
-    _check(load().mla_qkv_norm_rope(_ptr(q_nope), q_nope.stride(0), q_nope.stride(1), _ptr(q_pe), q_pe.stride(0),
-                                    q_pe.stride(1), int(q_eps is not None), _ptr(q_norm_weight),
-                                    0.0 if q_eps is None else float(q_eps), _ptr(kv_raw), kv_raw.stride(0), _ptr(slots),
-                                    _ptr(positions), _ptr(kv_norm_weight), float(kv_eps), _ptr(freqs), freqs.shape[0],
-                                    T, N, _ptr(q_out), _ptr(kv_cache), layout, kv_cache.shape[0], page_size,
-                                    _ptr(status), _stream(stream)))
+    _check(load().mla_qkv_norm_rope(q_nope.data_ptr(), qs, qh, q_pe.data_ptr(), ps, ph, q_eps is not None,
+                                    _ptr(q_norm_weight), 0.0 if q_eps is None else q_eps, kv_raw.data_ptr(), rs,
+                                    slots.data_ptr(), positions.data_ptr(), kv_norm_weight.data_ptr(), kv_eps,
+                                    freqs.data_ptr(), freqs.shape[0], T, N, q_out.data_ptr(), kv_cache.data_ptr(),
+                                    layout, kv_cache.shape[0], page_size, _ptr(status), _stream(stream)))
 
 
 def mla_kv_read(kv_cache, layout: int, page_size: int, slots, rows, status=None, stream=None):
@@ -364,6 +403,7 @@ def mla_kv_read(kv_cache, layout: int, page_size: int, slots, rows, status=None,
     left as it was). status: optional device uint32 [1] receiving MLA_STATUS_BAD_SLOT (4) for a slot past
     the cache."""
     _require_cuda(kv_cache, slots, rows, status)
+    _require_one_device(kv_cache, slots, rows, status)
     _require_cache(kv_cache, layout, page_size)
     _require("slots", slots, "int32", None)
     _require("rows", rows, "bfloat16", slots.shape[0], ROW_ELEMS[layout])
