@@ -104,31 +104,6 @@ struct PairMisc {
 static_assert(Cfg<4>::kOffMisc + sizeof(PairMisc) + 1024 <= 232448, "shared memory budget of one CTA");
 static_assert(Cfg<3>::kOffMisc + sizeof(PairMisc) + 1024 <= 232448, "shared memory budget of one CTA");
 
-// mbar_wait_cluster in few instructions, bounded the same way: the roles of a CTA run at once from one instruction
-// cache, and that function inlined at each of the kernel's waits was a third of its code (instruction fetches
-// were a sixth of all stalls; a call instead costs the registers that live across it: 132 us against 140). No timer is
-// read before the first test has failed, and the tests carry no suspend hint (each 1%).
-__device__ __forceinline__ bool wait_bar(uint32_t b, uint32_t parity, volatile int* abort, unsigned int* status) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p, q;\n .reg .u64 t0, t;\n .reg .u32 a;\n"
-      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n @p bra DONE_%=;\n"
-      " mov.u64 t0, %%globaltimer;\n"
-      "POLL_%=:\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n @p bra DONE_%=;\n"
-      " ld.volatile.shared.u32 a, [%3];\n mov.u64 t, %%globaltimer;\n sub.u64 t, t, t0;\n"
-      " setp.lt.u64 q, t, 2000000000;\n setp.eq.and.u32 q, a, 0, q;\n @q bra POLL_%=;\n"
-      "DONE_%=:\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(b), "r"(parity), "r"(smem_addr(const_cast<int*>(abort)))
-      : "memory");
-  if (ok != 0) return true;
-  if (*abort == 0) {
-    atomicOr(status, 1u);
-    *abort = 1;
-  }
-  return false;
-}
-
 // mma_bf16_pair with the operands' descriptors given by their low words (the start address; an offset within shared
 // memory does not carry out of it): half the arithmetic of an MMA in the issuers, whose instructions wait their turn
 // among the other roles' (125 us against 128; PV held back behind the next tile's S instead: 132).

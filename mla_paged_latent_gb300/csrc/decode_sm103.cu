@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_s = idesc_bf16_f32(64, 64, 0, 0);  // M = 64: rows over all four lane quarters
       const uint64_t kmaj = sdesc_sw128(0, 16, 1024);  // K-major: Q, K tile
-      const uint64_t qa = kmaj | (sb >> 4);
+      const uint32_t khi = static_cast<uint32_t>(kmaj >> 32);
+      const uint32_t qa = static_cast<uint32_t>(kmaj) | (sb >> 4);
       int it = 0, u = 0;
       for (int w = blockIdx.x; w < P.num_work && !*abort_flag; w += gridDim.x) {
         const int part = w / G;
@@ -294,13 +295,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             if (itj >= 2 && !mbar_wait(bar(kSFree + st), par ^ 1u, abort_flag, P.status)) return;
             tc_fence_after();
             const uint32_t d = tmem_s + st * 64;
-            uint64_t qs = qa, ksd = kmaj | (C::stage(sb, st) >> 4);
+            uint32_t qs = qa, ksd = static_cast<uint32_t>(kmaj) | (C::stage(sb, st) >> 4);
 #pragma unroll 1
             for (int s = 0; s < NS; ++s) {
               if (TMA_KV && (s & 3) == 0 && !mbar_wait(bar(kv_full(st, slab_group(s))), par, abort_flag, P.status))
                 return;
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk) mma_bf16_ss(d, qs + kk * 2, ksd + kk * 2, idesc_s, (s | kk) ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_ss_lo(d, qs + kk * 2, khi, ksd + kk * 2, khi, idesc_s, (s | kk) ? 1u : 0u);
               qs += kSlab >> 4;
               ksd += kSlab >> 4;
             }
@@ -324,6 +326,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     if (lane == 0) {
       const uint64_t kmaj = sdesc_sw128(0, 16, 1024);     // K-major: P^T
       const uint64_t vmaj = sdesc_sw128(0, kSlab, 1024);  // MN-major: V^T (slab pairs)
+      const uint32_t phi = static_cast<uint32_t>(kmaj >> 32), vhi = static_cast<uint32_t>(vmaj >> 32);
       int it = 0, u = 0;
       for (int w = blockIdx.x; w < P.num_work && !*abort_flag; w += gridDim.x) {
         const int part = w / G, g = w % G;
@@ -340,19 +343,21 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
             if (!mbar_wait(bar(kPFull + st), (itj >> 1) & 1, abort_flag, P.status)) return;
             if (jj == 0 && u > 0 && !mbar_wait(bar(kOFree), (u - 1) & 1, abort_flag, P.status)) return;
             tc_fence_after();
-            const uint64_t pb = kmaj | (C::parea(sb, st) >> 4);
-            const uint64_t plo = kmaj | (C::plo(sb, st) >> 4);
+            const uint32_t pb = static_cast<uint32_t>(kmaj) | (C::parea(sb, st) >> 4);
+            const uint32_t plo = static_cast<uint32_t>(kmaj) | (C::plo(sb, st) >> 4);
             // compact (rolled) issue loop: the issuing thread must not stall on instruction fetch
-            uint64_t vblk = vmaj | (C::stage(sb, st) >> 4);
+            uint32_t vblk = static_cast<uint32_t>(vmaj) | (C::stage(sb, st) >> 4);
 #pragma unroll 1
             for (int blk = 0; blk < 4; ++blk) {
               const uint32_t dcol = tmem_o + blk * 64;
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ss(dcol, vblk + kk * (2048 >> 4), pb + kk * 2, idesc_o, (jj == 0 && kk == 0) ? 0u : 1u);
+                mma_bf16_ss_lo(dcol, vblk + kk * (2048 >> 4), vhi, pb + kk * 2, phi, idesc_o,
+                               (jj == 0 && kk == 0) ? 0u : 1u);
               if (C::kPSplit) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_bf16_ss(dcol, vblk + kk * (2048 >> 4), plo + kk * 2, idesc_o, 1u);
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_bf16_ss_lo(dcol, vblk + kk * (2048 >> 4), vhi, plo + kk * 2, phi, idesc_o, 1u);
               }
               mma_commit(bar(kv_empty(st, blk)));  // V slabs 2blk, 2blk+1 may be refilled
               vblk += (2 * kSlab) >> 4;
