@@ -176,6 +176,36 @@ __global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* __restric
             page_bytes);
 }
 
+// The same for 4-bit rows. Bound by the length of a row's chain (one row a warp, as many warps as fit) and by its
+// instructions. So the row is loaded beside its slot and not after it, and the largest magnitude of a group and its
+// NaNs are found at once, on bf16 pairs taken as integers. 65000 rows of 448 + 64: 20 us (4.5 TB/s) against 29 with
+// neither.
+template <int LAYOUT>
+__global__ void __launch_bounds__(256) kv_write_fp4_kernel(const uint16_t* __restrict__ rows,
+                                                           const int32_t* __restrict__ slots, int n,
+                                                           uint8_t* __restrict__ kv, int64_t num_pages, int page_size,
+                                                           int64_t page_bytes, uint32_t* status) {
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kNope = row_nope(LAYOUT), kRowBytes = row_stored_bytes(LAYOUT);
+  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= n) return;
+  const uint4* x = reinterpret_cast<const uint4*>(rows + (int64_t)r * row_width(LAYOUT));
+  const uint4 x0 = x[2 * lane], x1 = x[2 * lane + 1], pe = x[kNope / 8 + (lane & 7)];
+  const int slot = slots[r];
+  if (slot < 0) return;
+  const int page = slot / page_size;
+  const int off = slot - page * page_size;
+  if (page >= num_pages) {  // reported, not written
+    if (lane == 0 && status != nullptr) atomicOr(status, 4u);
+    return;
+  }
+  uint8_t* const pg = kv + page * page_bytes;
+  write_row_fp4(x0, x1, pe, lane, kNope, pg + (int64_t)off * kRowBytes,
+                pg + (int64_t)page_size * kRowBytes + off * kFp4ScaleSlot);
+}
+
 // One warp per raw row: RMSNorm of the 512 latent elements and RoPE of the 64 RoPE
 // elements in fp32 ("MLA" API page of HALOps, mla_attention: its normalise-and-rotate
 // step before the cache write, kv_norm_weight / kv_eps / positions / freqs_real), the row
@@ -204,7 +234,7 @@ __global__ void __launch_bounds__(128) kv_write_norm_rope_kernel(
   const uint16_t* x = raw + (int64_t)r * row_elems;
   const float* f = freqs + (int64_t)pos * 64;
   norm_rope_row(x, w, eps, f, row_elems, lane, srow[wi]);
-  write_row(srow[wi], lane, kv, layout, page, static_cast<int>(slot % page_size), page_size, page_bytes);
+  write_any_row(srow[wi], lane, kv, layout, page, static_cast<int>(slot % page_size), page_size, page_bytes);
 }
 
 // ----------------------------------------------------------------------------- gather
@@ -294,6 +324,9 @@ cudaError_t launch_kv_write(const uint16_t* rows, const int32_t* slots, int n, u
                             int64_t num_pages, int page_size, int64_t page_bytes, uint32_t* status,
                             cudaStream_t stream) {
   if (n <= 0) return cudaSuccess;
+  if (layout >= 3)
+    return launch_pdl(layout == 3 ? kv_write_fp4_kernel<3> : kv_write_fp4_kernel<4>, dim3((n + 7) / 8), dim3(256), 0,
+                      stream, rows, slots, n, kv, num_pages, page_size, page_bytes, status);
   return launch_pdl(kv_write_kernel, dim3((n + 3) / 4), dim3(128), 0, stream, rows, slots, n, kv, layout, num_pages,
                     page_size, page_bytes, status);
 }

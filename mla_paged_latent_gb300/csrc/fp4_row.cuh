@@ -63,24 +63,23 @@ __device__ __forceinline__ void fp4x8_to_bf16(uint32_t w, const Fp4Scale& s, uin
   }
 }
 
-// 6 * 2^e as fp32 (exact; +inf once it exceeds the fp32 range).
-__device__ __forceinline__ float pow2x6(int e) {
-  const int E = e + 2 + 127;  // 6 = 1.5 * 2^2
-  if (E >= 255) return __uint_as_float(0x7F800000u);
-  if (E <= 0) return 0.f;
-  return __uint_as_float((static_cast<uint32_t>(E) << 23) | 0x400000u);
+// The scale byte e + 127 of a group whose largest magnitude has the bf16 bits m (taken as integers, so that a NaN
+// counts as the largest): the smallest e with 6 * 2^e >= max(m, 1e-10), where 6 = 1.5 * 2^2; 254 for an infinity, 255
+// for a NaN.
+__device__ __forceinline__ uint32_t fp4_scale_byte(uint32_t m) {
+  const uint32_t e = (m >> 7) - ((m & 0x7Fu) > 0x40u ? 1u : 2u);  // negative below 2^-125: the lower bound takes it
+  const uint32_t f = static_cast<int>(e) < 92 ? 92u : e;          // 1e-10 = 1.718 * 2^-34: e = -35
+  return m < 0x7F80u ? f : (m == 0x7F80u ? 254u : 255u);
 }
-// Smallest e with 6 * 2^e >= a (a >= 1e-10), clamped to [-127, 127].
-__device__ __forceinline__ int fp4_group_exponent(float a) {
-  if (!(a <= 3.4028235e38f)) return 127;
-  int e = static_cast<int>((__float_as_uint(a) >> 23) & 0xFFu) - 127 - 2;
-  if (!(pow2x6(e) >= a)) ++e;  // a's mantissa is above 1.5
-  return e > 127 ? 127 : e;
-}
-// Two fp32 -> two e2m1 codes, to nearest even, saturating; `lo` in bits 0-3, `hi` in bits 4-7.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+// Eight fp32 -> eight e2m1 codes, to nearest even, saturating; element 0 in bits 0-3.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(const float (&v)[8]) {
   uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("{\n .reg .b8 a, b, c, d;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n"
+      " mov.b32 %0, {a, b, c, d};\n}\n"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
 

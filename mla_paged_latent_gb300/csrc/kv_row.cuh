@@ -45,33 +45,37 @@ __device__ __forceinline__ float pow2neg(int e) {
   return __uint_as_float(static_cast<uint32_t>(E) << 23);
 }
 
-// The 4-bit form of write_row: lane l holds elements [16 l, 16 l + 16) of the bf16 row x in v,
-// and `a` is the largest magnitude over its group (lanes 2g, 2g + 1). Codes are rounded to
-// nearest even after an exact division by the group's power of two. e2m1 has no NaN: a group
-// that holds one gets the scale byte 255 (NaN) and zero codes, so that it reads back as NaN.
-__device__ __forceinline__ void write_row_fp4(const uint16_t* x, const float (&v)[16], float a, int lane, int nope,
-                                              uint8_t* dst, uint8_t* slot) {
-  float nan = 0.f;
+// The 4-bit form of write_row: lane l holds elements [16 l, 16 l + 16) of the bf16 row in x0 and x1, and lanes 0-7 the
+// RoPE part's elements [8 l, 8 l + 8) in pe. A group is lanes 2g and 2g + 1. Codes are rounded to nearest even after an
+// exact product with a power of two (what that takes below bf16's range is far below half a code). e2m1 has no
+// NaN: a group that holds one gets the scale byte 255 (NaN) and zero codes, so that it reads back as NaN.
+__device__ __forceinline__ void write_row_fp4(uint4 x0, uint4 x1, uint4 pe, int lane, int nope, uint8_t* dst,
+                                              uint8_t* slot) {
+  const uint32_t h[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+  uint32_t m = 0;  // magnitudes compare as integers, NaN above infinity
 #pragma unroll
-  for (int k = 0; k < 16; ++k) nan = v[k] != v[k] ? 1.f : nan;
-  nan = fmaxf(nan, __shfl_xor_sync(0xffffffffu, nan, 1));
-  const int e = fp4_group_exponent(fmaxf(a, 1e-10f));
-  const uint32_t sbyte = nan != 0.f ? 255u : static_cast<uint32_t>(e + 127);
+  for (int k = 0; k < 8; ++k) m = __vmaxu2(m, h[k] & 0x7FFF7FFFu);
+  m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  const uint32_t sbyte = fp4_scale_byte(m >> 16 > (m & 0xFFFFu) ? m >> 16 : m & 0xFFFFu);
   if (lane * 16 < nope) {
-    const float sc = nan != 0.f ? 0.f : pow2neg(e);
+    // 2^-e as a bf16 pair: exponent field 254 - (e + 127); 2^-127, an infinity's, is subnormal
+    const uint32_t sc = (sbyte < 254u ? (254u - sbyte) << 7 : 0x40u) * 0x00010001u;
     uint32_t w[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      w[h] = 0;
+    for (int i = 0; i < 2; ++i) {
+      float v[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        w[h] |= f32x2_to_e2m1x2(v[8 * h + 2 * k] * sc, v[8 * h + 2 * k + 1] * sc) << (8 * k);
-      if (nan != 0.f) w[h] = 0;
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t p = mul_bf16x2(h[4 * i + k], sc);
+        v[2 * k] = __uint_as_float(p << 16);
+        v[2 * k + 1] = __uint_as_float(p & 0xFFFF0000u);
+      }
+      w[i] = sbyte == 255u ? 0u : f32x8_to_e2m1x8(v);
     }
     reinterpret_cast<uint2*>(dst)[lane] = make_uint2(w[0], w[1]);
   }
   // the 64 RoPE elements stay bf16, after the codes
-  if (lane < 8) reinterpret_cast<uint4*>(dst + nope / 2)[lane] = reinterpret_cast<const uint4*>(x + nope)[lane];
+  if (lane < 8) reinterpret_cast<uint4*>(dst + nope / 2)[lane] = pe;
   // scale bytes: group g's sits in lane 2g; lane k < 4 assembles groups 4k .. 4k + 3
   uint32_t word = 0;
 #pragma unroll
@@ -83,7 +87,7 @@ __device__ __forceinline__ void write_row_fp4(const uint16_t* x, const float (&v
 }
 
 // Write one bf16 row (generic pointer x, 16-byte aligned, row_elems values) into its
-// page slot; all 32 lanes of the warp take part ("MLA" API page of HALOps,
+// page slot (layouts of 8 and 16 bits); all 32 lanes of the warp take part ("MLA" API page of HALOps,
 // mla_attention: KV cache write of the RMSNorm'd row; kv_cache parameter for the layout).
 __device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* __restrict__ kv, int layout,
                                           int64_t page, int off, int page_size, int64_t page_bytes) {
@@ -97,8 +101,7 @@ __device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* 
   const int row_bytes = row_stored_bytes(layout);
   uint8_t* dst = kv + page * page_bytes + (int64_t)off * row_bytes;
   // lane l holds elements [16 l, 16 l + 16), loaded at once; NoPE group g is lanes 4g .. 4g+3
-  // of an fp8 row and lanes 2g, 2g + 1 of a 4-bit one (in the 512-wide DSV4 rows, lanes 28-31
-  // hold the RoPE part)
+  // (in the 512-wide DSV4 rows, lanes 28-31 hold the RoPE part)
   float v[16];
   {
     const uint4 a = reinterpret_cast<const uint4*>(x)[2 * lane];
@@ -115,11 +118,6 @@ __device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* 
 #pragma unroll
   for (int k = 0; k < 16; ++k) a = fmaxf(a, fabsf(v[k]));
   a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  if (layout >= 3) {
-    write_row_fp4(x, v, a, lane, nope, dst,
-                  kv + page * page_bytes + (int64_t)page_size * row_bytes + off * kFp4ScaleSlot);
-    return;
-  }
   a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
   a = fmaxf(a, 1e-10f);
   const int e = group_exponent(a);
@@ -159,6 +157,20 @@ __device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* 
     uint2* sp = reinterpret_cast<uint2*>(kv + page * page_bytes + (int64_t)page_size * row_bytes + off * 8);
     *sp = make_uint2(sbytes[0], sbytes[1]);
   }
+}
+
+// write_row for every layout.
+__device__ __forceinline__ void write_any_row(const uint16_t* x, int lane, uint8_t* __restrict__ kv, int layout,
+                                              int64_t page, int off, int page_size, int64_t page_bytes) {
+  if (layout < 3) {
+    write_row(x, lane, kv, layout, page, off, page_size, page_bytes);
+    return;
+  }
+  const int nope = row_nope(layout), row_bytes = row_stored_bytes(layout);
+  const uint4* src = reinterpret_cast<const uint4*>(x);
+  uint8_t* const pg = kv + page * page_bytes;
+  write_row_fp4(src[2 * lane], src[2 * lane + 1], src[nope / 8 + (lane & 7)], lane, nope, pg + (int64_t)off * row_bytes,
+                pg + (int64_t)page_size * row_bytes + off * kFp4ScaleSlot);
 }
 
 // RMSNorm of the 512 latent elements and RoPE of the 64 RoPE elements of one raw row x

@@ -27,8 +27,8 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     f32x2_to_bf16x2(v[6], v[7]));
 }
 
-// One warp per row. The first blocks take the KV rows (norm_rope_row + write_row, as the fused
-// write), the others the (token, head) query rows: 64 sixteen-byte chunks, two a lane, NoPE from
+// One warp per row. The first blocks take the KV rows (norm_rope_row + write_any_row, as the
+// fused write), the others the (token, head) query rows: 64 sixteen-byte chunks, two a lane, NoPE from
 // q_nope and (512-wide rows) RoPE from q_pe, normalised over all 512 elements when asked; the
 // 576-wide rows' RoPE part is one pair a lane, rotated as it comes. A row is read whole into
 // registers before any of it is written, so q may be prepared in place.
@@ -42,9 +42,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) qkv_norm_rope_kernel(const __g
   if (static_cast<int>(blockIdx.x) < P.kv_blocks) {
     const int r = blockIdx.x * kRowWarps + wi;
     if (r >= P.tokens) return;
-    const int64_t slot = P.slots[r];
+    const int slot = P.slots[r];
     if (slot < 0) return;
-    const int64_t page = slot / P.page_size;
+    const int page = slot / P.page_size;
     const int pos = P.positions[r];
     const uint32_t bad = (page >= P.num_pages ? 4u : 0u) | (pos < 0 || pos >= P.max_pos ? 8u : 0u);
     if (bad != 0u) {  // reported, not written
@@ -53,13 +53,14 @@ __global__ void __launch_bounds__(kRowWarps * 32) qkv_norm_rope_kernel(const __g
     }
     norm_rope_row(P.kv_raw + (int64_t)r * P.kv_row_stride, P.kv_weight, P.kv_eps, P.freqs + (int64_t)pos * 64, WIDTH,
                   lane, srow[wi]);
-    write_row(srow[wi], lane, P.kv, P.layout, page, static_cast<int>(slot % P.page_size), P.page_size, P.page_bytes);
+    write_any_row(srow[wi], lane, P.kv, P.layout, page, slot - page * P.page_size, P.page_size, P.page_bytes);
     return;
   }
-  const int64_t row = (int64_t)(blockIdx.x - P.kv_blocks) * kRowWarps + wi;
-  if (row >= (int64_t)P.tokens * P.heads) return;
-  const int t = static_cast<int>(row / P.heads);
-  const int n = static_cast<int>(row - (int64_t)t * P.heads);
+  // (the entry point keeps tokens * heads below 2^31, and a block's rows end at most 7 past it)
+  const uint32_t row = (blockIdx.x - P.kv_blocks) * kRowWarps + wi;
+  if (row >= static_cast<uint32_t>(P.tokens) * P.heads) return;
+  const int t = static_cast<int>(row / static_cast<uint32_t>(P.heads));
+  const int n = static_cast<int>(row) - t * P.heads;
   const int pos = P.positions[t];
   if (pos < 0 || pos >= P.max_pos) {  // left as it was; reported unless it is padding
     if (lane == 0 && P.status != nullptr && (pos >= 0 || P.slots[t] >= 0)) atomicOr(P.status, 8u);
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) qkv_norm_rope_kernel(const __g
     o0 = pack8(a);
     o1 = pack8(b);
   }
-  uint16_t* q = P.q_out + row * WIDTH;
+  uint16_t* q = P.q_out + (int64_t)row * WIDTH;
   reinterpret_cast<uint4*>(q)[lane] = o0;
   reinterpret_cast<uint4*>(q)[32 + lane] = o1;
   if (WIDTH == 576) {
@@ -145,10 +146,10 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_read_kernel(const uint8_t* 
   const int r = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (r >= n) return;
-  const int64_t slot = slots[r];
+  const int slot = slots[r];
   if (slot < 0) return;
-  const int64_t page = slot / page_size;
-  const int off = static_cast<int>(slot % page_size);
+  const int page = slot / page_size;
+  const int off = slot - page * page_size;
   if (page >= num_pages) {  // reported, not read
     if (lane == 0 && status != nullptr) atomicOr(status, 4u);
     return;
