@@ -12,7 +12,8 @@ namespace {
 
 // ----------------------------------------------------------------------------- combine
 // One warp per query row of a request that the plan split into >= 2 pieces (the merge
-// itself is merge_row in combine_row.cuh).
+// itself is merge_row in combine_row.cuh), or with few rows WARPS = 4 of them, a quarter of the row each.
+template <int WARPS>
 __global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ part_out,
                                                       const float* __restrict__ part_lse,
                                                       const int32_t* __restrict__ num_splits, int R, int heads,
@@ -25,13 +26,15 @@ __global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ 
   const int s0 = num_splits[b];
   const int ns = num_splits[b + 1] - s0;
   if (ns < 2) return;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int wi = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int row = wi / WARPS, k0 = wi % WARPS;
   if (row >= R) return;
   const int lane = threadIdx.x & 31;
   const int64_t orow = (int64_t)b * R + row;
-  float acc[16];
-  const float lse_tot = merge_row(part_out, part_lse, s0, ns, R, row, lane, sink, row % heads, acc);
-  store_row_bf16(out + orow * 512, lane, acc);
+  float acc[16 / WARPS];
+  const float lse_tot = merge_row(part_out, part_lse, s0, ns, R, row, lane, sink, row % heads, acc, k0);
+  store_row_bf16(out + orow * 512, lane, acc, k0);
+  if (k0 != 0) return;
   if (lane == 0) lse[orow] = lse_tot;
   if (max_logits != nullptr) {  // the largest scaled score: the largest over the splits
     float m = -INFINITY;
@@ -296,11 +299,14 @@ cudaError_t launch_combine(const float* part_out, const float* part_lse, const i
                            int rows_per_req, int heads, const float* sink, uint16_t* out, float* lse,
                            const float* part_max, float* max_logits, cudaStream_t stream) {
   if (batch <= 0 || rows_per_req <= 0) return cudaSuccess;
-  // one warp per row, four rows per 128-thread block (96 registers a thread: five blocks
-  // per SM, against two of 256 threads)
-  dim3 grid((rows_per_req + 3) / 4, batch);
-  return launch_pdl(combine_kernel, grid, dim3(128), 0, stream, part_out, part_lse, num_splits, rows_per_req, heads,
-                    sink, out, lse, part_max, max_logits);
+  // blocks of 128 threads (96 registers a thread: five blocks per SM, against two of 256 threads)
+  // Four warps a row where rows are few: a few requests split many ways are bound by the loads that a warp keeps in
+  // flight. Measured, us, with the launch's 5: 128 rows of 76 partials 17 (a warp a row: 36), 256 of 38 15 (23), 384 of
+  // 25 13 (17), 512 of 19 15 (15), 512 of 5 12 (11).
+  const bool few = static_cast<int64_t>(rows_per_req) * batch <= 384;
+  const dim3 grid(few ? rows_per_req : (rows_per_req + 3) / 4, batch);
+  return launch_pdl(few ? combine_kernel<4> : combine_kernel<1>, grid, dim3(128), 0, stream, part_out, part_lse,
+                    num_splits, rows_per_req, heads, sink, out, lse, part_max, max_logits);
 }
 
 cudaError_t launch_swa_plan(const int32_t* kv_indices, const int32_t* topk_lengths, int num_tokens, int topk,

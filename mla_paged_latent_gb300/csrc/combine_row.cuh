@@ -12,18 +12,21 @@ namespace mla {
 // tduncan/Nvidia-Optimization-Stack-VLLM", Chunked Prefill: merge_attn_states; an empty
 // partial has lse = -inf and weight 0), then the sink factor 1 / (1 + e^(sink - lse))
 // ("MLA" API page of HALOps, mla_output_proj: the split-KV LSE combine receives attn_sink).
-// acc[4 k + i] receives element 4 (32 k + lane) + i; the return value is lse (-inf, with
-// acc = 0, when every partial is empty).
+// acc[4 k + i] receives element 4 (32 (k0 + k) + lane) + i: the whole row (N = 16), or a quarter
+// of it (N = 4, k0 = 0 .. 3); the return value is lse (-inf, with acc = 0, when every partial is
+// empty).
+template <int N>
 __device__ __forceinline__ float merge_row(const float* __restrict__ part_out, const float* __restrict__ part_lse,
                                            int s0, int ns, int R, int row, int lane, const float* __restrict__ sink,
-                                           int head, float (&acc)[16]) {
+                                           int head, float (&acc)[N], int k0 = 0) {
+  constexpr int K = N / 4;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
   float lse_tot;
   if (ns <= 4) {
     // up to 4 splits (the common case): every load first, in one round trip to memory
     float ls[4];
-    float4 v[4][4];
+    float4 v[4][K];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       ls[s] = -INFINITY;
@@ -31,7 +34,7 @@ __device__ __forceinline__ float merge_row(const float* __restrict__ part_out, c
         ls[s] = part_lse[(int64_t)(s0 + s) * R + row];
         const float4* src = reinterpret_cast<const float4*>(part_out + ((int64_t)(s0 + s) * R + row) * 512);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[s][k] = src[k * 32 + lane];
+        for (int k = 0; k < K; ++k) v[s][k] = src[(k0 + k) * 32 + lane];
       }
     }
     const float mx = fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3]));
@@ -46,7 +49,7 @@ __device__ __forceinline__ float merge_row(const float* __restrict__ part_out, c
       if (s >= ns || ls[s] == -INFINITY) continue;
       const float w = expf(ls[s] - lse_tot);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < K; ++k) {
         acc[4 * k + 0] += w * v[s][k].x;
         acc[4 * k + 1] += w * v[s][k].y;
         acc[4 * k + 2] += w * v[s][k].z;
@@ -64,35 +67,52 @@ __device__ __forceinline__ float merge_row(const float* __restrict__ part_out, c
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
     lse_tot = mx + logf(tot);
-    for (int s = 0; s < ns; ++s) {
-      const float ls = part_lse[(int64_t)(s0 + s) * R + row];
-      if (ls == -INFINITY) continue;
-      const float w = expf(ls - lse_tot);
-      const float4* src = reinterpret_cast<const float4*>(part_out + ((int64_t)(s0 + s) * R + row) * 512);
+    // Weights 32 splits at a time, a lane each; then the splits in order, U of them loaded at once: each element's sum
+    // is the same as one by one, without a round trip to memory for each split.
+    constexpr int U = K == 1 ? 16 : 2;
+    for (int base = 0; base < ns; base += 32) {
+      const float ls = base + lane < ns ? part_lse[(int64_t)(s0 + base + lane) * R + row] : -INFINITY;
+      const float wl = expf(ls - lse_tot);
+      const unsigned on = __ballot_sync(0xffffffffu, ls != -INFINITY);
+      for (int u = 0; u < 32 && base + u < ns; u += U) {
+        float4 v[U][K];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 v = src[k * 32 + lane];
-        acc[4 * k + 0] += w * v.x;
-        acc[4 * k + 1] += w * v.y;
-        acc[4 * k + 2] += w * v.z;
-        acc[4 * k + 3] += w * v.w;
+        for (int i = 0; i < U; ++i) {
+          if (!((on >> (u + i)) & 1u)) continue;
+          const float4* src = reinterpret_cast<const float4*>(part_out + ((int64_t)(s0 + base + u + i) * R + row) * 512);
+#pragma unroll
+          for (int k = 0; k < K; ++k) v[i][k] = src[(k0 + k) * 32 + lane];
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+          const float w = __shfl_sync(0xffffffffu, wl, u + i);
+          if (!((on >> (u + i)) & 1u)) continue;
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            acc[4 * k + 0] += w * v[i][k].x;
+            acc[4 * k + 1] += w * v[i][k].y;
+            acc[4 * k + 2] += w * v[i][k].z;
+            acc[4 * k + 3] += w * v[i][k].w;
+          }
+        }
       }
     }
   }
   float f = 1.f;
   if (sink != nullptr) f = 1.f / (1.f + expf(sink[head] - lse_tot));
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] *= f;
+  for (int i = 0; i < N; ++i) acc[i] *= f;
   return lse_tot;
 }
 
-// Round a merged row to bf16 and store it (dst = the row's 512 elements), rounding acc in place.
-__device__ __forceinline__ void store_row_bf16(uint16_t* dst, int lane, float (&acc)[16]) {
+// Round a merged row (or quarter k0 of it) to bf16 and store it (dst = the row's 512 elements), rounding acc in place.
+template <int N>
+__device__ __forceinline__ void store_row_bf16(uint16_t* dst, int lane, float (&acc)[N], int k0 = 0) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < N / 4; ++k) {
     const uint32_t lo = f32x2_to_bf16x2(acc[4 * k], acc[4 * k + 1]);
     const uint32_t hi = f32x2_to_bf16x2(acc[4 * k + 2], acc[4 * k + 3]);
-    *reinterpret_cast<uint2*>(dst + (k * 32 + lane) * 4) = make_uint2(lo, hi);
+    *reinterpret_cast<uint2*>(dst + ((k0 + k) * 32 + lane) * 4) = make_uint2(lo, hi);
     acc[4 * k] = __uint_as_float(lo << 16);
     acc[4 * k + 1] = __uint_as_float(lo & 0xFFFF0000u);
     acc[4 * k + 2] = __uint_as_float(hi << 16);

@@ -739,3 +739,37 @@ def test_sparse_prefill_over_a_quantised_cache():
     for t in range(T):
         ref = attend(bf16_f64(q[t]), held[idx[t][idx[t] >= 0]], float(np.float32(0.05)))
         assert_decode(bf16_to_f64(out)[t], lse[t].cpu().numpy().astype(np.float64), ref, f"token {t}")
+
+
+@pytest.mark.parametrize("rows,splits", [(16, 5), (16, 16), (20, 33), (128, 77), (96, 2), (400, 21)])
+def test_combine_of_many_splits(rows, splits):
+    """Partials merged in 64 bits: few rows and many, counts of splits on both sides of a group of loads and of a
+    warp, empty partials among them (their values not numbers), a row with nothing, a request left alone."""
+    rng = np.random.default_rng(rows + splits)
+    B = 2
+    ns = np.array([0, splits, splits + 1], np.int32)      # the second request is not split: left as it was
+    po = rng.standard_normal((splits + 1, rows, 512)).astype(np.float32)
+    pl = (3 * rng.standard_normal((splits + 1, rows))).astype(np.float32)
+    empty = rng.random((splits + 1, rows)) < 0.2
+    empty[:, 3] = True
+    pl[empty], po[empty] = -np.inf, np.nan
+    sink = rng.standard_normal(rows).astype(np.float32)
+    out = torch.full((B * rows, 512), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((B * rows,), 7.0, device="cuda")
+    mla.mla_combine(_cuda(po), _cuda(pl), _cuda(ns), rows, rows, out, lse, sink=_cuda(sink))
+    torch.cuda.synchronize()
+    assert bool((out[rows:] == 7).all()) and bool((lse[rows:] == 7).all())
+    got, glse = bf16_to_f64(out)[:rows], lse.cpu().numpy().astype(np.float64)[:rows]
+    for r in range(rows):
+        on = ~empty[:splits, r]
+        if not on.any():
+            assert np.isneginf(glse[r]) and np.all(got[r] == 0)
+            continue
+        l, o = pl[:splits, r][on].astype(np.float64), po[:splits, r][on].astype(np.float64)
+        ref_lse = np.log(np.exp(l).sum())
+        w = np.exp(l - ref_lse) / (1 + np.exp(float(sink[r]) - ref_lse))
+        # fp32 weights: the exponentials and the logarithm (2 units each), their arguments (|lse| below 16: 2^-20)
+        # and the sums of up to 77 terms (77 * 2^-24 of their magnitudes); then one rounding to bf16
+        mean = w @ np.abs(o)
+        assert abs(glse[r] - ref_lse) <= 2.0 ** -19
+        assert np.all(np.abs(got[r] - w @ o) <= (2.0 ** -17) * mean + 2.0 ** -8 * np.abs(w @ o))
