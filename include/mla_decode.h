@@ -50,7 +50,9 @@
  *  A 4-bit NoPE value is e2m1(code) * 2^(scale_byte - 127); e2m1 = {0, 0.5, 1, 1.5, 2, 3, 4, 6}
  *  for codes 0-7, and their negatives for 8-15; scale byte 255 is NaN (OCP MX formats).
  *  Reading 4-bit rows, the decode passes the softmax weights to the value product as one
- *  bf16 each (as it does for bf16 rows; the fp8 layouts pass a pair).
+ *  bf16 each (as it does for bf16 rows; the fp8 layouts pass a pair). A NaN in a row makes NaN
+ *  of every query row of its request that is computed with it, those of draft tokens before it
+ *  (causal, weight zero) too. A row of a page out of range is left out of the sums.
  */
 #ifndef MLA_DECODE_H_
 #define MLA_DECODE_H_
@@ -158,7 +160,7 @@ int mla_decode_plan(const int32_t* cache_seqlens, int32_t batch, int32_t q_token
  *  q            device bf16 [T = batch*q_tokens_per_req, num_heads, Dqk]
  *               (Dqk = 576, or 512 for the 448-NoPE layouts), 16-byte aligned.
  *  kv_cache     device uint8 [num_pages, page_bytes(layout, page_size)], 16-B aligned (4-bit
- *               layouts: 32-B aligned).
+ *               layouts: 32-B aligned, pages of at most 2^22 rows, fewer than 2^32 rows in all).
  *  block_table  device int32 [batch, max_pages]: page of each page-sized block.
  *  cache_seqlens device int32 [batch]: L_b, context rows including the query
  *               tokens' own new rows (seq_len = context_len + query_len,
@@ -345,7 +347,8 @@ int mla_combine_inv_rope(const float* part_out, const float* part_lse, const int
  * HALOps, mla_attention: its cache-write step and kv_cache parameter).
  *  rows   device bf16 [n, row_elems], already RMSNorm'd (and RoPE'd);
  *         row_elems = 576 (layouts 0, 2, 4) or 512 (layouts 1, 3: 448 NoPE | 64 RoPE).
- *  slots  device int32 [n]: page * page_size + offset; negative slots are skipped.
+ *  slots  device int32 [n]: page * page_size + offset; negative slots are skipped, the others
+ *         must be distinct.
  * Layout 0 copies the bits. fp8 layouts: per 64-element NoPE group,
  * amax = max(max|x|, 1e-10f), e = the smallest integer with 448 * 2^e >= amax,
  * scale byte = e + 127, code = e4m3 round-to-nearest-even, saturating, of
@@ -418,7 +421,7 @@ int mla_kv_write_norm_rope(const void* raw, const int32_t* slots, const int32_t*
  *          and is reported, unless slot and position are both negative (padding).
  *  q_out   device bf16 [num_tokens, num_heads, row_elems]. It may be the queries' own memory row for
  *          row (q_nope == q_out, q_pe == q_out + its offset, strides those of q_out); any other
- *          overlap with an input is refused.
+ *          overlap with an input, or of q_out or an input with kv_cache, is refused.
  * Strides are multiples of 8 elements >= 0 and every pointer is 16-byte aligned (status, slots
  * and positions 4-byte). status (device uint32 or NULL) is OR-ed with MLA_STATUS_BAD_SLOT and
  * MLA_STATUS_BAD_POSITION.

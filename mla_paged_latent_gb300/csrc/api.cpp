@@ -72,6 +72,16 @@ int layout_geometry(int layout, int page_size, int64_t* row_bytes, int64_t* page
   }
 }
 
+// Byte range [lo, hi) that rows by strides (elements of 2 bytes) cover.
+struct ByteRange {
+  uintptr_t lo, hi;
+};
+ByteRange strided_range(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t elems) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + 2 * static_cast<uintptr_t>((n0 - 1) * s0 + (n1 - 1) * s1 + elems)};
+}
+bool overlap(const ByteRange& a, const ByteRange& b) { return a.lo < b.hi && b.lo < a.hi; }
+
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
@@ -237,6 +247,9 @@ int decode_impl(const void* q, const void* kv_cache, mla_kv_layout layout, int64
     return fail(MLA_ERR_INVALID_ARG, "mla_decode: a 4-bit kv_cache must be 32-byte aligned");
   if (layout >= MLA_KV_FP4_448_UE8M0 && num_pages >= ((1ll << 32) - 1) / page_size)
     return fail(MLA_ERR_UNSUPPORTED, "mla_decode: more than 2^32 cache slots");
+  // (a row's way to its scales is kept in 31 bits)
+  if (layout >= MLA_KV_FP4_448_UE8M0 && page_size > (1 << 22))
+    return fail(MLA_ERR_UNSUPPORTED, "mla_decode: page_size %d of a 4-bit cache is above 2^22", page_size);
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(MLA_ERR_INVALID_ARG, "mla_decode: workspace must be 256-byte aligned");
   const size_t need = workspace_bytes_for(total_splits, R);
@@ -564,16 +577,6 @@ int mla_kv_write_norm_rope(const void* raw, const int32_t* slots, const int32_t*
   return MLA_OK;
 }
 
-// Byte range [lo, hi) that rows by strides (elements of 2 bytes) cover.
-struct ByteRange {
-  uintptr_t lo, hi;
-};
-static ByteRange strided_range(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t elems) {
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return {lo, lo + 2 * static_cast<uintptr_t>((n0 - 1) * s0 + (n1 - 1) * s1 + elems)};
-}
-static bool overlap(const ByteRange& a, const ByteRange& b) { return a.lo < b.hi && b.lo < a.hi; }
-
 int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
                       int64_t q_pe_token_stride, int64_t q_pe_head_stride, int32_t q_norm, const void* q_norm_weight,
                       float q_eps, const void* kv_raw, int64_t kv_row_stride, const int32_t* slots,
@@ -604,6 +607,10 @@ int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q
     if (s < 0 || s % 8 != 0 || s >= (1ll << 40))
       return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: stride %lld must be a multiple of 8 elements >= 0",
                   static_cast<long long>(s));
+  for (int i = 0; i < 5; ++i)  // (so that the ranges below fit 64 bits)
+    if (strides[i] > (1ll << 46) / ((i == 1 || i == 3) ? num_heads : num_tokens))
+      return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: stride %lld is past any memory",
+                  static_cast<long long>(strides[i]));
   if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(q_norm_weight) || !aligned16(kv_raw) ||
       !aligned16(kv_norm_weight) || !aligned16(freqs) || !aligned16(q_out) || !aligned16(kv_cache))
     return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: pointers must be 16-byte aligned");
@@ -618,6 +625,12 @@ int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q
       (!pe_here && overlap(out, strided_range(q_pe, T, q_pe_token_stride, N, q_pe_head_stride, 64))) ||
       overlap(out, strided_range(kv_raw, T, kv_row_stride, 1, 0, dqk)))
     return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: q_out overlaps an input other than row for row");
+  const uintptr_t cache = reinterpret_cast<uintptr_t>(kv_cache);
+  const ByteRange kv = {cache, cache + static_cast<uintptr_t>(num_pages) * static_cast<uintptr_t>(pb)};
+  if (overlap(kv, out) || overlap(kv, strided_range(q_nope, T, q_nope_token_stride, N, q_nope_head_stride, nope)) ||
+      overlap(kv, strided_range(q_pe, T, q_pe_token_stride, N, q_pe_head_stride, 64)) ||
+      overlap(kv, strided_range(kv_raw, T, kv_row_stride, 1, 0, dqk)))
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: kv_cache overlaps the queries or the rows");
   mla::QkvParams p;
   std::memset(&p, 0, sizeof p);
   p.q_nope = static_cast<const uint16_t*>(q_nope);
@@ -664,6 +677,10 @@ int mla_kv_read(const void* kv_cache, mla_kv_layout layout, int64_t num_pages, i
   if (num_pages < 1) return fail(MLA_ERR_INVALID_ARG, "mla_kv_read: num_pages < 1");
   if (!aligned16(rows) || !aligned16(kv_cache))
     return fail(MLA_ERR_INVALID_ARG, "mla_kv_read: rows and kv_cache must be 16-byte aligned");
+  const uintptr_t cache = reinterpret_cast<uintptr_t>(kv_cache);
+  if (overlap({cache, cache + static_cast<uintptr_t>(num_pages) * static_cast<uintptr_t>(pb)},
+              strided_range(rows, n, dqk, 1, 0, dqk)))
+    return fail(MLA_ERR_INVALID_ARG, "mla_kv_read: rows overlaps kv_cache");
   cudaError_t e = mla::launch_kv_read(static_cast<const uint8_t*>(kv_cache), static_cast<int>(layout), num_pages,
                                       page_size, pb, slots, n, static_cast<uint16_t*>(rows), status,
                                       static_cast<cudaStream_t>(stream));

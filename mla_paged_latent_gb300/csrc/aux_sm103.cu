@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(256) kv_write_fp4_kernel(const uint16_t* __res
   }
   uint8_t* const pg = kv + page * page_bytes;
   write_row_fp4(x0, x1, pe, lane, kNope, pg + (int64_t)off * kRowBytes,
-                pg + (int64_t)page_size * kRowBytes + off * kFp4ScaleSlot);
+                pg + (int64_t)page_size * kRowBytes + (int64_t)off * kFp4ScaleSlot);
 }
 
 // One warp per raw row: RMSNorm of the 512 latent elements and RoPE of the 64 RoPE
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(128) kv_gather_kernel(const uint8_t* __restric
   const int nope = row_nope(layout);
   const int row_bytes = row_stored_bytes(layout);
   const uint8_t* src = kv + page * page_bytes + (int64_t)off * row_bytes;
-  const uint8_t* sc = kv + page * page_bytes + (int64_t)page_size * row_bytes + off * row_scale_slot(layout);
+  const uint8_t* sc = kv + page * page_bytes + (int64_t)page_size * row_bytes + (int64_t)off * row_scale_slot(layout);
   if (layout >= 3) {
     for (int i = lane; i < nope / 8; i += 32) {
       uint32_t o4[4];

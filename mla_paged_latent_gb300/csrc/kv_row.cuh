@@ -170,7 +170,7 @@ __device__ __forceinline__ void write_any_row(const uint16_t* x, int lane, uint8
   const uint4* src = reinterpret_cast<const uint4*>(x);
   uint8_t* const pg = kv + page * page_bytes;
   write_row_fp4(src[2 * lane], src[2 * lane + 1], src[nope / 8 + (lane & 7)], lane, nope, pg + (int64_t)off * row_bytes,
-                pg + (int64_t)page_size * row_bytes + off * kFp4ScaleSlot);
+                pg + (int64_t)page_size * row_bytes + (int64_t)off * kFp4ScaleSlot);
 }
 
 // RMSNorm of the 512 latent elements and RoPE of the 64 RoPE elements of one raw row x

@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_read_kernel(const uint8_t* 
     return;
   }
   const uint8_t* src = kv + page * page_bytes + (int64_t)off * kRowBytes;
-  const uint8_t* sc = kv + page * page_bytes + (int64_t)page_size * kRowBytes + off * row_scale_slot(LAYOUT);
+  const uint8_t* sc = kv + page * page_bytes + (int64_t)page_size * kRowBytes + (int64_t)off * row_scale_slot(LAYOUT);
   uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)r * kWidth);
   uint4 pe = make_uint4(0, 0, 0, 0);
   if (lane < 8) pe = reinterpret_cast<const uint4*>(src + kCodeBytes)[lane];

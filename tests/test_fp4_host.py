@@ -258,3 +258,51 @@ def test_decode_refuses_as_other_layouts(lib):
         assert rc(layout, sq=2, topk=8, idx=FAKE) == -2
         assert rc(layout, topk=8) == -1
     assert rc(5) == -1
+
+
+def test_decode_refuses_what_a_4_bit_cache_cannot_be(lib):
+    """Its alignment, its count of slots, its page size; a cache of another layout may be so."""
+    def rc(layout, kv=FAKE, pages=4, ps=64):
+        return lib.mla_decode(FAKE, kv, layout, pages, ps, FAKE, 2, FAKE, 2, 1, 128, 0.1, None, None, 0, 0, FAKE, FAKE,
+                              1, 2, FAKE, 100, FAKE, FAKE, 0, None)   # (a workspace of 100 bytes: -3 when all else is right)
+
+    for layout in FP4:
+        assert rc(layout) == -3
+        assert rc(layout, kv=ctypes.c_void_p(0x100010)) == -1 and b"32-byte" in lib.mla_last_error()
+        assert rc(layout, pages=1 << 26) == -2 and b"2^32" in lib.mla_last_error()
+        assert rc(layout, pages=(1 << 26) - 2) == -3
+        assert rc(layout, ps=1 << 23) == -2 and rc(layout, ps=1 << 22) == -3
+    assert rc(2, kv=ctypes.c_void_p(0x100010)) == -3 and rc(2, pages=1 << 26) == -3 and rc(2, ps=1 << 23) == -3
+
+
+def test_overlaps_with_the_cache_are_refused(lib):
+    """Rows that are read or written inside the cache, and strides that no memory holds."""
+    at = lambda k, o=0: ctypes.c_void_p(0x1000000 * k + o)  # noqa: E731
+    end = mla.mla_page_bytes(4, 64) * 4
+
+    def qkv(qn=at(1), qnt=1024, qp=at(2), kv_raw=at(3), kvs=576, out=at(8), T=3):
+        return lib.mla_qkv_norm_rope(qn, qnt, 512, qp, 128, 64, 0, None, 0.0, kv_raw, kvs, at(4), at(5), at(6), 1e-6, at(7),
+                                     100, T, 2, out, at(9), 4, 4, 64, None, None)
+
+    for name in ("qn", "qp", "kv_raw", "out"):
+        assert qkv(**{name: at(9, end - 16)}) == -1 and b"kv_cache overlaps" in lib.mla_last_error(), name
+    assert qkv(qn=at(9, -1024)) == -1
+    for name in ("qnt", "kvs"):
+        assert qkv(T=1 << 20, **{name: 1 << 39}) == -1 and b"past any memory" in lib.mla_last_error(), name
+    assert lib.mla_kv_read(at(9), 4, 4, 64, at(1), 3, at(9, end - 16), None, None) == -1
+    assert lib.mla_kv_read(at(9), 4, 4, 64, at(1), 3, at(9, -1024), None, None) == -1
+    assert b"overlaps" in lib.mla_last_error()
+
+
+def test_binding_wants_one_device(monkeypatch):
+    """Tensors of another device than the others', or than the current one, are refused before the call."""
+    class On:
+        def __init__(self, d):
+            self.device, self.get_device = f"cuda:{d}", lambda: d
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(mla, "_torch_c", None)
+    mla._require_one_device(On(0), None, On(0))
+    for tensors in ((On(0), On(1)), (On(1), On(1)), (On(1), None, On(0))):
+        with pytest.raises(ValueError):
+            mla._require_one_device(*tensors)
