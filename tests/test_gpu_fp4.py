@@ -345,7 +345,8 @@ def test_decode_topk(layout, topk, heads, sq, splits):
 
 
 @pytest.mark.parametrize("layout", FP4)
-@pytest.mark.parametrize("window,ps,heads", [(1, 8, 64), (96, 64, 64), (128, 128, 20), (40, 32, 128)])
+@pytest.mark.parametrize("window,ps,heads", [(1, 8, 64), (96, 64, 64), (128, 128, 20), (40, 32, 128),
+                                             (300, 256, 128)])
 def test_decode_windows(layout, window, ps, heads):
     w = workloads.generate(workloads.dsv4(batch=9, seqlens=(300,) * 9, len_dist="fixed", heads=heads, layout=layout,
                                           page_size=ps, new_rows=False))
@@ -660,6 +661,80 @@ def test_pairs_nan_group_and_bad_page(layout):
         mla.mla_read_status(d.ws)
     out, lse = d.run(write=False)
     assert_decode(out, lse, decode(w, w.kv_cache, dense_slots(w)), "after a timed-out call")
+
+
+@pytest.mark.parametrize("layout", FP4)
+@pytest.mark.parametrize("ps,heads,splits", [(8, 128, 2), (1024, 128, 1), (4096, 64, 3), (32, 384, 1), (64, 4096, 1)])
+def test_decode_page_sizes_and_head_counts(layout, ps, heads, splits):
+    """Pages smaller and much larger than a tile, many groups of query rows, and requests that share pages."""
+    w = workloads.generate(workloads.dsv4(batch=3, seqlens=(3000, 777, 3000) if heads < 4096 else (130, 1, 70),
+                                          len_dist="fixed", heads=heads, layout=layout, page_size=ps, new_rows=False,
+                                          tail_fill="nan", seed=ps))
+    w.block_table[2] = w.block_table[0]
+    _, out, lse = _run(w, min_splits=splits)
+    assert_decode(out, lse, decode(w, w.kv_cache, dense_slots(w)), f"pages of {ps}, {heads} heads")
+
+
+@pytest.mark.parametrize("layout,heads", [(3, 64), (4, 128)])
+def test_step_captured_on_a_side_stream(layout, heads):
+    """A decode step captured once (queries and rows prepared, the decode, the rows read back) on a stream of its own,
+    replayed with other queries, rows, positions and slots; the second replay finds the first one's rows."""
+    rng = np.random.default_rng(210 + layout)
+    ps, B, max_pos = 16, 4, 300
+    width = workloads._DQK[layout]
+    table = rng.permutation(64)[:B * 16].reshape(B, 16).astype(np.int32)
+    ctx = np.array([0, 17, 120, 47])
+    slot_of = lambda b, j: table[b, j // ps].astype(np.int64) * ps + j % ps  # noqa: E731
+    held = np.zeros((64, workloads.page_bytes(layout, ps)), np.uint8)
+    for b in range(B):
+        j = np.arange(ctx[b])
+        held = oracle.kv_write(_bits(rng.standard_normal((ctx[b], width))), slot_of(b, j).astype(np.int32), held, layout, ps)
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        kv, freqs, gain = _cuda(held), _cuda(_table(max_pos)), torch.ones(512, dtype=torch.bfloat16, device="cuda")
+        q = torch.zeros(B, heads, width, dtype=torch.bfloat16, device="cuda")
+        prepared, raw = torch.empty_like(q), torch.zeros(B, width, dtype=torch.bfloat16, device="cuda")
+        slots, pos, lens = (torch.zeros(B, dtype=torch.int32, device="cuda") for _ in range(3))
+        bt, st = _cuda(table), _status()
+        plan = mla.mla_decode_plan(ctx + 3, 1, heads)  # each request has as many 64-row blocks in every step
+        ws, sched, ns = mla.alloc_workspace(plan.workspace_bytes), _cuda(plan.sched), _cuda(plan.num_splits)
+        out = torch.empty(B, heads, 512, dtype=torch.bfloat16, device="cuda")
+        lse, back = torch.empty(B, heads, device="cuda"), torch.empty_like(raw)
+
+        def step():
+            mla.mla_qkv_norm_rope(q[..., :width - 64], q[..., width - 64:], raw, slots, pos, gain, 1e-6, freqs, prepared,
+                                  kv, layout, ps, q_eps=1e-6, status=st)
+            mla.mla_decode(prepared, kv, layout, ps, bt, lens, 1, 0.07, sched, ns, plan.num_partitions, plan.total_splits,
+                           ws, out, lse)
+            mla.mla_kv_read(kv, layout, ps, slots, back, status=st)
+
+        def fill(ctx):
+            q.copy_(bf16_tensor(_bits(rng.standard_normal((B, heads, width)))))
+            raw.copy_(bf16_tensor(_bits(rng.standard_normal((B, width)))))
+            slots.copy_(_cuda(np.array([slot_of(b, ctx[b]) for b in range(B)]).astype(np.int32)))
+            pos.copy_(_cuda(ctx.astype(np.int32)))
+            lens.copy_(_cuda((ctx + 1).astype(np.int32)))
+
+        fill(ctx)
+        step()                                        # the first step, eager
+    stream.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=stream):
+        step()
+    for _ in range(2):
+        ctx = ctx + 1
+        with torch.cuda.stream(stream):
+            fill(ctx)
+            g.replay()
+        stream.synchronize()
+        assert int(st.item()) == 0
+        bytes_now, q64 = kv.cpu().numpy(), bf16_f64(_bits_of(prepared))
+        got, glse = bf16_to_f64(out), lse.cpu().numpy().astype(np.float64)
+        for b in range(B):
+            k = rows_of(bytes_now, layout, ps, slot_of(b, np.arange(ctx[b] + 1)))
+            assert_decode(got[b], glse[b], attend(q64[b], k, float(np.float32(0.07))), f"request {b}")
+            assert np.array_equal(bf16_to_f64(back[b]), k[-1])
+            assert k[-1].any()
 
 
 # ----------------------------------------------------------------------------- a step as a whole
