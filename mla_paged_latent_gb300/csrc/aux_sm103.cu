@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(256) kv_write_fp4_kernel(const uint16_t* __res
   const uint4 x0 = x[2 * lane], x1 = x[2 * lane + 1], pe = x[kNope / 8 + (lane & 7)];
   const int slot = slots[r];
   if (slot < 0) return;
-  const int page = slot / page_size;
-  const int off = slot - page * page_size;
+  const int page = slot >> (31 - __clz(page_size));  // (a power of two)
+  const int off = slot & (page_size - 1);
   if (page >= num_pages) {  // reported, not written
     if (lane == 0 && status != nullptr) atomicOr(status, 4u);
     return;

@@ -76,14 +76,8 @@ __device__ __forceinline__ void write_row_fp4(uint4 x0, uint4 x1, uint4 pe, int 
   }
   // the 64 RoPE elements stay bf16, after the codes
   if (lane < 8) reinterpret_cast<uint4*>(dst + nope / 2)[lane] = pe;
-  // scale bytes: group g's sits in lane 2g; lane k < 4 assembles groups 4k .. 4k + 3
-  uint32_t word = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t b = __shfl_sync(0xffffffffu, sbyte, ((lane & 3) * 8 + 2 * k) & 31);
-    if ((lane & 3) * 4 + k < nope / kFp4Group) word |= b << (8 * k);
-  }
-  if (lane < 4) reinterpret_cast<uint32_t*>(slot)[lane] = word;
+  // scale bytes: group g's sits in lanes 2g and 2g + 1; zeros behind the last
+  if ((lane & 1) == 0) slot[lane >> 1] = lane * 16 < nope ? static_cast<uint8_t>(sbyte) : 0;
 }
 
 // Write one bf16 row (generic pointer x, 16-byte aligned, row_elems values) into its

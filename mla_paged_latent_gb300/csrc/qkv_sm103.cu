@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) qkv_norm_rope_kernel(const __g
     if (r >= P.tokens) return;
     const int slot = P.slots[r];
     if (slot < 0) return;
-    const int page = slot / P.page_size;
+    const int page = slot >> (31 - __clz(P.page_size));  // (a power of two)
     const int pos = P.positions[r];
     const uint32_t bad = (page >= P.num_pages ? 4u : 0u) | (pos < 0 || pos >= P.max_pos ? 8u : 0u);
     if (bad != 0u) {  // reported, not written
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) qkv_norm_rope_kernel(const __g
     }
     norm_rope_row(P.kv_raw + (int64_t)r * P.kv_row_stride, P.kv_weight, P.kv_eps, P.freqs + (int64_t)pos * 64, WIDTH,
                   lane, srow[wi]);
-    write_any_row(srow[wi], lane, P.kv, P.layout, page, slot - page * P.page_size, P.page_size, P.page_bytes);
+    write_any_row(srow[wi], lane, P.kv, P.layout, page, slot & (P.page_size - 1), P.page_size, P.page_bytes);
     return;
   }
   // (the entry point keeps tokens * heads below 2^31, and a block's rows end at most 7 past it)
@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_read_kernel(const uint8_t* 
   if (r >= n) return;
   const int slot = slots[r];
   if (slot < 0) return;
-  const int page = slot / page_size;
-  const int off = slot - page * page_size;
+  const int page = slot >> (31 - __clz(page_size));  // (a power of two)
+  const int off = slot & (page_size - 1);
   if (page >= num_pages) {  // reported, not read
     if (lane == 0 && status != nullptr) atomicOr(status, 4u);
     return;
