@@ -31,9 +31,11 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
 // fused write), the others the (token, head) query rows: 64 sixteen-byte chunks, two a lane, NoPE from
 // q_nope and (512-wide rows) RoPE from q_pe, normalised over all 512 elements when asked; the
 // 576-wide rows' RoPE part is one pair a lane, rotated as it comes. A row is read whole into
-// registers before any of it is written, so q may be prepared in place.
+// registers before any of it is written, so q may be prepared in place. Bound by the bytes (2.3 KB a query row), and
+// for those by the loads in flight: 8192 x 128 rows of 576 take 366 us at eight blocks an SM (32 registers a thread,
+// some of the KV rows' spilled; 6.7 TB/s, as fast as a copy), 401 at six, 426 at five (48 registers).
 template <int WIDTH>
-__global__ void __launch_bounds__(kRowWarps * 32) qkv_norm_rope_kernel(const __grid_constant__ QkvParams P) {
+__global__ void __launch_bounds__(kRowWarps * 32, 8) qkv_norm_rope_kernel(const __grid_constant__ QkvParams P) {
   pdl_trigger();
   pdl_wait();
   __shared__ __align__(16) uint16_t srow[kRowWarps][576];
