@@ -143,9 +143,25 @@ __device__ __forceinline__ uint4 ld_or_zero(const void* p, bool on) {
       : "l"(p), "r"(static_cast<uint32_t>(on)));
   return v;
 }
+// The same of 32 bytes (32-byte aligned), in one load: two of 16 would ask for every sector twice.
+__device__ __forceinline__ void ld32_or_zero(const void* p, bool on, uint4& a, uint4& b) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %9, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
+      " mov.u32 %4, 0;\n mov.u32 %5, 0;\n mov.u32 %6, 0;\n mov.u32 %7, 0;\n"
+      " @p ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n}\n"
+      : "=&r"(a.x), "=&r"(a.y), "=&r"(a.z), "=&r"(a.w), "=&r"(b.x), "=&r"(b.y), "=&r"(b.z), "=&r"(b.w)
+      : "l"(p), "r"(static_cast<uint32_t>(on)));
+}
 __device__ __forceinline__ int ld_i32_or(const int32_t* p, bool on, int other) {
   int v;
   asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.s32 %0, %3;\n @p ld.global.nc.s32 %0, [%1];\n}\n"
+               : "=&r"(v)
+               : "l"(p), "r"(static_cast<uint32_t>(on)), "r"(other));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_u16_or(const void* p, bool on, uint32_t other) {
+  uint32_t v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, %3;\n @p ld.global.nc.u16 %0, [%1];\n}\n"
                : "=&r"(v)
                : "l"(p), "r"(static_cast<uint32_t>(on)), "r"(other));
   return v;
@@ -584,23 +600,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     const int w8 = (warp - 12) * 8;
     const int h = 1 - c;                      // the peer's half
     const int my_half = lane < 8 ? c : h;
-    const int g8 = lane & 7, r8 = lane >> 3;  // S operand: group of a part, row of a step
-    const int g4 = lane & 3, r4 = lane >> 2;  // values: group of a block, row
+    const int r8 = lane & 7, g4 = lane >> 3;  // row; S operand: a slab of a part, values: a group of a block
     auto wait = [&](uint32_t b, uint32_t parity) {  // warp-uniform
       return __all_sync(0xffffffffu, wait_bar(b, parity, abort_flag, P.status));
     };
     // One group of 32 codes as four 16-byte chunks. Chunk q of the group goes to addr ^ (q << 4): addr holds the
-    // row's place of chunk 0 in the 128-byte swizzle. Eight lanes store halves of several slabs' rows at once; x
-    // (part of addr already) is the order q ^ x in which a lane takes its words, so that they hit different banks.
-    auto put = [&](uint4 v, uint32_t sbyte, uint32_t x, uint32_t addr, bool on) {
+    // row's place of chunk 0 in the 128-byte swizzle. The eight lanes that store at once hold eight rows, whose
+    // places are eight different banks' groups.
+    auto put = [&](uint4 v, uint32_t sbyte, uint32_t addr, bool on) {
       if (!__all_sync(0xffffffffu, fp4_scale_plain(sbyte))) {
-        if (on) put_wide(v, sbyte, addr ^ (x << 4));
+        if (on) put_wide(v, sbyte, addr);
         return;
       }
       Fp4Scale s;
       s.h = static_cast<uint16_t>((sbyte - 112u) << 10);
-      const uint32_t a0 = x & 1 ? v.y : v.x, a1 = x & 1 ? v.x : v.y, a2 = x & 1 ? v.w : v.z, a3 = x & 1 ? v.z : v.w;
-      const uint32_t w4[4] = {x & 2 ? a2 : a0, x & 2 ? a3 : a1, x & 2 ? a0 : a2, x & 2 ? a1 : a3};
+      const uint32_t w4[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         uint32_t e[4];
@@ -608,12 +622,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (on) st_shared_v4(addr ^ (q << 4), make_uint4(e[0], e[1], e[2], e[3]));
       }
     };
-    // this thread's places: of the S operand in slab g8 / 2 (row w8 + r8, then 4 rows on), of the values in slab
-    // 2h + g4 / 2, of the RoPE slab
-    const uint32_t own_at = (g8 >> 1) * kPSlab + (w8 + r8) * 128 + (((4 * (g8 & 1)) ^ r8 ^ (g8 >> 1)) << 4);
-    const uint32_t val_at =
-        (2 * h + (g4 >> 1)) * kPSlab + (w8 + r4) * 128 + (((4 * (g4 & 1)) ^ (r4 & 7) ^ (g4 & 2)) << 4);
-    const uint32_t pe_at = (C::kNslab - 1) * kPSlab + (w8 + r8) * 128 + ((g8 ^ r8) << 4);
+    // this thread's places (row w8 + r8): of the S operand in slab g4 of a part, of the values in slab 2h + g4 / 2, of
+    // the RoPE slab
+    const uint32_t row_at = (w8 + r8) * 128;
+    const uint32_t own_at = g4 * kPSlab + row_at + (r8 << 4);
+    const uint32_t val_at = (2 * h + (g4 >> 1)) * kPSlab + row_at + (((4 * (g4 & 1)) ^ r8) << 4);
+    const uint32_t pe_at = (C::kNslab - 1) * kPSlab + row_at + ((g4 ^ r8) << 4);
     constexpr int kNopeGroups = C::kNope / kFp4Group;
     int it = 0;  // tiles whose V is in place
     bool live = true;
@@ -627,25 +641,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         int pos3 = -1, pos2 = -1, page2 = -1;  // this lane's row of tiles t + 3 and t + 2
         uint64_t row1 = 0;                     // address of its row of tile t + 1 (0: none)
         int32_t sc1 = 0;                       // from there to its scale slot
-        // S operand of tile t + 1: parts 0 and 1, two steps each; scale bytes
-        // values of tile t: the two blocks' groups of the peer's row r4; where a row has eight slabs, the last
+        // values of tile t: the two blocks' groups of the peer's row r8; where a row has eight slabs, the last
         // block's second slab is RoPE, 64 bytes a lane (16 in vr, 48 in vp)
         uint4 vr[2], vp[C::kNslab == 9 ? 1 : 3];
         uint32_t vs[2];
-        uint64_t ao[2] = {0, 0};  // S operand of tile t + 1: this thread's rows, their scales
-        const uint8_t* spo[2] = {nullptr, nullptr};
+        uint64_t ao = 0;  // S operand of tile t + 1: this thread's row, its scales
+        const uint8_t* spo = nullptr;
         uint32_t ok1 = 0;  // which rows of tile t + 1 count
         for (int t = -4; t < ntile; ++t) {
+          // codes of the S operand of tile t + 1: of each part the two groups of a slab, with their scale bytes
           uint4 raw[4];
-          uint32_t rs[4];
+          uint32_t rs[2];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const bool any = ao[i] != 0 && 8 * q + g8 < kNopeGroups;
-              raw[2 * q + i] = ld_or_zero(reinterpret_cast<const uint8_t*>(ao[i]) + 128 * q + 16 * g8, any);
-              rs[2 * q + i] = ld_u8_or(spo[i] + 8 * q, any, 127u);
-            }
+            const bool any = ao != 0 && 8 * q + 2 * g4 < kNopeGroups;
+            ld32_or_zero(reinterpret_cast<const uint8_t*>(ao) + 128 * q + 32 * g4, any, raw[2 * q], raw[2 * q + 1]);
+            rs[q] = ld_u16_or(spo + 8 * q, any, 0x7F7Fu);
           }
           if (t >= 0) {
             // ---- values of tile t: the peer's rows, this CTA's dims, over slabs that S has read
@@ -658,11 +669,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               }
               const bool code = 8 * b + 4 * c + g4 < kNopeGroups;
               const uint32_t at = base + 4 * b * kPSlab + val_at;
-              put(vr[b], vs[b], g4 & 2, at, code);
+              put(vr[b], vs[b], at, code);
               if (C::kNslab == 8 && b == 1 && !code) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                  st_shared_v4(at ^ ((q ^ (g4 & 2)) << 4), q == 0 ? vr[1] : vp[q > 0 ? q - 1 : 0]);
+                  st_shared_v4(at ^ (q << 4), q == 0 ? vr[1] : vp[q > 0 ? q - 1 : 0]);
               }
             }
             fence_proxy_async_smem();
@@ -685,16 +696,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             }
             const uint32_t base = stage(st) + own_at;
             // the RoPE slab: as it is, beside the conversion
+            const uint8_t* pe = (ao != 0 ? reinterpret_cast<const uint8_t*>(ao) : P.kv) + C::kNope / 2 + 16 * g4;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint64_t a = __shfl_sync(0xffffffffu, row1, 4 * i + r8);
-              cp_async16((stage(st) + pe_at + 512 * i) ^ (64 * i),
-                         (a != 0 ? reinterpret_cast<const uint8_t*>(a) : P.kv) + C::kNope / 2 + 16 * g8, a != 0);
-            }
+            for (int i = 0; i < 2; ++i) cp_async16((stage(st) + pe_at) ^ (64 * i), pe + 64 * i, ao != 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // part i / 2, step i % 2
-              put(raw[i], rs[i], g8 >> 1, (base + (i >> 1) * 4 * kPSlab + (i & 1) * 512) ^ ((i & 1) << 6),
-                  8 * (i >> 1) + g8 < kNopeGroups);
+            for (int i = 0; i < 4; ++i) {  // part i / 2, group i % 2 of its slab
+              put(raw[i], (rs[i >> 1] >> (8 * (i & 1))) & 0xFFu, (base + (i >> 1) * 4 * kPSlab) ^ ((i & 1) << 6),
+                  8 * (i >> 1) + 2 * g4 < kNopeGroups);
               if (i == 1 || (C::kNslab == 9 && i == 3)) {
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -725,13 +733,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           // ---- codes of tile t + 1's values (those of the operand follow at the top of the next iteration). All rows'
           // addresses first: a shuffle among loads in flight can come to wait for them.
-          const uint64_t av = __shfl_sync(0xffffffffu, row1, 8 + r4);
-          const uint8_t* spv = reinterpret_cast<const uint8_t*>(av) + __shfl_sync(0xffffffffu, sc1, 8 + r4);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            ao[i] = __shfl_sync(0xffffffffu, row, 4 * i + r8);
-            spo[i] = reinterpret_cast<const uint8_t*>(ao[i]) + __shfl_sync(0xffffffffu, sc, 4 * i + r8) + g8;
-          }
+          const uint64_t av = __shfl_sync(0xffffffffu, row1, 8 + r8);
+          const uint8_t* spv = reinterpret_cast<const uint8_t*>(av) + __shfl_sync(0xffffffffu, sc1, 8 + r8);
+          ao = __shfl_sync(0xffffffffu, row, r8);
+          spo = reinterpret_cast<const uint8_t*>(ao) + __shfl_sync(0xffffffffu, sc, r8) + 2 * g4;
           ok1 = __ballot_sync(0xffffffffu, row != 0);
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
