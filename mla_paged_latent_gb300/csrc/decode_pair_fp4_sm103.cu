@@ -14,13 +14,13 @@
 // that S has read and this CTA's half of V does not need, the peer's 64 rows in this CTA's 256 value dims.
 // That is three conversions of a half row for two SMs' work, against four (two whole rows) when the groups run
 // on one SM each, and S runs at N = 128 instead of M = 64. Measured against the single-SM kernel, us, 128 heads:
-//   64 requests, 295K rows in all            125 (656 TFLOP/s)   156
-//   32 requests x 4 draft tokens             431 (763 TFLOP/s)   552
-//   2048 listed rows for each of 64 tokens    68                  84
-//   one request of 131071 rows                94                 105
-// A tile takes about 6K cycles, of which the tensor cores work 2.8K (36 S steps of 49 cycles, 16 PV steps of 64). They
+//   64 requests, 295K rows in all            117 (702 TFLOP/s)   156
+//   32 requests x 4 draft tokens             393 (837 TFLOP/s)   552
+//   2048 listed rows for each of 64 tokens    67                  84
+//   one request of 131071 rows                65 (with the merge of 76 partials: 14)
+// A tile takes about 5.7K cycles, of which the tensor cores work 2.8K (36 S steps of 49 cycles, 16 PV steps of 64). They
 // are a chain: with two stages, the operand of S(t + 1) waits for the values of tile t, those for S(t), and S(t) for
-// its operand: 1.4K cycles of values, 2K to the operand's first part, 2.8K of S and the PV between (traced). What it
+// its operand: 1.4K cycles of values, 2K to the operand's first part, 2.8K of S and the PV between (traced at 6.2K a tile). What it
 // holds to: no load waited for soon after its issue (each row's address runs three tiles ahead, RoPE goes past the
 // registers), few instructions an MMA (the issuers share their sub-partitions with four busy warps), and code that
 // stays small beside the instruction cache. Registers are split by role for the same reason.
@@ -114,6 +114,29 @@ __device__ __forceinline__ void mma_bf16_pair_lo(uint32_t d, uint32_t a_lo, uint
       " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// (a.x, a.y) * (b, b) + (c.x, c.y), and a + b, two lanes an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 p, q, s, d;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %4};\n mov.b64 s, {%5, %6};\n"
+      " fma.rn.f32x2 d, p, q, s;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 p, q, d;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n add.rn.f32x2 d, p, q;\n"
+      " mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
 }
 
 // 16 bytes of global memory to shared memory, past the registers; zeros where `on` is false.
@@ -241,9 +264,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   const int num_work = P.num_partitions * PG;
   const int cl0 = static_cast<int>(cluster_id_x());
   const int ncl = static_cast<int>(num_clusters_x());
-  // Registers: 640 threads x 96 at launch; the issuing warps give some of theirs to the softmax, which spilled with 96.
+  // Registers: 640 threads x 96 at launch; the issuing warps give some of theirs to the softmax, which spilled with 96
+  // (64 and 112 instead of 72 and 104: 396 us against 393 on the draft tokens above).
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0) {
       // ------------------------------------------------------------ queries
       if (lane == 0) {
@@ -387,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
   } else if (warp < 12) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
     // ------------------------------------------------------------ softmax / epilogue
     // Lane wt = r + 64h of TMEM holds query row r (of this CTA's 64) against KV tile half
     // h in S, and dims 256b + 128h + 0..127 of that row in O. Two warps share each
@@ -436,14 +460,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           wait(bar(kMask + st), (it >> 1) & 1);
           const uint32_t vmask = *reinterpret_cast<const uint32_t*>(&misc->mask[st][8 * half + 4 * cg]) &
                                  (nv == 32 ? ~0u : ((1u << nv) - 1u));
-          float x[32];
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // masked scores become -inf: weight 0 (rarely any: one test a warp)
+          if (!__all_sync(0xffffffffu, vmask == ~0u)) {
 #pragma unroll
-          for (int cc = 0; cc < 32; ++cc) {
-            x[cc] = ((vmask >> cc) & 1u) ? __uint_as_float(sr[cc]) : -INFINITY;
-            m4[cc & 3] = fmaxf(m4[cc & 3], x[cc]);
+            for (int cc = 0; cc < 32; ++cc) sr[cc] = ((vmask >> cc) & 1u) ? sr[cc] : 0xFF800000u;
           }
-          const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * P.scale_log2;
+          float mt0 = -INFINITY, mt1 = -INFINITY;
+#pragma unroll
+          for (int cc = 0; cc < 32; cc += 4) {
+            mt0 = max3(mt0, __uint_as_float(sr[cc]), __uint_as_float(sr[cc + 1]));
+            mt1 = max3(mt1, __uint_as_float(sr[cc + 2]), __uint_as_float(sr[cc + 3]));
+          }
+          const float mt = fmaxf(mt0, mt1) * P.scale_log2;
           // the running maximum of a row moves (lazily) only when a tile exceeds it by more
           // than kPairRescaleLog2 powers of two; the four threads of the row take the same
           // decision
@@ -464,16 +492,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const bool rescale = any && !first && m_new != m_run && m_run != -INFINITY;
           const float m_use = (m_new == -INFINITY) ? 0.f : m_new;
           const float alpha = fast_exp2(m_run - m_use);
-          float ps4[4] = {0.f, 0.f, 0.f, 0.f};
+          float2 ps = make_float2(0.f, 0.f);
           uint32_t pk[16];
 #pragma unroll
           for (int cc = 0; cc < 16; ++cc) {
-            const float p0 = fast_exp2(fmaf(x[2 * cc], P.scale_log2, -m_use));
-            const float p1 = fast_exp2(fmaf(x[2 * cc + 1], P.scale_log2, -m_use));
-            ps4[cc & 3] += p0 + p1;
-            pk[cc] = f32x2_to_bf16x2(p0, p1);
+            const float2 x = fma2(make_float2(__uint_as_float(sr[2 * cc]), __uint_as_float(sr[2 * cc + 1])), P.scale_log2,
+                                  make_float2(-m_use, -m_use));
+            const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+            ps = add2(ps, p);
+            pk[cc] = f32x2_to_bf16x2(p.x, p.y);
           }
-          l_run = l_run * alpha + ((ps4[0] + ps4[1]) + (ps4[2] + ps4[3]));
+          l_run = l_run * alpha + (ps.x + ps.y);
           m_run = m_new;
           // P and O belong to the previous tile's PV until it completes
           if (it > 0) wait(bar(kPvDone), (it - 1) & 1);
