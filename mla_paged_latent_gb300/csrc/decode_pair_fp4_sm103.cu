@@ -14,10 +14,10 @@
 // that S has read and this CTA's half of V does not need, the peer's 64 rows in this CTA's 256 value dims.
 // That is three conversions of a half row for two SMs' work, against four (two whole rows) when the groups run
 // on one SM each, and S runs at N = 128 instead of M = 64. Measured against the single-SM kernel, us, 128 heads:
-//   64 requests, 295K rows in all            117 (702 TFLOP/s)   156
-//   32 requests x 4 draft tokens             393 (837 TFLOP/s)   552
+//   64 requests, 295K rows in all            116 (706 TFLOP/s)   156
+//   32 requests x 4 draft tokens             390 (844 TFLOP/s)   552
 //   2048 listed rows for each of 64 tokens    67                  84
-//   one request of 131071 rows                65 (with the merge of 76 partials: 14)
+//   one request of 131071 rows                64 (with the merge of 76 partials: 14)
 // A tile takes about 5.7K cycles, of which the tensor cores work 2.8K (36 S steps of 49 cycles, 16 PV steps of 64). They
 // are a chain: with two stages, the operand of S(t + 1) waits for the values of tile t, those for S(t), and S(t) for
 // its operand: 1.4K cycles of values, 2K to the operand's first part, 2.8K of S and the PV between (traced at 6.2K a tile). What it
@@ -417,14 +417,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // h in S, and dims 256b + 128h + 0..127 of that row in O. Two warps share each
     // 32-lane quarter (a warp reaches the lanes 32 (warp % 4) .. + 31): column group
     // cg = 0 takes S columns 0-31 and O block 0, cg = 1 columns 32-63 and O block 1. The
-    // four threads of a row meet through shared memory; the eight warps meet at named
-    // barrier 1 (no time limit: a thread whose bounded wait fails marks itself dead and
-    // all stop together at the next barrier).
+    // four threads of a row meet through shared memory; the four warps that hold the same 32
+    // rows meet at a named barrier of theirs (all eight at one: 1% slower; no time limit: a
+    // thread whose bounded wait fails marks itself dead and all stop together at the next
+    // barrier, the other four warps when the abort ends a wait of theirs).
     const int sx = tid - 128;  // 0 .. 255
     const int cg = sx >> 7;
     const int wt = sx & 127;
     const int r = wt & 63;
     const int half = wt >> 6;
+    const int rows_bar = 1 + (warp & 1);  // of the four warps that share query rows 32 (warp % 2) .. + 31
     const uint32_t lane_off = static_cast<uint32_t>(wt & ~31) << 16;
     bool dead = false, stop = false;
     auto wait = [&](uint32_t b, uint32_t parity) {
@@ -477,14 +479,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           // decision
           const bool raise = mt > m_run + kPairRescaleLog2;
           float m_new = m_run;
-          const bool any = named_bar_or(1, 256, raise || dead);
+          const bool any = named_bar_or(rows_bar, 128, raise || dead);
           if (any) {
-            if (named_bar_or(1, 256, dead)) {
+            if (named_bar_or(rows_bar, 128, dead)) {
               stop = true;
               return;
             }
             misc->xchg[sx] = mt;
-            named_bar_sync(1, 256);
+            named_bar_sync(rows_bar, 128);
             const float mh = fmaxf(fmaxf(misc->xchg[r], misc->xchg[r + 64]),
                                    fmaxf(misc->xchg[128 + r], misc->xchg[128 + r + 64]));
             m_new = (mh > m_run + kPairRescaleLog2) ? mh : m_run;
@@ -538,9 +540,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           if (lane == 0 && !dead) mbar_arrive_cluster(lead(kPFull));
         }
         // -------------------------------------------------------- epilogue
-        named_bar_sync(1, 256);  // every thread has read the last tile's maxima
+        named_bar_sync(rows_bar, 128);  // every thread has read the last tile's maxima
         misc->xchg[sx] = l_run;
-        if (named_bar_or(1, 256, dead)) {
+        if (named_bar_or(rows_bar, 128, dead)) {
           stop = true;
           return;
         }
@@ -565,10 +567,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           tc_fence_after();
           // A warp holds 32 consecutive output rows (one per lane) and, per TMEM load, the same
           // 32 value dims of each. Eight rows at a time pass through this warp's 1-KiB slice of
-          // the P slab (free here: the unit's last PV has completed; 16-B chunk q of staged row i
+          // the P slab (free here: the unit's last PV has completed, and the next P of the slice's rows is
+          // written by warps of this one's barrier; 16-B chunk q of staged row i
           // at position q ^ i), so that each global store covers contiguous dims of one row
           // (a store of one 16-B chunk per lane would touch 32 rows).
-          const uint32_t xb = parea(0, 1) + static_cast<uint32_t>(warp - 4) * 1024u;
+          const uint32_t xb = parea(0, 1) + static_cast<uint32_t>((warp & 1) * 4 + ((warp - 4) >> 1)) * 1024u;
           const int64_t row0 = (nsplit == 1 ? (int64_t)rq : (int64_t)sg) * R + (grow - lane);
 #pragma unroll 1
           for (int k = 0; k < 4; ++k) {
