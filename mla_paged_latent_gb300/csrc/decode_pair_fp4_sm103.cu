@@ -14,16 +14,16 @@
 // that S has read and this CTA's half of V does not need, the peer's 64 rows in this CTA's 256 value dims.
 // That is three conversions of a half row for two SMs' work, against four (two whole rows) when the groups run
 // on one SM each, and S runs at N = 128 instead of M = 64. Measured against the single-SM kernel, us, 128 heads:
-//   64 requests, 295K rows in all            116 (706 TFLOP/s)   156
-//   32 requests x 4 draft tokens             390 (844 TFLOP/s)   552
-//   2048 listed rows for each of 64 tokens    67                  84
-//   one request of 131071 rows                64 (with the merge of 76 partials: 14)
-// A tile takes about 5.7K cycles, of which the tensor cores work 2.8K (36 S steps of 49 cycles, 16 PV steps of 64). They
-// are a chain: with two stages, the operand of S(t + 1) waits for the values of tile t, those for S(t), and S(t) for
-// its operand: 1.4K cycles of values, 2K to the operand's first part, 2.8K of S and the PV between (traced at 6.2K a tile). What it
-// holds to: no load waited for soon after its issue (each row's address runs three tiles ahead, RoPE goes past the
-// registers), few instructions an MMA (the issuers share their sub-partitions with four busy warps), and code that
-// stays small beside the instruction cache. Registers are split by role for the same reason.
+//   64 requests, 295K rows in all            116 (708 TFLOP/s)   156
+//   32 requests x 4 draft tokens             389 (846 TFLOP/s)   552
+//   2048 listed rows for each of 64 tokens    66                  84
+//   one request of 131071 rows                63 (with the merge of 76 partials, 12)
+// A tile takes about 5.7K cycles, of which the tensor cores work 2.8K (36 S steps of 49 cycles, 16 PV steps of 64).
+// They are a chain: with two stages, the operand of S(t + 1) waits for the values of tile t, those for S(t), and S(t)
+// for its operand (traced: 0.6K cycles from S to its values, 2K to the operand's first part, 3.4K of S and the PV
+// between). What it holds to: no load waited for soon after its issue (each row's address runs three tiles ahead, RoPE
+// goes past the registers), few instructions a group of codes and an MMA (issue slots are 45% used, the issuers share
+// theirs with four busy warps), and code that stays small beside the instruction cache.
 //
 // Shared memory per CTA: Q (64 rows x 64 dims a slab, 128-B swizzle), two stages of the tile's rows, P of the
 // tile's two halves: the 512-NoPE row's P of half 0 takes its stage's RoPE slab, which V does not read and S
@@ -447,6 +447,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const int st = it & 1;
           const bool first = b0 == lo;
           uint32_t sr[32];
+          wait(bar(kMask + st), (it >> 1) & 1);
+          const uint32_t held = *reinterpret_cast<const uint32_t*>(&misc->mask[st][8 * half + 4 * cg]);
           wait(bar(kSFull + st), (it >> 1) & 1);
           if (!dead) {
             tc_fence_after();
@@ -459,9 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           const int pos0 = (b0 + half) * kBlockRows + cg * 32;  // KV position of this thread's column 0
           int nv = row_end - pos0;
           nv = nv < 0 ? 0 : (nv > 32 ? 32 : nv);
-          wait(bar(kMask + st), (it >> 1) & 1);
-          const uint32_t vmask = *reinterpret_cast<const uint32_t*>(&misc->mask[st][8 * half + 4 * cg]) &
-                                 (nv == 32 ? ~0u : ((1u << nv) - 1u));
+          const uint32_t vmask = held & (nv == 32 ? ~0u : ((1u << nv) - 1u));
           // masked scores become -inf: weight 0 (rarely any: one test a warp)
           if (!__all_sync(0xffffffffu, vmask == ~0u)) {
 #pragma unroll
@@ -498,8 +498,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           uint32_t pk[16];
 #pragma unroll
           for (int cc = 0; cc < 16; ++cc) {
-            const float2 x = fma2(make_float2(__uint_as_float(sr[2 * cc]), __uint_as_float(sr[2 * cc + 1])), P.scale_log2,
-                                  make_float2(-m_use, -m_use));
+            const float2 x = fma2(make_float2(__uint_as_float(sr[2 * cc]), __uint_as_float(sr[2 * cc + 1])),
+                                  P.scale_log2, make_float2(-m_use, -m_use));
             const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
             ps = add2(ps, p);
             pk[cc] = f32x2_to_bf16x2(p.x, p.y);
