@@ -392,8 +392,8 @@ def mla_qkv_norm_rope(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, kv
         _require("q_norm_weight", q_norm_weight, "bfloat16", 512)
     _require_status(status)
     _check(load().mla_qkv_norm_rope(q_nope.data_ptr(), qs, qh, q_pe.data_ptr(), ps, ph, q_eps is not None,
-                                    _ptr(q_norm_weight), 0.0 if q_eps is None else q_eps, kv_raw.data_ptr(), rs,
-                                    slots.data_ptr(), positions.data_ptr(), kv_norm_weight.data_ptr(), kv_eps,
+                                    _ptr(q_norm_weight), 0.0 if q_eps is None else float(q_eps), kv_raw.data_ptr(), rs,
+                                    slots.data_ptr(), positions.data_ptr(), kv_norm_weight.data_ptr(), float(kv_eps),
                                     freqs.data_ptr(), freqs.shape[0], T, N, q_out.data_ptr(), kv_cache.data_ptr(),
                                     layout, kv_cache.shape[0], page_size, _ptr(status), _stream(stream)))
 

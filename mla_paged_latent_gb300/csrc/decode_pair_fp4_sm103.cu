@@ -156,12 +156,13 @@ __device__ __noinline__ void put_wide(uint4 v, uint32_t sbyte, uint32_t addr) {
   }
 }
 
-// Predicated loads (no branch): zeros, or `other`, where `on` is false.
+// Predicated loads (no branch): zeros, or `other`, where `on` is false. (Not the non-coherent ones: this grid may be on
+// its SMs before the grid that writes the rows has ended.)
 __device__ __forceinline__ uint4 ld_or_zero(const void* p, bool on) {
   uint4 v;
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
-      " @p ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n}\n"
+      " @p ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n}\n"
       : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
       : "l"(p), "r"(static_cast<uint32_t>(on)));
   return v;
@@ -171,27 +172,27 @@ __device__ __forceinline__ void ld32_or_zero(const void* p, bool on, uint4& a, u
   asm volatile(
       "{\n .reg .pred p;\n setp.ne.u32 p, %9, 0;\n mov.u32 %0, 0;\n mov.u32 %1, 0;\n mov.u32 %2, 0;\n mov.u32 %3, 0;\n"
       " mov.u32 %4, 0;\n mov.u32 %5, 0;\n mov.u32 %6, 0;\n mov.u32 %7, 0;\n"
-      " @p ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n}\n"
+      " @p ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n}\n"
       : "=&r"(a.x), "=&r"(a.y), "=&r"(a.z), "=&r"(a.w), "=&r"(b.x), "=&r"(b.y), "=&r"(b.z), "=&r"(b.w)
       : "l"(p), "r"(static_cast<uint32_t>(on)));
 }
 __device__ __forceinline__ int ld_i32_or(const int32_t* p, bool on, int other) {
   int v;
-  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.s32 %0, %3;\n @p ld.global.nc.s32 %0, [%1];\n}\n"
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.s32 %0, %3;\n @p ld.global.s32 %0, [%1];\n}\n"
                : "=&r"(v)
                : "l"(p), "r"(static_cast<uint32_t>(on)), "r"(other));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_u16_or(const void* p, bool on, uint32_t other) {
   uint32_t v;
-  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, %3;\n @p ld.global.nc.u16 %0, [%1];\n}\n"
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, %3;\n @p ld.global.u16 %0, [%1];\n}\n"
                : "=&r"(v)
                : "l"(p), "r"(static_cast<uint32_t>(on)), "r"(other));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_u8_or(const void* p, bool on, uint32_t other) {
   uint32_t v;
-  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, %3;\n @p ld.global.nc.u8 %0, [%1];\n}\n"
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.u32 %0, %3;\n @p ld.global.u8 %0, [%1];\n}\n"
                : "=&r"(v)
                : "l"(p), "r"(static_cast<uint32_t>(on)), "r"(other));
   return v;
