@@ -136,28 +136,38 @@ def _require_cuda(*tensors):
 
 
 def _require_one_device(*tensors):
-    """All on one GPU, the one that the call launches on."""
+    """All on the GPU, and on the one that the call launches on."""
     device = tensors[0].get_device()
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError(f"all tensors must live on one device, not on {tensors[0].device} and {t.device}")
     if device >= 0:
-        import torch
-        current = torch.cuda.current_device() if _torch_c is None else _torch_c._cuda_getDevice()
+        if _torch_c is not None:
+            current = _torch_c._cuda_getDevice()
+        else:
+            import torch
+            current = torch.cuda.current_device()
         if device != current:
             raise ValueError(f"the tensors live on cuda:{device}, the current device is cuda:{current}")
+    else:
+        _require_cuda(*tensors)
 
 
-_dtypes = {}  # name -> torch dtype
+_torch_types = None
 
 
-def _require(name: str, t, dtype: str, *shape, contiguous: bool = True):
-    """One tensor's type, shape (None: any size) and layout; raises ValueError."""
-    want = _dtypes.get(dtype)
-    if want is None:
+def _types():
+    """torch's bfloat16, float32, int32 and uint8."""
+    global _torch_types
+    if _torch_types is None:
         import torch
-        want = _dtypes[dtype] = getattr(torch, dtype)
-    if t.dtype is not want:
+        _torch_types = torch.bfloat16, torch.float32, torch.int32, torch.uint8
+    return _torch_types
+
+
+def _require(name: str, t, dtype, *shape, contiguous: bool = True):
+    """One tensor's type, shape (None: any size) and layout; raises ValueError."""
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     have = t.shape
     if have != shape and (len(have) != len(shape) or
@@ -165,10 +175,6 @@ def _require(name: str, t, dtype: str, *shape, contiguous: bool = True):
         raise ValueError(f"{name} must have the shape {list(shape)}, not {list(have)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-
-
-def _require_cache(kv_cache, layout: int, page_size: int):
-    _require("kv_cache", kv_cache, "uint8", None, _page_bytes(layout, page_size))
 
 
 def _require_status(status):
@@ -372,24 +378,34 @@ def mla_qkv_norm_rope(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, kv
     freqs float32 [max_pos, 64]; q_out bf16 [T, N, ROW_ELEMS] (or the queries' own memory, row for row).
     status: optional device uint32 [1] receiving MLA_STATUS_BAD_SLOT (4) / MLA_STATUS_BAD_POSITION (8)."""
     tensors = q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, freqs, q_out, kv_cache, q_norm_weight, status
-    _require_cuda(*tensors)
     _require_one_device(*tensors)
-    _require_cache(kv_cache, layout, page_size)
+    pb = _page_bytes(layout, page_size)
     width = ROW_ELEMS[layout]
+    nope = 448 if width == 512 else 512
     T, N = q_nope.shape[:2]
-    _require("q_nope", q_nope, "bfloat16", T, N, 448 if width == 512 else 512, contiguous=False)
-    _require("q_pe", q_pe, "bfloat16", T, N, 64, contiguous=False)
-    _require("kv_raw", kv_raw, "bfloat16", T, width, contiguous=False)
+    bf16, f32, i32, u8 = _types()
+    if not (q_nope.dtype is q_pe.dtype is kv_raw.dtype is kv_norm_weight.dtype is q_out.dtype is bf16
+            and slots.dtype is positions.dtype is i32 and freqs.dtype is f32 and kv_cache.dtype is u8
+            and q_nope.shape == (T, N, nope) and q_pe.shape == (T, N, 64) and q_out.shape == (T, N, width)
+            and kv_raw.shape == (T, width) and slots.shape == positions.shape == (T,)
+            and kv_norm_weight.shape == (512,) and freqs.shape[1:] == (64,) and kv_cache.shape[1:] == (pb,)
+            and q_out.is_contiguous() and slots.is_contiguous() and positions.is_contiguous()
+            and kv_norm_weight.is_contiguous() and freqs.is_contiguous() and kv_cache.is_contiguous()):
+        # which of them it is (the host time of a small step is these checks': all at once they take half of it)
+        _require("kv_cache", kv_cache, u8, None, pb)
+        _require("q_nope", q_nope, bf16, T, N, nope, contiguous=False)
+        _require("q_pe", q_pe, bf16, T, N, 64, contiguous=False)
+        _require("kv_raw", kv_raw, bf16, T, width, contiguous=False)
+        _require("slots", slots, i32, T)
+        _require("positions", positions, i32, T)
+        _require("kv_norm_weight", kv_norm_weight, bf16, 512)
+        _require("freqs", freqs, f32, None, 64)
+        _require("q_out", q_out, bf16, T, N, width)
     (qs, qh, q1), (ps, ph, p1), (rs, r1) = q_nope.stride(), q_pe.stride(), kv_raw.stride()
     if T > 0 and not (q1 == p1 == r1 == 1):
         raise ValueError("q_nope, q_pe and kv_raw must have their last elements adjacent")
-    _require("slots", slots, "int32", T)
-    _require("positions", positions, "int32", T)
-    _require("kv_norm_weight", kv_norm_weight, "bfloat16", 512)
-    _require("freqs", freqs, "float32", None, 64)
-    _require("q_out", q_out, "bfloat16", T, N, width)
     if q_norm_weight is not None:
-        _require("q_norm_weight", q_norm_weight, "bfloat16", 512)
+        _require("q_norm_weight", q_norm_weight, bf16, 512)
     _require_status(status)
     _check(load().mla_qkv_norm_rope(q_nope.data_ptr(), qs, qh, q_pe.data_ptr(), ps, ph, q_eps is not None,
                                     _ptr(q_norm_weight), 0.0 if q_eps is None else float(q_eps), kv_raw.data_ptr(), rs,
@@ -402,11 +418,15 @@ def mla_kv_read(kv_cache, layout: int, page_size: int, slots, rows, status=None,
     """Cached rows decoded to bf16: rows [n, ROW_ELEMS] receives the rows at slots int32 [n] (negative:
     left as it was). status: optional device uint32 [1] receiving MLA_STATUS_BAD_SLOT (4) for a slot past
     the cache."""
-    _require_cuda(kv_cache, slots, rows, status)
     _require_one_device(kv_cache, slots, rows, status)
-    _require_cache(kv_cache, layout, page_size)
-    _require("slots", slots, "int32", None)
-    _require("rows", rows, "bfloat16", slots.shape[0], ROW_ELEMS[layout])
+    bf16, _, i32, u8 = _types()
+    pb, width = _page_bytes(layout, page_size), ROW_ELEMS[layout]
+    if not (kv_cache.dtype is u8 and slots.dtype is i32 and rows.dtype is bf16 and kv_cache.shape[1:] == (pb,)
+            and rows.shape == (*slots.shape, width) and slots.dim() == 1 and kv_cache.is_contiguous()
+            and slots.is_contiguous() and rows.is_contiguous()):
+        _require("kv_cache", kv_cache, u8, None, pb)
+        _require("slots", slots, i32, None)
+        _require("rows", rows, bf16, slots.shape[0], width)
     _require_status(status)
     _check(load().mla_kv_read(_ptr(kv_cache), layout, kv_cache.shape[0], page_size, _ptr(slots), slots.shape[0],
                               _ptr(rows), _ptr(status), _stream(stream)))
