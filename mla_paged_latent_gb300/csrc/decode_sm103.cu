@@ -71,6 +71,9 @@ constexpr uint32_t kPrefetchBytes = 160u * 1024u;  // 96-224 KB measured alike; 
 // group scales make a few rows score far above the rest).
 constexpr float kRescaleLog2 = 64.0f;
 
+// The role of warp w in hexadecimal digit w: converters (8-15) on 0, 8, 12, 1, 9, 13 and 14, 15.
+constexpr uint64_t kFp4Roles = 0xEFDA01C9765432B8ull;
+
 struct Misc {
   uint64_t bar[kNumBars];
   uint32_t tmem_base;
@@ -145,7 +148,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   volatile int* abort_flag = &misc->abort;
 
   const int tid = threadIdx.x;
-  const int warp = tid >> 5;
+  // The role's warp number (the list above). 4-bit rows: an MMA issuer holds up the other warps of its SM sub-partition
+  // (w % 4) while the tensor cores' queue is full (traced: their converters finish a tile 1-2K cycles after the others),
+  // so the converters stand three on each of the sub-partitions 0 and 1 and one beside each issuer, with the query and
+  // prefetch warps: 128 requests x 64 heads 234 us against 244 with two on each, 239 with both issuers on one.
+  const int warp = C::kFp4 ? static_cast<int>(kFp4Roles >> (4 * (tid >> 5))) & 15 : tid >> 5;
   const int lane = tid & 31;
   // candidates listed per token: top-k positions (indices) or the rows of its slot runs
   // (gathered variants only: the TMA variant never sees either)
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
     // a thread that gave up after the last barrier of its last unit: nothing left to share
   } else if (warp >= 8 && !TMA_KV) {
     // ------------------------------------------------------------ converters
-    const int ct = tid - 256;        // 0..255
+    const int ct = (warp - 8) * 32 + lane;  // 0..255
     const int crow = ct >> 2;        // tile row handled
     const int part4 = ct & 3;        // chunk phase
     int it = 0;
