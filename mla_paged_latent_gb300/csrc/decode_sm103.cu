@@ -138,8 +138,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // and 5: DSV4-shaped decode 3 % faster, DSV3-shaped 0.5 %, verify 1.3 %). The sparse
   // variants keep the PV issuer on warp 1: their prefetch warp does per-row work and they
   // were 3 % slower.
-  constexpr int kPvWarp = (LAYOUT == 1 || LAYOUT == 3 || TMA_KV) ? 3 : 1;
-  constexpr int kPrefetchWarp = (LAYOUT == 1 || LAYOUT == 3 || TMA_KV) ? 1 : 3;
+  constexpr int kPvWarp = (LAYOUT == 1 || LAYOUT >= 3 || TMA_KV) ? 3 : 1;
+  constexpr int kPrefetchWarp = (LAYOUT == 1 || LAYOUT >= 3 || TMA_KV) ? 1 : 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_addr(smem);
