@@ -622,14 +622,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // ------------------------------------------------------------ converters
-    // A warp takes rows 8 w .. + 7 of both tile halves (w = warp - 12): of the peer's half this CTA's 256 value dims
-    // (V of tile t: four lanes a row and block), then of its CTA's own half all dims (the S operand of tile t + 1:
-    // eight lanes a row, one 16-byte group of 32 codes each, four rows at a time). Lanes 0-7 look up the own half's
-    // rows, lanes 8-15 the peer's. The codes are loaded an iteration before they are converted, and every step of the
-    // address chain (listed index -> block-table entry -> row) an iteration before the next: one loop body does them
-    // all, its first iterations (t < 0) only what there is. The order is fixed: V(t) waits for S(t), the operand of
-    // S(t + 1) for the value product of tile t - 1, and warps that each took what could go first held one another
-    // up (6% slower; the operand before the values: 4%).
+    // A warp takes rows 8 w .. + 7 of both tile halves (w = warp - 12), four lanes a row: of the peer's half this CTA's
+    // 256 value dims (V of tile t: a group of 32 codes a lane and block), then of its CTA's own half all dims (the S
+    // operand of tile t + 1: of each part a slab a lane, two groups). Lanes 0-7 look up the own half's rows, lanes 8-15
+    // the peer's. Codes are loaded a conversion or more before their own (the operand's at the top of the iteration,
+    // V's at the end of the one before), and every step of the address chain (listed index -> block-table entry -> row)
+    // an iteration before the next: one loop body does them all, its first iterations (t < 0) only what there is. The
+    // order is fixed: V(t) waits for S(t), the operand of S(t + 1) for the value product of tile t - 1, and warps that
+    // each took what could go first held one another up (6% slower; the operand before the values: 4%).
     const int w8 = (warp - 12) * 8;
     const int h = 1 - c;                      // the peer's half
     const int my_half = lane < 8 ? c : h;

@@ -28,7 +28,8 @@
 //   warp 2      S MMA issuer (one thread)
 //   warp 3      PV MMA issuer (one thread) [layout 2 and bf16 gather: L2 prefetch]
 //   warps 4-7   softmax (16 query rows per warp, two threads per row) + O rescale + epilogue
-//   warps 8-15  converters: fp8 -> bf16 dequantisation and sparse row gathers
+//   warps 8-15  converters: fp8 and 4-bit -> bf16 dequantisation and sparse row gathers (4-bit rows: the roles' warps
+//               are placed otherwise, kFp4Roles)
 #include <cstdint>
 #include <cuda_runtime.h>
 

@@ -1,5 +1,5 @@
 // The 4-bit row: e2m1 codes with one ue8m0 scale per 32 elements, decoded to bf16 and encoded
-// from fp32. Shared by the decode kernel, the KV writes and the reads back.
+// from it. Shared by the decode kernels, the KV writes and the reads back.
 //
 // e2m1 (OCP MX): sign, two exponent bits (bias 1), one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6.
 // A value is e2m1(code) * 2^(scale - 127); a code has two significant bits, so the product is
