@@ -291,7 +291,8 @@ int mla_decode_runs(const void* q, const void* kv_cache, mla_kv_layout layout, i
  * (num_splits[b+1] - num_splits[b]) is at least 2, merge its partials by
  * log-sum-exp — lse = ln sum_s e^(lse_s), out = sum_s e^(lse_s - lse) o_s, a
  * partial with lse_s = -inf carrying no weight ("mla_attention.py", Chunked
- * Prefill: merge_attn_states; neutralize_empty_context_partials) — then apply
+ * Prefill: merge_attn_states; neutralize_empty_context_partials), one with a NaN
+ * lse_s making NaN of its row whatever stands beside it — then apply
  * the sink once: out *= 1 / (1 + e^(sink - lse)). Requests with one split are
  * left untouched.
  *  part_out device float [total_splits, rows_per_req, 512]; part_lse device

@@ -14,7 +14,8 @@ namespace mla {
 // ("MLA" API page of HALOps, mla_output_proj: the split-KV LSE combine receives attn_sink).
 // acc[4 k + i] receives element 4 (32 (k0 + k) + lane) + i: the whole row (N = 16), or a quarter
 // of it (N = 4, k0 = 0 .. 3); the return value is lse (-inf, with acc = 0, when every partial is
-// empty).
+// empty). A partial whose lse is NaN is not empty and makes NaN of lse and acc; the maximum passes
+// over it, so what is empty is asked of the partials themselves.
 template <int N>
 __device__ __forceinline__ float merge_row(const float* __restrict__ part_out, const float* __restrict__ part_lse,
                                            int s0, int ns, int R, int row, int lane, const float* __restrict__ sink,
@@ -37,8 +38,11 @@ __device__ __forceinline__ float merge_row(const float* __restrict__ part_out, c
         for (int k = 0; k < K; ++k) v[s][k] = src[(k0 + k) * 32 + lane];
       }
     }
+    bool any = false;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) any |= ls[s] != -INFINITY;
+    if (!any) return -INFINITY;
     const float mx = fmaxf(fmaxf(ls[0], ls[1]), fmaxf(ls[2], ls[3]));
-    if (mx == -INFINITY) return -INFINITY;
     float tot = 0.f;
 #pragma unroll
     for (int s = 0; s < 4; ++s)
@@ -58,10 +62,15 @@ __device__ __forceinline__ float merge_row(const float* __restrict__ part_out, c
     }
   } else {
     float mx = -INFINITY;
-    for (int s = lane; s < ns; s += 32) mx = fmaxf(mx, part_lse[(int64_t)(s0 + s) * R + row]);
+    bool any = false;
+    for (int s = lane; s < ns; s += 32) {
+      const float l = part_lse[(int64_t)(s0 + s) * R + row];
+      mx = fmaxf(mx, l);
+      any |= l != -INFINITY;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if (mx == -INFINITY) return -INFINITY;
+    if (!__any_sync(0xffffffffu, any)) return -INFINITY;
     float tot = 0.f;
     for (int s = lane; s < ns; s += 32) tot += expf(part_lse[(int64_t)(s0 + s) * R + row] - mx);
 #pragma unroll
