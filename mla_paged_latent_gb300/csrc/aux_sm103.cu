@@ -14,12 +14,10 @@ namespace {
 // One warp per query row of a request that the plan split into >= 2 pieces (the merge
 // itself is merge_row in combine_row.cuh), or with few rows WARPS = 4 of them, a quarter of the row each.
 template <int WARPS>
-__global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ part_out,
-                                                      const float* __restrict__ part_lse,
-                                                      const int32_t* __restrict__ num_splits, int R, int heads,
-                                                      const float* __restrict__ sink, uint16_t* __restrict__ out,
-                                                      float* __restrict__ lse, const float* __restrict__ part_max,
-                                                      float* __restrict__ max_logits) {
+__global__ void __launch_bounds__(128) combine_kernel(const float* part_out, const float* part_lse,
+                                                      const int32_t* num_splits, int R, int heads, const float* sink,
+                                                      uint16_t* out, float* lse, const float* part_max,
+                                                      float* max_logits) {
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.y;
@@ -51,9 +49,9 @@ __global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ 
 // mla_output_proj: the split-KV partials merged by LSE, then the RoPE of O undone). Written
 // back to out.
 __global__ void __launch_bounds__(256) combine_inv_rope_kernel(
-    const float* __restrict__ part_out, const float* __restrict__ part_lse, const int32_t* __restrict__ num_splits,
-    int R, int sq, int heads, const float* __restrict__ sink, const int32_t* __restrict__ positions,
-    const float* __restrict__ freqs, int max_pos, int rope0, uint16_t* __restrict__ out, float* __restrict__ lse) {
+    const float* part_out, const float* part_lse, const int32_t* num_splits,
+    int R, int sq, int heads, const float* sink, const int32_t* positions,
+    const float* freqs, int max_pos, int rope0, uint16_t* out, float* lse) {
   pdl_trigger();
   pdl_wait();
   const int b = blockIdx.y;
@@ -63,6 +61,7 @@ __global__ void __launch_bounds__(256) combine_inv_rope_kernel(
   const int64_t orow = (int64_t)b * R + row;
   const int s0 = num_splits[b];
   const int ns = num_splits[b + 1] - s0;
+  const int pos = positions[b * sq + row / heads];
   float acc[16];
   if (ns >= 2 && part_out != nullptr) {  // no partials given: every row is taken as written
     const float lse_tot = merge_row(part_out, part_lse, s0, ns, R, row, lane, sink, row % heads, acc);
@@ -78,7 +77,6 @@ __global__ void __launch_bounds__(256) combine_inv_rope_kernel(
       acc[4 * k + 3] = __uint_as_float(v.y & 0xFFFF0000u);
     }
   }
-  const int pos = positions[b * sq + row / heads];
   if (pos < 0 || pos >= max_pos) return;  // no table row: left as merged
   const float* f = freqs + (int64_t)pos * 64;
   // lane holds elements d = 4 (32 k + lane) .. +3, i.e. pairs (d, d + 1) and (d + 2, d + 3)
@@ -107,9 +105,8 @@ __global__ void __launch_bounds__(256) combine_inv_rope_kernel(
 // its first row. Each run is stored from its lowest slot upwards (attention does not depend
 // on the order of its rows): row g < len0 is slot slot0 + g, row g >= len0 slot1 + g - len0.
 // The lanes read 32 window entries at a time and find the run breaks with one ballot.
-__global__ void __launch_bounds__(128) swa_plan_kernel(const int32_t* __restrict__ idx,
-                                                       const int32_t* __restrict__ lens, int T, int topk,
-                                                       int log2_ps, int step, int4* __restrict__ runs) {
+__global__ void __launch_bounds__(128) swa_plan_kernel(const int32_t* idx, const int32_t* lens, int T, int topk,
+                                                       int log2_ps, int step, int4* runs) {
   pdl_trigger();
   pdl_wait();
   const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -158,10 +155,9 @@ __global__ void __launch_bounds__(128) swa_plan_kernel(const int32_t* __restrict
 
 // ----------------------------------------------------------------------------- kv write
 // One warp per new row, already normalised.
-__global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* __restrict__ rows,
-                                                       const int32_t* __restrict__ slots, int n,
-                                                       uint8_t* __restrict__ kv, int layout, int64_t num_pages,
-                                                       int page_size, int64_t page_bytes, uint32_t* status) {
+__global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* rows, const int32_t* slots, int n,
+                                                       uint8_t* kv, int layout, int64_t num_pages, int page_size,
+                                                       int64_t page_bytes, uint32_t* status) {
   pdl_trigger();
   pdl_wait();
   const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -184,9 +180,8 @@ __global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* __restric
 // NaNs are found at once, on bf16 pairs taken as integers. 65000 rows of 448 + 64: 20 us (4.5 TB/s) against 29 with
 // neither.
 template <int LAYOUT>
-__global__ void __launch_bounds__(256) kv_write_fp4_kernel(const uint16_t* __restrict__ rows,
-                                                           const int32_t* __restrict__ slots, int n,
-                                                           uint8_t* __restrict__ kv, int64_t num_pages, int page_size,
+__global__ void __launch_bounds__(256) kv_write_fp4_kernel(const uint16_t* rows, const int32_t* slots, int n,
+                                                           uint8_t* kv, int64_t num_pages, int page_size,
                                                            int64_t page_bytes, uint32_t* status) {
   pdl_trigger();
   pdl_wait();
@@ -214,9 +209,9 @@ __global__ void __launch_bounds__(256) kv_write_fp4_kernel(const uint16_t* __res
 // step before the cache write, kv_norm_weight / kv_eps / positions / freqs_real), the row
 // rounded to bf16 in shared memory (norm_rope_row), then written as write_row writes it.
 __global__ void __launch_bounds__(128) kv_write_norm_rope_kernel(
-    const uint16_t* __restrict__ raw, const int32_t* __restrict__ slots, const int32_t* __restrict__ positions,
-    const uint16_t* __restrict__ w, float eps, const float* __restrict__ freqs, int max_pos, int n,
-    uint8_t* __restrict__ kv, int layout, int64_t num_pages, int page_size, int64_t page_bytes, uint32_t* status) {
+    const uint16_t* raw, const int32_t* slots, const int32_t* positions,
+    const uint16_t* w, float eps, const float* freqs, int max_pos, int n,
+    uint8_t* kv, int layout, int64_t num_pages, int page_size, int64_t page_bytes, uint32_t* status) {
   pdl_trigger();
   pdl_wait();
   __shared__ __align__(16) uint16_t srow[4][576];
@@ -241,10 +236,9 @@ __global__ void __launch_bounds__(128) kv_write_norm_rope_kernel(
 }
 
 // ----------------------------------------------------------------------------- gather
-__global__ void __launch_bounds__(128) kv_gather_kernel(const uint8_t* __restrict__ kv, int layout,
-                                                        int64_t num_pages, int page_size, int64_t page_bytes,
-                                                        const int32_t* __restrict__ bt_row, int max_pages,
-                                                        int length, float* __restrict__ out) {
+__global__ void __launch_bounds__(128) kv_gather_kernel(const uint8_t* kv, int layout, int64_t num_pages,
+                                                        int page_size, int64_t page_bytes, const int32_t* bt_row,
+                                                        int max_pages, int length, float* out) {
   pdl_trigger();
   pdl_wait();
   const int j = blockIdx.x * 4 + (threadIdx.x >> 5);

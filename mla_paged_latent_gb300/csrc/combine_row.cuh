@@ -17,8 +17,8 @@ namespace mla {
 // empty). A partial whose lse is NaN is not empty and makes NaN of lse and acc; the maximum passes
 // over it, so what is empty is asked of the partials themselves.
 template <int N>
-__device__ __forceinline__ float merge_row(const float* __restrict__ part_out, const float* __restrict__ part_lse,
-                                           int s0, int ns, int R, int row, int lane, const float* __restrict__ sink,
+__device__ __forceinline__ float merge_row(const float* part_out, const float* part_lse,
+                                           int s0, int ns, int R, int row, int lane, const float* sink,
                                            int head, float (&acc)[N], int k0 = 0) {
   constexpr int K = N / 4;
 #pragma unroll

@@ -801,14 +801,14 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
 #pragma unroll
           for (int i = 0; i < CPT; ++i) {
             const int c = part4 + 4 * i;
-            v[i] = valid && c < C::kChunks ? ld_nc_v4(rowp + c * 16) : make_uint4(0, 0, 0, 0);
+            v[i] = valid && c < C::kChunks ? ld_once_v4(rowp + c * 16) : make_uint4(0, 0, 0, 0);
           }
           uint2 sc = make_uint2(0, 0);
           uint4 sc4 = make_uint4(0, 0, 0, 0);
           if (C::kFp4) {
-            if (valid) sc4 = ld_nc_v4(scp);
+            if (valid) sc4 = ld_once_v4(scp);
           } else if (LAYOUT != 0 && valid) {
-            sc = ld_nc_v2(scp);
+            sc = ld_once_v2(scp);
           }
           // dequantise in registers before waiting for the stage, so that only the stores
           // remain once the PV two tiles back has released it: an fp8 chunk (16 e4m3 codes of

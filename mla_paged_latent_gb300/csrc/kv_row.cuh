@@ -83,12 +83,15 @@ __device__ __forceinline__ void write_row_fp4(uint4 x0, uint4 x1, uint4 pe, int 
 // Write one bf16 row (generic pointer x, 16-byte aligned, row_elems values) into its
 // page slot (layouts of 8 and 16 bits); all 32 lanes of the warp take part ("MLA" API page of HALOps,
 // mla_attention: KV cache write of the RMSNorm'd row; kv_cache parameter for the layout).
-__device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* __restrict__ kv, int layout,
+__device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* kv, int layout,
                                           int64_t page, int off, int page_size, int64_t page_bytes) {
   if (layout == 0) {
     const uint4* src = reinterpret_cast<const uint4*>(x);
     uint4* dst = reinterpret_cast<uint4*>(kv + page * page_bytes + (int64_t)off * 1152);
-    for (int c = lane; c < 72; c += 32) dst[c] = src[c];
+    const uint4 c0 = src[lane], c1 = src[32 + lane], c2 = src[64 + (lane & 7)];
+    dst[lane] = c0;
+    dst[32 + lane] = c1;
+    if (lane < 8) dst[64 + lane] = c2;
     return;
   }
   const int nope = row_nope(layout);
@@ -96,11 +99,13 @@ __device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* 
   uint8_t* dst = kv + page * page_bytes + (int64_t)off * row_bytes;
   // lane l holds elements [16 l, 16 l + 16), loaded at once; NoPE group g is lanes 4g .. 4g+3
   // (in the 512-wide DSV4 rows, lanes 28-31 hold the RoPE part)
+  const uint4 x0 = reinterpret_cast<const uint4*>(x)[2 * lane];
+  const uint4 x1 = reinterpret_cast<const uint4*>(x)[2 * lane + 1];
+  uint4 pe = make_uint4(0, 0, 0, 0);  // the 576-wide row's RoPE part
+  if (layout != 1 && lane < 8) pe = reinterpret_cast<const uint4*>(x + nope)[lane];
   float v[16];
   {
-    const uint4 a = reinterpret_cast<const uint4*>(x)[2 * lane];
-    const uint4 b = reinterpret_cast<const uint4*>(x)[2 * lane + 1];
-    const uint32_t h[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    const uint32_t h[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       v[2 * k] = bf16_to_f32(h[k] & 0xFFFFu);
@@ -132,10 +137,9 @@ __device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* 
     reinterpret_cast<uint4*>(dst)[lane] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
   } else {
     // DSV4 row: its 64 RoPE elements stay bf16, after the 448 code bytes
-    const uint4* src = reinterpret_cast<const uint4*>(x) + 2 * lane;
     uint4* d2 = reinterpret_cast<uint4*>(dst + nope + (lane * 16 - nope) * 2);
-    d2[0] = src[0];
-    d2[1] = src[1];
+    d2[0] = x0;
+    d2[1] = x1;
   }
   // scale bytes: group g's exponent sits in lane 4g; lane 0 assembles the 8-byte slot
   uint32_t sbytes[2] = {0u, 0u};
@@ -144,9 +148,7 @@ __device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* 
     const int eg = __shfl_sync(0xffffffffu, e, 4 * g);
     if (g < nope / 64) sbytes[g >> 2] |= static_cast<uint32_t>(eg + 127) << (8 * (g & 3));
   }
-  // the 576-wide row's RoPE part: 64 bf16 copied
-  if (layout != 1 && lane < 8)
-    reinterpret_cast<uint4*>(dst + nope)[lane] = reinterpret_cast<const uint4*>(x + nope)[lane];
+  if (layout != 1 && lane < 8) reinterpret_cast<uint4*>(dst + nope)[lane] = pe;
   if (lane == 0) {
     uint2* sp = reinterpret_cast<uint2*>(kv + page * page_bytes + (int64_t)page_size * row_bytes + off * 8);
     *sp = make_uint2(sbytes[0], sbytes[1]);
@@ -154,7 +156,7 @@ __device__ __forceinline__ void write_row(const uint16_t* x, int lane, uint8_t* 
 }
 
 // write_row for every layout.
-__device__ __forceinline__ void write_any_row(const uint16_t* x, int lane, uint8_t* __restrict__ kv, int layout,
+__device__ __forceinline__ void write_any_row(const uint16_t* x, int lane, uint8_t* kv, int layout,
                                               int64_t page, int off, int page_size, int64_t page_bytes) {
   if (layout < 3) {
     write_row(x, lane, kv, layout, page, off, page_size, page_bytes);
@@ -171,8 +173,8 @@ __device__ __forceinline__ void write_any_row(const uint16_t* x, int lane, uint8
 // (16-byte aligned), in fp32, rounded once to bf16 into srow (shared memory; all lanes of the warp
 // take part, and it ends with a __syncwarp). Lane l holds latent elements [16 l, 16 l + 16) and
 // RoPE pair l of the 576-wide layouts; f is the position's row of the (cos, sin) table.
-__device__ __forceinline__ void norm_rope_row(const uint16_t* x, const uint16_t* __restrict__ w, float eps,
-                                              const float* __restrict__ f, int width, int lane, uint16_t* srow) {
+__device__ __forceinline__ void norm_rope_row(const uint16_t* x, const uint16_t* w, float eps,
+                                              const float* f, int width, int lane, uint16_t* srow) {
   float v[16];
   {
     const uint4 a = reinterpret_cast<const uint4*>(x)[2 * lane];

@@ -261,16 +261,21 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
 }
 
 // ------------------------------------------------------------------ global loads
-__device__ __forceinline__ uint4 ld_nc_v4(const void* p) {
+// Every kernel of this library may be on its SMs before the kernel ahead of it on the stream has ended
+// (programmatic dependent launch), so none may load what that kernel writes (cached rows, partials, runs) through
+// the non-coherent path: that path asks for memory which nobody writes while the kernel lives. Hence no ld.global.nc,
+// and no pointer parameter is declared free of aliases, from which the compiler would take leave to use it.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return v;
 }
-__device__ __forceinline__ uint2 ld_nc_v2(const void* p) {
+__device__ __forceinline__ uint2 ld_once_v2(const void* p) {
   uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
   return v;
 }
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {

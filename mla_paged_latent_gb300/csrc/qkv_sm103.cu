@@ -137,10 +137,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 8) qkv_norm_rope_kernel(const 
 // One warp per row: the cached row at slots[r], decoded to bf16. A lane takes eight elements a
 // step, so loads and stores of a warp are contiguous.
 template <int LAYOUT>
-__global__ void __launch_bounds__(kRowWarps * 32) kv_read_kernel(const uint8_t* __restrict__ kv, int64_t num_pages,
+__global__ void __launch_bounds__(kRowWarps * 32) kv_read_kernel(const uint8_t* kv, int64_t num_pages,
                                                                  int page_size, int64_t page_bytes,
-                                                                 const int32_t* __restrict__ slots, int n,
-                                                                 uint16_t* __restrict__ out, uint32_t* status) {
+                                                                 const int32_t* slots, int n,
+                                                                 uint16_t* out, uint32_t* status) {
   pdl_trigger();
   pdl_wait();
   constexpr int kNope = row_nope(LAYOUT), kRowBytes = row_stored_bytes(LAYOUT), kWidth = row_width(LAYOUT);
@@ -159,24 +159,41 @@ __global__ void __launch_bounds__(kRowWarps * 32) kv_read_kernel(const uint8_t* 
   const uint8_t* src = kv + page * page_bytes + (int64_t)off * kRowBytes;
   const uint8_t* sc = kv + page * page_bytes + (int64_t)page_size * kRowBytes + (int64_t)off * row_scale_slot(LAYOUT);
   uint4* dst = reinterpret_cast<uint4*>(out + (int64_t)r * kWidth);
+  // every load before the first store, which may alias them for all that the compiler knows
   uint4 pe = make_uint4(0, 0, 0, 0);
   if (lane < 8) pe = reinterpret_cast<const uint4*>(src + kCodeBytes)[lane];
+  uint4 raw[2];      // elements 8c .. 8c + 7, c = lane + 32 h: 16, 8 or 4 bytes
+  uint32_t sb[2];    // and their scale byte
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int c = lane + 32 * h;  // elements 8c .. 8c + 7
+    const int c = lane + 32 * h;
     if (8 * c >= kNope) break;
     if (LAYOUT == 0) {
-      dst[c] = reinterpret_cast<const uint4*>(src)[c];
+      raw[h] = reinterpret_cast<const uint4*>(src)[c];
     } else if (LAYOUT <= 2) {
       const uint2 w = reinterpret_cast<const uint2*>(src)[c];
-      const float s = ue8m0_to_f32(sc[c >> 3]);
-      const float2 a = e4m3x2_to_f32x2(w.x & 0xFFFFu), b = e4m3x2_to_f32x2(w.x >> 16);
-      const float2 d = e4m3x2_to_f32x2(w.y & 0xFFFFu), e = e4m3x2_to_f32x2(w.y >> 16);
+      raw[h] = make_uint4(w.x, w.y, 0, 0);
+      sb[h] = sc[c >> 3];
+    } else {
+      raw[h] = make_uint4(reinterpret_cast<const uint32_t*>(src)[c], 0, 0, 0);
+      sb[h] = sc[c >> 2];
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = lane + 32 * h;
+    if (8 * c >= kNope) break;
+    if (LAYOUT == 0) {
+      dst[c] = raw[h];
+    } else if (LAYOUT <= 2) {
+      const float s = ue8m0_to_f32(sb[h]);
+      const float2 a = e4m3x2_to_f32x2(raw[h].x & 0xFFFFu), b = e4m3x2_to_f32x2(raw[h].x >> 16);
+      const float2 d = e4m3x2_to_f32x2(raw[h].y & 0xFFFFu), e = e4m3x2_to_f32x2(raw[h].y >> 16);
       dst[c] = make_uint4(f32x2_to_bf16x2(a.x * s, a.y * s), f32x2_to_bf16x2(b.x * s, b.y * s),
                           f32x2_to_bf16x2(d.x * s, d.y * s), f32x2_to_bf16x2(e.x * s, e.y * s));
     } else {
       uint32_t o[4];
-      fp4x8_to_bf16(reinterpret_cast<const uint32_t*>(src)[c], fp4_scale(sc[c >> 2]), o);
+      fp4x8_to_bf16(raw[h].x, fp4_scale(sb[h]), o);
       dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
