@@ -423,8 +423,8 @@ int mla_kv_write_norm_rope(const void* raw, const int32_t* slots, const int32_t*
  *  q_out   device bf16 [num_tokens, num_heads, row_elems]. It may be the queries' own memory row for
  *          row (q_nope == q_out, q_pe == q_out + its offset, strides those of q_out); any other
  *          overlap with an input, or of q_out or an input with kv_cache, is refused.
- * Strides are multiples of 8 elements >= 0 and every pointer is 16-byte aligned (status, slots
- * and positions 4-byte). status (device uint32 or NULL) is OR-ed with MLA_STATUS_BAD_SLOT and
+ * Strides are multiples of 8 elements >= 0 (that of one token or one head is not read) and every
+ * pointer is 16-byte aligned (status, slots and positions 4-byte). status (device uint32 or NULL) is OR-ed with MLA_STATUS_BAD_SLOT and
  * MLA_STATUS_BAD_POSITION.
  */
 int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,

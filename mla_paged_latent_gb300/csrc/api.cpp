@@ -601,6 +601,12 @@ int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q
     return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: eps must be a finite number >= 0");
   if (!q_norm && q_norm_weight != nullptr)
     return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: q_norm_weight given without q_norm");
+  // a dimension of size one has whatever stride its history left: taken as that of rows that follow one another
+  if (num_tokens == 1) {
+    q_nope_token_stride = q_pe_token_stride = static_cast<int64_t>(num_heads) * dqk;
+    kv_row_stride = dqk;
+  }
+  if (num_heads == 1) q_nope_head_stride = q_pe_head_stride = dqk;
   const int64_t strides[5] = {q_nope_token_stride, q_nope_head_stride, q_pe_token_stride, q_pe_head_stride,
                               kv_row_stride};
   for (int64_t s : strides)
