@@ -637,6 +637,22 @@ int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q
       overlap(kv, strided_range(q_pe, T, q_pe_token_stride, N, q_pe_head_stride, 64)) ||
       overlap(kv, strided_range(kv_raw, T, kv_row_stride, 1, 0, dqk)))
     return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: kv_cache overlaps the queries or the rows");
+  const int64_t index_bytes = 4 * T;
+  const struct {
+    const void* p;
+    int64_t bytes;
+  } small[] = {{slots, index_bytes},
+               {positions, index_bytes},
+               {kv_norm_weight, 1024},
+               {q_norm_weight, 1024},
+               {freqs, static_cast<int64_t>(max_pos) * 256}};
+  for (const auto& in : small) {
+    if (in.p == nullptr) continue;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(in.p);
+    const ByteRange r = {lo, lo + static_cast<uintptr_t>(in.bytes)};
+    if (overlap(out, r) || overlap(kv, r))
+      return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: q_out or kv_cache overlaps slots, positions, a gain or freqs");
+  }
   mla::QkvParams p;
   std::memset(&p, 0, sizeof p);
   p.q_nope = static_cast<const uint16_t*>(q_nope);
