@@ -238,7 +238,7 @@ def mla_decode(q, kv_cache, layout: int, page_size: int, block_table, cache_seql
     out bf16 [T, N, 512]; lse float32 [T, N]; sink float32 [N] or None; indices int32 [T, topk] or None.
     single_sm: run a decode whose query rows come in groups of 128 (dense over bf16 rows, or over
     4-bit rows) on the single-SM kernel instead of the CTA-pair kernel."""
-    _require_cuda(q, kv_cache, block_table, cache_seqlens, sched, num_splits, workspace, out, lse, sink, indices)
+    _require_one_device(q, kv_cache, block_table, cache_seqlens, sched, num_splits, workspace, out, lse, sink, indices)
     T, N, D = q.shape
     B = cache_seqlens.shape[0]
     topk = 0 if indices is None else int(indices.shape[-1])
@@ -257,7 +257,7 @@ def mla_sparse_prefill(q, kv, indices, sm_scale: float, sched, num_splits, num_p
     [T, N, 576]; kv bf16 [s_kv, 576]; indices int32 [T, topk] (positions in kv, others skipped);
     the plan from mla_decode_plan(np.full(T, s_kv), 1, N, topk, ...). Writes out bf16
     [T, N, 512], max_logits float32 [T, N] and lse float32 [T, N]."""
-    _require_cuda(q, kv, indices, sched, num_splits, workspace, out, max_logits, lse)
+    _require_one_device(q, kv, indices, sched, num_splits, workspace, out, max_logits, lse)
     T, N, D = q.shape
     _check(load().mla_sparse_prefill(_ptr(q), _ptr(kv), kv.shape[0], _ptr(indices), int(indices.shape[-1]), T, N,
                                      float(sm_scale), _ptr(sched), _ptr(num_splits), num_partitions, total_splits,
@@ -267,7 +267,7 @@ def mla_sparse_prefill(q, kv, indices, sm_scale: float, sched, num_splits, num_p
 
 def mla_swa_plan(kv_indices, page_size: int, kv_run_step: int, runs, topk_lengths=None, stream=None):
     """Window runs: kv_indices int32 [T, topk] cache slots -> runs int32 [T, 4] (slot0, len0, slot1, rows)."""
-    _require_cuda(kv_indices, runs, topk_lengths)
+    _require_one_device(kv_indices, runs, topk_lengths)
     T, topk = kv_indices.shape
     _check(load().mla_swa_plan(_ptr(kv_indices), _ptr(topk_lengths), T, topk, page_size, kv_run_step, _ptr(runs),
                                _stream(stream)))
@@ -278,7 +278,7 @@ def mla_decode_runs(q, kv_cache, layout: int, page_size: int, runs, window: int,
                     sink=None, skip_combine: bool = False, stream=None):
     """Decode where token t attends over the rows of its window runs (runs int32 [T, 4] from
     mla_swa_plan); the plan comes from mla_decode_plan with topk = window."""
-    _require_cuda(q, kv_cache, runs, sched, num_splits, workspace, out, lse, sink)
+    _require_one_device(q, kv_cache, runs, sched, num_splits, workspace, out, lse, sink)
     T, N, D = q.shape
     B = T // q_tokens_per_req
     _check(load().mla_decode_runs(_ptr(q), _ptr(kv_cache), layout, kv_cache.shape[0], page_size, _ptr(runs), window,
@@ -294,7 +294,7 @@ def mla_decode_static_workspace(q, kv_cache, layout: int, page_size: int, block_
     """mla_decode without a caller workspace: for callers that cannot allocate device
     memory, the library's static device workspace (STATIC_WORKSPACE_BYTES) is used.
     status_out: optional device int32/uint32 [1] receiving the call's status bits."""
-    _require_cuda(q, kv_cache, block_table, cache_seqlens, sched, num_splits, out, lse, sink, indices, status_out)
+    _require_one_device(q, kv_cache, block_table, cache_seqlens, sched, num_splits, out, lse, sink, indices, status_out)
     T, N, D = q.shape
     B = cache_seqlens.shape[0]
     topk = 0 if indices is None else int(indices.shape[-1])
@@ -318,7 +318,7 @@ def workspace_partials(workspace, total_splits: int, rows_per_req: int):
 
 def mla_combine(part_out, part_lse, num_splits, rows_per_req: int, num_heads: int, out, lse, sink=None,
                 stream=None):
-    _require_cuda(part_out, part_lse, num_splits, out, lse, sink)
+    _require_one_device(part_out, part_lse, num_splits, out, lse, sink)
     B = num_splits.shape[0] - 1
     _check(load().mla_combine(_ptr(part_out), _ptr(part_lse), _ptr(num_splits), B, rows_per_req, num_heads,
                               _ptr(sink), _ptr(out), _ptr(lse), _stream(stream)))
@@ -327,7 +327,7 @@ def mla_combine(part_out, part_lse, num_splits, rows_per_req: int, num_heads: in
 def mla_kv_write(rows, slots, kv_cache, layout: int, page_size: int, status=None, stream=None):
     """Write new rows into their page slots. status: optional device uint32 [1] that
     receives MLA_STATUS_BAD_SLOT (4) for a row whose page is out of range (not written)."""
-    _require_cuda(rows, slots, kv_cache, status)
+    _require_one_device(rows, slots, kv_cache, status)
     _check(load().mla_kv_write(_ptr(rows), _ptr(slots), slots.shape[0], _ptr(kv_cache), layout, kv_cache.shape[0],
                                page_size, _ptr(status), _stream(stream)))
 
@@ -337,7 +337,7 @@ def mla_combine_v_up(part_out, part_lse, num_splits, q_tokens_per_req: int, num_
     """Split combine + value up-projection: o_v [T, N, 128] bf16 = bf16 latent out [T, N, 512] x W_UV[n]
     (w_uv bf16 [N, 512, 128]); split requests are merged into out / lse first. part_out / part_lse may be
     None when no request is split. status: optional device uint32 [1] (bit 0: a bounded wait ran out)."""
-    _require_cuda(part_out, part_lse, num_splits, w_uv, out, lse, o_v, sink, status)
+    _require_one_device(num_splits, part_out, part_lse, w_uv, out, lse, o_v, sink, status)
     B = num_splits.shape[0] - 1
     _check(load().mla_combine_v_up(_ptr(part_out), _ptr(part_lse), _ptr(num_splits), B, q_tokens_per_req, num_heads,
                                    _ptr(sink), _ptr(w_uv), _ptr(out), _ptr(lse), _ptr(o_v), _ptr(status),
@@ -349,7 +349,7 @@ def mla_combine_inv_rope(part_out, part_lse, num_splits, q_tokens_per_req: int, 
     """Split combine + inverse RoPE of out[..., rope0:rope0 + 64] (in place, bf16 [T, N, 512]);
     positions int32 [T]; freqs float32 [max_pos, 64]. part_out / part_lse may be None when no
     request is split."""
-    _require_cuda(part_out, part_lse, num_splits, positions, freqs, out, lse, sink)
+    _require_one_device(num_splits, part_out, part_lse, positions, freqs, out, lse, sink)
     B = num_splits.shape[0] - 1
     _check(load().mla_combine_inv_rope(_ptr(part_out), _ptr(part_lse), _ptr(num_splits), B, q_tokens_per_req,
                                        num_heads, _ptr(sink), _ptr(positions), _ptr(freqs), freqs.shape[0], rope0,
@@ -362,7 +362,7 @@ def mla_kv_write_norm_rope(raw, slots, positions, norm_weight, eps: float, freqs
     slots int32 [n]; positions int32 [n]; norm_weight bf16 [512]; freqs float32 [max_pos, 64]
     (32 interleaved (cos, sin) pairs per position). All on the GPU. status: optional device
     uint32 [1] receiving MLA_STATUS_BAD_SLOT (4) / MLA_STATUS_BAD_POSITION (8) for skipped rows."""
-    _require_cuda(raw, slots, positions, norm_weight, freqs, kv_cache, status)
+    _require_one_device(raw, slots, positions, norm_weight, freqs, kv_cache, status)
     _check(load().mla_kv_write_norm_rope(_ptr(raw), _ptr(slots), _ptr(positions), _ptr(norm_weight), float(eps),
                                          _ptr(freqs), freqs.shape[0], slots.shape[0], _ptr(kv_cache), layout,
                                          kv_cache.shape[0], page_size, _ptr(status), _stream(stream)))
@@ -433,7 +433,7 @@ def mla_kv_read(kv_cache, layout: int, page_size: int, slots, rows, status=None,
 
 
 def mla_kv_gather(kv_cache, layout: int, page_size: int, block_table_row, length: int, out, stream=None):
-    _require_cuda(kv_cache, block_table_row, out)
+    _require_one_device(kv_cache, block_table_row, out)
     _check(load().mla_kv_gather(_ptr(kv_cache), layout, kv_cache.shape[0], page_size, _ptr(block_table_row),
                                 block_table_row.shape[0], length, _ptr(out), _stream(stream)))
 
