@@ -154,24 +154,26 @@ __global__ void __launch_bounds__(128) swa_plan_kernel(const int32_t* idx, const
 }
 
 // ----------------------------------------------------------------------------- kv write
-// One warp per new row, already normalised.
-__global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* rows, const int32_t* slots, int n,
-                                                       uint8_t* kv, int layout, int64_t num_pages, int page_size,
-                                                       int64_t page_bytes, uint32_t* status) {
+// One warp per new row, already normalised. A kernel a layout, the page by a shift: bound by a row's instructions
+// (65000 rows of layouts 0, 1, 2: 23.1, 22.5, 23.2 us, 4.7 to 6.5 TB/s; with the layout as an argument and a division
+// 27.2, 29.7, 29.9).
+template <int LAYOUT>
+__global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* rows, const int32_t* slots, int n, uint8_t* kv,
+                                                       int64_t num_pages, int page_size, int64_t page_bytes,
+                                                       uint32_t* status) {
   pdl_trigger();
   pdl_wait();
   const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (r >= n) return;
-  const int64_t slot = slots[r];
+  const int slot = slots[r];
   if (slot < 0) return;
-  const int64_t page = slot / page_size;
+  const int64_t page = slot >> (31 - __clz(page_size));  // (a power of two)
   if (page >= num_pages) {  // reported, not written
     if (lane == 0 && status != nullptr) atomicOr(status, 4u);
     return;
   }
-  const int row_elems = row_width(layout);
-  write_row(rows + (int64_t)r * row_elems, lane, kv, layout, page, static_cast<int>(slot % page_size), page_size,
+  write_row(rows + (int64_t)r * row_width(LAYOUT), lane, kv, LAYOUT, page, slot & (page_size - 1), page_size,
             page_bytes);
 }
 
@@ -327,8 +329,10 @@ cudaError_t launch_kv_write(const uint16_t* rows, const int32_t* slots, int n, u
   if (layout >= 3)
     return launch_pdl(layout == 3 ? kv_write_fp4_kernel<3> : kv_write_fp4_kernel<4>, dim3((n + 7) / 8), dim3(256), 0,
                       stream, rows, slots, n, kv, num_pages, page_size, page_bytes, status);
-  return launch_pdl(kv_write_kernel, dim3((n + 3) / 4), dim3(128), 0, stream, rows, slots, n, kv, layout, num_pages,
-                    page_size, page_bytes, status);
+  return launch_pdl(layout == 0   ? kv_write_kernel<0>
+                    : layout == 1 ? kv_write_kernel<1>
+                                  : kv_write_kernel<2>,
+                    dim3((n + 3) / 4), dim3(128), 0, stream, rows, slots, n, kv, num_pages, page_size, page_bytes, status);
 }
 
 cudaError_t launch_kv_write_norm_rope(const uint16_t* raw, const int32_t* slots, const int32_t* positions,
