@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kVupThreads, 1)
         const int ns = P.num_splits[b + 1] - s0;
         if (ns >= 2 && P.part_out != nullptr) {
           // merged exactly as the combine kernel merges it, and written back the same way
-          const float lse_tot = merge_row(P.part_out, P.part_lse, s0, ns, R, row, lane, P.sink, n, acc);
+          const float lse_tot = merge_row<16, 1>(P.part_out, P.part_lse, s0, ns, R, row, lane, P.sink, n, acc);
           store_row_bf16(P.out + orow * 512, lane, acc);
           if (lane == 0) P.lse[orow] = lse_tot;
         } else {
