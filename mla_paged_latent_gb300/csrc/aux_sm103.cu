@@ -295,11 +295,15 @@ cudaError_t launch_combine(const float* part_out, const float* part_lse, const i
                            int rows_per_req, int heads, const float* sink, uint16_t* out, float* lse,
                            const float* part_max, float* max_logits, cudaStream_t stream) {
   if (batch <= 0 || rows_per_req <= 0) return cudaSuccess;
-  // blocks of 128 threads (96 registers a thread: five blocks per SM, against two of 256 threads)
-  // Four warps a row where rows are few: a few requests split many ways are bound by the loads that a warp keeps in
-  // flight. Measured, us, with the launch's 5: 128 rows of 76 partials 17 (a warp a row: 36), 256 of 38 15 (23), 384 of
-  // 25 13 (17), 512 of 19 15 (15), 512 of 5 12 (11).
-  const bool few = static_cast<int64_t>(rows_per_req) * batch <= 384;
+  // Blocks of 128 threads: 94 registers a thread with a warp a row (five blocks an SM, against two of 256 threads), 114
+  // with four warps a row (four). Four warps a row where rows are few: a few requests split many ways are bound by the
+  // loads that a warp keeps in flight. Measured, us a launch, partials of 2 / 4 / 8 / 16 / 76 splits out of L2 and DRAM in
+  // turn, four warps a row against one:
+  //   128 rows  1.5 / 1.7 / 2.8 / 3.0 / 14.1   1.6 / 1.8 / 3.1 / 4.3 / 29.5
+  //   384       1.6 / 2.0 / 3.2 / 4.9 / 16.3   1.7 / 2.1 / 3.3 / 8.0 / 30.3
+  //   512       1.7 / 1.9 / 3.4 / 5.8 / 17.8   1.9 / 2.2 / 3.9 / 8.6 / 31.1
+  //   640       2.2 / 2.5 / 5.1 / 8.8 / 29.9   2.1 / 2.5 / 4.7 / 9.0 / 32.7
+  const bool few = static_cast<int64_t>(rows_per_req) * batch <= 512;
   const dim3 grid(few ? rows_per_req : (rows_per_req + 3) / 4, batch);
   return launch_pdl(few ? combine_kernel<4> : combine_kernel<1>, grid, dim3(128), 0, stream, part_out, part_lse,
                     num_splits, rows_per_req, heads, sink, out, lse, part_max, max_logits);

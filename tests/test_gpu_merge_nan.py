@@ -47,7 +47,7 @@ def _check(out, lse, rows, what):
     assert np.isfinite(out[5:]).all() and np.isfinite(lse[5:]).all(), what
 
 
-@pytest.mark.parametrize("rows", [8, 400])          # four warps a row, and one
+@pytest.mark.parametrize("rows", [8, 400, 600])     # four warps a row, and one
 @pytest.mark.parametrize("ns", [2, 3, 4, 5, 33])
 @pytest.mark.parametrize("sink", [False, True])
 def test_merge_keeps_nan(rows, ns, sink):
@@ -70,6 +70,32 @@ def test_merge_keeps_nan(rows, ns, sink):
     mla.mla_combine_v_up(_cuda(po), _cuda(pl), counts, 1, rows, w, o2, l2, ov, sink=s)
     _check(bf16_to_f64(o2), l2.cpu().numpy(), rows, "up-projection")
     _check(bf16_to_f64(ov), l2.cpu().numpy(), rows, "up-projection's values")
+
+
+@pytest.mark.parametrize("rows,splits", [(513, 2), (520, 5), (600, 21), (600, 33), (512, 33)])
+def test_merge_of_many_rows(rows, splits):
+    """One warp a row (and, at 512, the last count with four), in 64 bits; some partials empty, one row wholly."""
+    rng = np.random.default_rng(rows + splits)
+    po = rng.standard_normal((splits, rows, 512)).astype(np.float32)
+    pl = (3 * rng.standard_normal((splits, rows))).astype(np.float32)
+    empty = rng.random((splits, rows)) < 0.2
+    empty[0], empty[:, 3] = False, True
+    pl[empty], po[empty] = -np.inf, np.nan
+    sink = rng.standard_normal(rows).astype(np.float32)
+    out = torch.empty(rows, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(rows, device="cuda")
+    mla.mla_combine(_cuda(po), _cuda(pl), _cuda(np.array([0, splits], np.int32)), rows, rows, out, lse, sink=_cuda(sink))
+    got, glse = bf16_to_f64(out), lse.cpu().numpy().astype(np.float64)
+    assert np.isneginf(glse[3]) and np.all(got[3] == 0)
+    keep = np.arange(rows) != 3
+    l, o = pl[:, keep].astype(np.float64), np.where(empty, 0.0, po.transpose(2, 0, 1))[:, :, keep].astype(np.float64)
+    ref_lse = np.log(np.exp(l).sum(0))
+    wt = np.exp(l - ref_lse) / (1 + np.exp(sink[keep] - ref_lse))
+    ref, mean = np.einsum("sr,dsr->rd", wt, o), np.einsum("sr,dsr->rd", wt, np.abs(o))
+    # fp32 weights: exponentials and logarithm (2 units each), their arguments (|lse| below 16: 2^-20), sums of up to 33
+    # terms (33 * 2^-24 of their magnitudes); then one rounding to bf16
+    assert np.all(np.abs(glse[keep] - ref_lse) <= 2.0 ** -19)
+    assert np.all(np.abs(got[keep] - ref) <= 2.0 ** -17 * mean + 2.0 ** -8 * np.abs(ref))
 
 
 def _nan_scales(w, request, rows):
