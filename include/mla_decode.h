@@ -53,6 +53,10 @@
  *  bf16 each (as it does for bf16 rows; the fp8 layouts pass a pair). A NaN in a row makes NaN
  *  of every query row of its request that is computed with it, those of draft tokens before it
  *  (causal, weight zero) too. A row of a page out of range is left out of the sums.
+ *  Range of the values: the decodes of the fp8 and 4-bit layouts, and of bf16 rows on the single-SM
+ *  kernel, weigh rows with up to 2^64 before the sum is normalised, so a request's rows times its
+ *  largest |V| must stay below 2^64 (2^20 rows of values up to 2^43); past that a sum may overflow
+ *  to infinity or NaN where the result would not. The CTA-pair kernel of bf16 rows: 2^32 and 2^96.
  */
 #ifndef MLA_DECODE_H_
 #define MLA_DECODE_H_

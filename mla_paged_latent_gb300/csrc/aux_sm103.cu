@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(128) kv_write_kernel(const uint16_t* rows, con
 
 // The same for 4-bit rows. Bound by the length of a row's chain (one row a warp, as many warps as fit) and by its
 // instructions. So the row is loaded beside its slot and not after it, and the largest magnitude of a group and its
-// NaNs are found at once, on bf16 pairs taken as integers. 65000 rows of 448 + 64: 20 us (4.5 TB/s) against 29 with
-// neither.
+// NaNs are found at once, on bf16 pairs taken as integers: 65000 rows of 448 + 64 20 us against 29 with neither; 16.9 us
+// (5.4 TB/s) since the row's arithmetic is in 32 bits.
 template <int LAYOUT>
 __global__ void __launch_bounds__(256) kv_write_fp4_kernel(const uint16_t* rows, const int32_t* slots, int n,
                                                            uint8_t* kv, int64_t num_pages, int page_size,

@@ -17,7 +17,7 @@
 //   64 requests, 295K rows in all            116 (708 TFLOP/s)   156
 //   32 requests x 4 draft tokens             389 (846 TFLOP/s)   552
 //   2048 listed rows for each of 64 tokens    66                  84
-//   one request of 131071 rows                63 (with the merge of 76 partials, 12)
+//   one request of 131071 rows                64 (59 and the merge of 76 partials)
 // A tile takes about 5.7K cycles, of which the tensor cores work 2.8K (36 S steps of 49 cycles, 16 PV steps of 64).
 // They are a chain: with two stages, the operand of S(t + 1) waits for the values of tile t, those for S(t), and S(t)
 // for its operand (traced: 0.6K cycles from S to its values, 2K to the operand's first part, 3.4K of S and the PV

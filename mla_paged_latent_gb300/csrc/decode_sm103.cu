@@ -109,7 +109,7 @@ struct Cfg {
   // pair P = P_hi + P_lo (P_lo = bf16(P - P_hi)) in extra 8 KB buffers: one per stage
   // where shared memory allows (8-slab rows), else one shared by both stages, whose
   // writer then waits for the previous tile's PV to finish.
-  // 4-bit rows keep one bf16 P: its rounding (2^-9 of each term) is far inside their own (2^-3).
+  // 4-bit rows keep one bf16 P: its rounding (2^-8 of a term at most) is far inside their own (2^-2 of a value).
   static constexpr bool kPSplit = LAYOUT == 1 || LAYOUT == 2;
   static constexpr uint32_t kOffPLo = kOffP + (kPInStage ? 0 : 2 * kSlab);
   static constexpr int kPLoBufs =
@@ -152,7 +152,8 @@ __global__ void __launch_bounds__(kDecodeThreads, 1)
   // The role's warp number (the list above). 4-bit rows: an MMA issuer holds up the other warps of its SM sub-partition
   // (w % 4) while the tensor cores' queue is full (traced: their converters finish a tile 1-2K cycles after the others),
   // so the converters stand three on each of the sub-partitions 0 and 1 and one beside each issuer, with the query and
-  // prefetch warps: 128 requests x 64 heads 234 us against 244 with two on each, 239 with both issuers on one.
+  // prefetch warps: 128 requests x 64 heads 234 us against 244 with two on each, 239 with both issuers on one
+  // (an L2 flush before each call; calls in a row 227 against 237).
   const int warp = C::kFp4 ? static_cast<int>(kFp4Roles >> (4 * (tid >> 5))) & 15 : tid >> 5;
   const int lane = tid & 31;
   // candidates listed per token: top-k positions (indices) or the rows of its slot runs
