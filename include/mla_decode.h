@@ -52,7 +52,8 @@
  *  Reading 4-bit rows, the decode passes the softmax weights to the value product as one
  *  bf16 each (as it does for bf16 rows; the fp8 layouts pass a pair). A NaN in a row makes NaN
  *  of every query row of its request that is computed with it, those of draft tokens before it
- *  (causal, weight zero) too. A row of a page out of range is left out of the sums.
+ *  (causal, weight zero) too; an infinity does so in its own value elements at least. A row of a
+ *  page out of range is left out of the sums.
  *  Range of the values: the decodes of the fp8 and 4-bit layouts, and of bf16 rows on the single-SM
  *  kernel, weigh rows with up to 2^64 before the sum is normalised, so a request's rows times its
  *  largest |V| must stay below 2^64 (2^20 rows of values up to 2^43); past that a sum may overflow
