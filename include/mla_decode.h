@@ -23,8 +23,8 @@
  *  - Device work is enqueued on `stream` (a cudaStream_t passed as void*;
  *    NULL = the legacy default stream) and is asynchronous. mla_decode,
  *    mla_combine, mla_combine_v_up, mla_combine_inv_rope, mla_kv_write,
- *    mla_kv_write_norm_rope, mla_qkv_norm_rope, mla_kv_read and mla_kv_gather perform no host synchronisation and
- *    no device allocation.
+ *    mla_kv_write_norm_rope, mla_qkv_norm_rope, mla_qkv_norm_rope_axes, mla_kv_read, mla_kv_gather,
+ *    mla_chunk_attention and mla_linear perform no host synchronisation and no device allocation.
  *  - bf16 = IEEE bfloat16 bit patterns (uint16); all row-major, contiguous.
  *
  * KV layouts (one page = page_size rows, page_size a power of two >= 8):
@@ -438,6 +438,106 @@ int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q
                       const int32_t* positions, const void* kv_norm_weight, float kv_eps, const float* freqs,
                       int32_t max_pos, int32_t num_tokens, int32_t num_heads, void* q_out, void* kv_cache,
                       mla_kv_layout layout, int64_t num_pages, int32_t page_size, uint32_t* status, void* stream);
+
+/*
+ * Prepare queries and append KV rows by positions of several axes (device): mla_qkv_norm_rope where a token has a position
+ * on each of num_axes axes (time, height and width of images and video; a text token has the same on all), and RoPE pair i
+ * of its queries and of its KV row turns by freqs[positions[axis_of_pair[i]][t], 2i .. 2i + 1].
+ *  positions    device int32 [num_axes, num_tokens], num_axes 1 to 4.
+ *  axis_of_pair host int32 [32], each in [0, num_axes): sections of pairs one after another, pairs of the axes in turn, or
+ *               any other order. An axis that no pair has is not read.
+ *  q_width      elements of a query row, the last 64 of them RoPE: the layout's row width (512 or 576, the absorbed
+ *               queries that mla_decode reads), or 192 beside 576-wide rows (128 NoPE: the per-head queries that
+ *               mla_chunk_attention reads; rotated only, q_norm must be 0). q_out is [num_tokens, num_heads, q_width].
+ * A token with a position outside [0, max_pos) on an axis in use writes neither its query rows nor its KV row and is
+ * reported, unless its slot and its positions on all axes in use are negative (padding). Everything else is as for
+ * mla_qkv_norm_rope: strides, in-place queries (q_out their own memory row for row; then what is not rotated or normalised
+ * is neither read nor written), refused overlaps, status.
+ */
+int mla_qkv_norm_rope_axes(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
+                           int64_t q_pe_token_stride, int64_t q_pe_head_stride, int32_t q_width, int32_t q_norm,
+                           const void* q_norm_weight, float q_eps, const void* kv_raw, int64_t kv_row_stride,
+                           const int32_t* slots, const int32_t* positions, int32_t num_axes, const int32_t* axis_of_pair,
+                           const void* kv_norm_weight, float kv_eps, const float* freqs, int32_t max_pos,
+                           int32_t num_tokens, int32_t num_heads, void* q_out, void* kv_cache, mla_kv_layout layout,
+                           int64_t num_pages, int32_t page_size, uint32_t* status, void* stream);
+
+/*
+ * Attention of chunks of new tokens over the paged cache (device), in the per-head form ("mla_attention.py ·
+ * tduncan/Nvidia-Optimization-Stack-VLLM", module docstring, Compute Friendly Approach: k_nope and v of every head come
+ * from kv_c by the up-projection, k_pe is shared by the heads; and its Chunked Prefill). Row j of a request's cache, [c_j 512 |
+ * r_j 64], gives head h the key [W_k[h] c_j | r_j] (192 wide) and the value W_v[h] c_j (128 wide). From a few hundred new
+ * tokens on this is less work than the absorbed form of mla_decode (640 operations a query, row and head against 2176, for
+ * 2^18 a row and head once).
+ *
+ * A batch is a list of requests: request b has q_lens[b] new tokens and kv_lens[b] rows in the cache, those of the new tokens
+ * last among them (they are appended before the call). Either may be 0. Its query i attends, causal, to rows
+ * j <= kv_lens[b] - q_lens[b] + i, otherwise to all rows. A query that sees no row gives zeros and an lse of -infinity.
+ *
+ * mla_chunk_plan (host): the schedule of a batch, for any number of calls (layers) with these lengths.
+ *  q_lens, kv_lens host int32 [batch].
+ *  kv_budget       bytes for K and V of the heads that are expanded at once: 512 a row (each request's rows rounded up to 128)
+ *                  and head. Where not all heads fit they go in groups, one after another; one head always goes.
+ *  num_sms         SMs of the device.
+ *  sched           host int32 [sched_capacity], or NULL to have info filled only; too short: MLA_ERR_CAPACITY, info filled.
+ *  info            what mla_chunk_attention needs beside sched, passed on as it is.
+ * Rule: the queries of a request and head are cut into tiles of 512; each is a unit for one pair of SMs, handed out head by
+ * head, longest first, to the pair that is free first by a cost of their KV tiles of 128 rows. Where there are too few units
+ * for the pairs, they are cut over the KV tiles too and their partial results merged.
+ */
+typedef struct {
+  int32_t batch, heads, causal, tokens;   /* tokens: sum of q_lens */
+  int32_t kv_rows;                        /* rows of all requests, each rounded up to 128 */
+  int32_t group;                          /* heads expanded at once */
+  int32_t pairs, items, merges, slots;
+  int64_t sched_words;                    /* length of sched */
+  size_t workspace_bytes;
+} mla_chunk_info;
+
+int mla_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int32_t batch, int32_t num_heads, int32_t causal,
+                   size_t kv_budget, int32_t num_sms, int32_t* sched, int64_t sched_capacity, mla_chunk_info* info);
+
+/*
+ * mla_chunk_attention (device):
+ *  q           device bf16 [tokens, num_heads, 192], the requests' new tokens one after another: [q_nope 128 | q_pe 64].
+ *  kv_cache    layouts 0, 2, 4 (576-wide rows). block_table device int32 [batch, max_pages], as for mla_decode. An entry
+ *              needed for a row < kv_lens[b] that is outside [0, num_pages), or past max_pages, is reported
+ *              (MLA_STATUS_BAD_PAGE) and its rows are taken as zeros.
+ *  w_kv        device bf16 [num_heads, 256, 512]: W_k (128 rows) then W_v (128 rows) of each head, the weight of
+ *              kv_b_proj as a linear layer holds it.
+ *  info, sched from mla_chunk_plan, sched copied to the device (int32 [sched_words], 16-byte aligned).
+ *  workspace   device, 256-byte aligned, info->workspace_bytes, its status header zeroed once (mla_workspace_init); one call
+ *              at a time may use it.
+ *  out         device bf16 [tokens, num_heads, 128], 32-byte aligned. lse device float [tokens, num_heads] or NULL: natural
+ *              log of the sum of e^score.
+ * K and V are rounded to bf16 once (operands of the tensor cores), as are the softmax weights; sums, maxima and the
+ * accumulator are fp32. A score, and so lse, is off by up to 2^-8 of the sum of its terms' magnitudes for K's rounding.
+ * A request's rows times its largest |V| must stay below 2^96. A NaN or infinity in a row makes NaN of query rows of the
+ * request that do not see it too, if they are computed with its tile of 128 rows.
+ */
+int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layout, int64_t num_pages, int32_t page_size,
+                        const int32_t* block_table, int32_t max_pages, const void* w_kv, float sm_scale,
+                        const mla_chunk_info* info, const int32_t* sched, void* workspace, size_t workspace_bytes, void* out,
+                        float* lse, void* stream);
+
+/*
+ * Matrix product with an epilogue (device): out = act(x weight^T + bias) + residual, for the layer's projections on either
+ * side of the attention. Sums are fp32, the result is rounded to bf16 once.
+ *  x        device bf16 [rows, inner], rows x_stride elements apart. weight device bf16 [outer, inner], contiguous, as a
+ *           linear layer holds it.
+ *  bias     device bf16 [outer] or NULL. residual device bf16 [rows, outer], rows residual_stride elements apart, or NULL.
+ *  activation MLA_ACT_NONE, MLA_ACT_SILU (y / (1 + e^-y)) or MLA_ACT_GELU (y times the normal distribution function of y).
+ *  out      device bf16 [rows, outer], rows out_stride elements apart. It may be residual's own memory, element for element;
+ *           any other overlap with an input is refused.
+ * inner and outer are multiples of 8, strides too (that of one row is not read); pointers 16-byte aligned (status 4-byte).
+ * status (device uint32 or NULL) is OR-ed with MLA_STATUS_WAIT_TIMEOUT if a bounded wait ran out.
+ */
+#define MLA_ACT_NONE 0
+#define MLA_ACT_SILU 1
+#define MLA_ACT_GELU 2
+int mla_linear(const void* x, int64_t x_stride, const void* weight, const void* bias, const void* residual,
+               int64_t residual_stride, int32_t activation, int32_t rows, int32_t inner, int32_t outer, void* out,
+               int64_t out_stride, uint32_t* status, void* stream);
 
 /*
  * Read cached rows back (device): rows[i] = the cached row at slots[i] as bf16 [n, row_elems]

@@ -46,6 +46,12 @@ class MlaError(RuntimeError):
         self.code = code
 
 
+class _ChunkInfo(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("batch", "heads", "causal", "tokens", "kv_rows", "group", "pairs", "items",
+                                                    "merges", "slots")]
+    _fields_ += [("sched_words", ctypes.c_int64), ("workspace_bytes", ctypes.c_size_t)]
+
+
 class _PlanInfo(ctypes.Structure):
     _fields_ = [("num_partitions", ctypes.c_int32), ("groups", ctypes.c_int32), ("total_splits", ctypes.c_int32),
                 ("max_splits", ctypes.c_int32), ("workspace_bytes", ctypes.c_size_t)]
@@ -54,6 +60,7 @@ class _PlanInfo(ctypes.Structure):
 EXPORTS = ["mla_page_bytes", "mla_decode_plan", "mla_decode", "mla_decode_runs", "mla_sparse_prefill", "mla_swa_plan",
            "mla_decode_static_workspace", "mla_combine",
            "mla_combine_v_up", "mla_combine_inv_rope", "mla_kv_write", "mla_kv_write_norm_rope", "mla_qkv_norm_rope",
+           "mla_qkv_norm_rope_axes", "mla_chunk_plan", "mla_chunk_attention", "mla_linear",
            "mla_kv_read", "mla_kv_gather", "mla_workspace_init", "mla_read_status",
            "mla_last_error"]
 STATIC_WORKSPACE_BYTES = 64 << 20
@@ -90,6 +97,12 @@ def load(path: str | None = None):
         lib.mla_kv_write_norm_rope.argtypes = [V, V, V, V, F32, V, I32, I32, V, I32, I64, I32, V, V]
         lib.mla_qkv_norm_rope.argtypes = [V, I64, I64, V, I64, I64, I32, V, F32, V, I64, V, V, V, F32, V, I32, I32, I32,
                                           V, V, I32, I64, I32, V, V]
+        lib.mla_qkv_norm_rope_axes.argtypes = [V, I64, I64, V, I64, I64, I32, I32, V, F32, V, I64, V, V, I32, V, V, F32, V,
+                                               I32, I32, I32, V, V, I32, I64, I32, V, V]
+        lib.mla_chunk_plan.argtypes = [V, V, I32, I32, I32, SZ, I32, V, I64, ctypes.POINTER(_ChunkInfo)]
+        lib.mla_chunk_attention.argtypes = [V, V, I32, I64, I32, V, I32, V, F32, ctypes.POINTER(_ChunkInfo), V, V, SZ, V, V,
+                                            V]
+        lib.mla_linear.argtypes = [V, I64, V, V, V, I64, I32, I32, I32, I32, V, I64, V, V]
         lib.mla_kv_read.argtypes = [V, I32, I64, I32, V, I32, V, V, V]
         lib.mla_kv_gather.argtypes = [V, I32, I64, I32, V, I32, I32, V, V]
         lib.mla_workspace_init.argtypes = [V, V]
@@ -412,6 +425,160 @@ def mla_qkv_norm_rope(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, kv
                                     slots.data_ptr(), positions.data_ptr(), kv_norm_weight.data_ptr(), float(kv_eps),
                                     freqs.data_ptr(), freqs.shape[0], T, N, q_out.data_ptr(), kv_cache.data_ptr(),
                                     layout, kv_cache.shape[0], page_size, _ptr(status), _stream(stream)))
+
+
+def mla_qkv_norm_rope_axes(q_nope, q_pe, kv_raw, slots, positions, axis_of_pair, kv_norm_weight, kv_eps: float, freqs, q_out,
+                           kv_cache, layout: int, page_size: int, q_norm_weight=None, q_eps: float | None = None,
+                           status=None, stream=None):
+    """mla_qkv_norm_rope by positions of several axes: positions int32 [A, T] (A 1 to 4), axis_of_pair 32 whole numbers below
+    A, the axis whose position turns each RoPE pair. q_nope bf16 [T, N, 512 or 448] as mla_qkv_norm_rope takes it, or
+    [T, N, 128] beside 576-wide rows (the queries of mla_chunk_attention, rotated only); q_out [T, N, its width + 64]."""
+    tensors = q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, freqs, q_out, kv_cache, q_norm_weight, status
+    _require_one_device(*tensors)
+    pb = _page_bytes(layout, page_size)
+    width = ROW_ELEMS[layout]
+    T, N, nope = q_nope.shape
+    bf16, f32, i32, u8 = _types()
+    if nope != 128 or width != 576:
+        nope = 448 if width == 512 else 512
+    if not (q_nope.dtype is q_pe.dtype is kv_raw.dtype is kv_norm_weight.dtype is q_out.dtype is bf16
+            and slots.dtype is positions.dtype is i32 and freqs.dtype is f32 and kv_cache.dtype is u8
+            and q_nope.shape == (T, N, nope) and q_pe.shape == (T, N, 64) and q_out.shape == (T, N, nope + 64)
+            and kv_raw.shape == (T, width) and slots.shape == (T,) and positions.dim() == 2 and positions.shape[1:] == (T,)
+            and kv_norm_weight.shape == (512,) and freqs.shape[1:] == (64,) and kv_cache.shape[1:] == (pb,)
+            and q_out.is_contiguous() and slots.is_contiguous() and positions.is_contiguous()
+            and kv_norm_weight.is_contiguous() and freqs.is_contiguous() and kv_cache.is_contiguous()):
+        _require("kv_cache", kv_cache, u8, None, pb)
+        _require("q_nope", q_nope, bf16, T, N, nope, contiguous=False)
+        _require("q_pe", q_pe, bf16, T, N, 64, contiguous=False)
+        _require("kv_raw", kv_raw, bf16, T, width, contiguous=False)
+        _require("slots", slots, i32, T)
+        _require("positions", positions, i32, None, T)
+        _require("kv_norm_weight", kv_norm_weight, bf16, 512)
+        _require("freqs", freqs, f32, None, 64)
+        _require("q_out", q_out, bf16, T, N, nope + 64)
+    if len(axis_of_pair) != 32:
+        raise ValueError(f"axis_of_pair must name the axis of 32 pairs, not of {len(axis_of_pair)}")
+    (qs, qh, q1), (ps, ph, p1), (rs, r1) = q_nope.stride(), q_pe.stride(), kv_raw.stride()
+    if T > 0 and not (q1 == p1 == r1 == 1):
+        raise ValueError("q_nope, q_pe and kv_raw must have their last elements adjacent")
+    if q_norm_weight is not None:
+        _require("q_norm_weight", q_norm_weight, bf16, 512)
+    _require_status(status)
+    _check(load().mla_qkv_norm_rope_axes(
+        q_nope.data_ptr(), qs, qh, q_pe.data_ptr(), ps, ph, nope + 64, q_eps is not None, _ptr(q_norm_weight),
+        0.0 if q_eps is None else float(q_eps), kv_raw.data_ptr(), rs, slots.data_ptr(), positions.data_ptr(),
+        positions.shape[0], (ctypes.c_int32 * 32)(*axis_of_pair), kv_norm_weight.data_ptr(), float(kv_eps),
+        freqs.data_ptr(), freqs.shape[0], T, N, q_out.data_ptr(), kv_cache.data_ptr(), layout, kv_cache.shape[0], page_size,
+        _ptr(status), _stream(stream)))
+
+
+@dataclasses.dataclass
+class ChunkPlan:
+    sched: np.ndarray            # int32 [sched_words], to be copied to the device
+    tokens: int                  # new tokens of all requests
+    batch: int
+    heads: int
+    group: int                   # heads whose keys and values are held at once
+    slots: int                   # partial results that are merged
+    workspace_bytes: int
+    info: _ChunkInfo
+
+
+KV_BUDGET = 8 << 30
+
+
+def mla_chunk_plan(q_lens, kv_lens, num_heads: int, causal: bool = True, kv_budget: int = KV_BUDGET,
+                   num_sms: int | None = None) -> ChunkPlan:
+    """Host plan of a batch of chunks: request b has q_lens[b] new tokens, the last of its kv_lens[b] cached rows."""
+    lib = load()
+    ql = np.ascontiguousarray(np.asarray(q_lens).astype(np.int32).ravel())
+    kl = np.ascontiguousarray(np.asarray(kv_lens).astype(np.int32).ravel())
+    if ql.shape != kl.shape:
+        raise ValueError(f"q_lens and kv_lens must have one entry a request, not {ql.shape[0]} and {kl.shape[0]}")
+    if kv_budget < 0:
+        raise ValueError("kv_budget must not be negative")
+    if num_sms is None:
+        import torch
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    info = _ChunkInfo()
+    words = 4096
+    while True:
+        sched = np.empty(words, dtype=np.int32)
+        rc = lib.mla_chunk_plan(ql.ctypes.data, kl.ctypes.data, ql.shape[0], num_heads, int(bool(causal)), int(kv_budget),
+                                num_sms, sched.ctypes.data, words, ctypes.byref(info))
+        if rc == -6 and info.sched_words > words:
+            words = info.sched_words
+            continue
+        _check(rc)
+        break
+    return ChunkPlan(sched[:info.sched_words], info.tokens, info.batch, info.heads, info.group, info.slots,
+                     info.workspace_bytes, info)
+
+
+def mla_chunk_attention(q, kv_cache, layout: int, page_size: int, block_table, w_kv, sm_scale: float, plan: ChunkPlan, sched,
+                        workspace, out, lse=None, stream=None):
+    """Attention of a batch of chunks of new tokens over their paged rows: q bf16 [T, N, 192], the requests' new tokens one
+    after another; kv_cache of 576-wide rows (layouts 0, 2, 4); block_table int32 [B, max_pages]; w_kv bf16 [N, 256, 512] (W_k
+    then W_v of each head); sched: plan.sched on the device; workspace uint8 of plan.workspace_bytes (alloc_workspace).
+    Writes out bf16 [T, N, 128] and, if given, lse float32 [T, N]."""
+    _require_one_device(q, kv_cache, block_table, w_kv, sched, workspace, out, lse)
+    bf16, f32, i32, u8 = _types()
+    T, N, B = plan.tokens, plan.heads, plan.batch
+    pb = _page_bytes(layout, page_size)
+    if not (q.dtype is w_kv.dtype is out.dtype is bf16 and block_table.dtype is sched.dtype is i32
+            and kv_cache.dtype is workspace.dtype is u8 and q.shape == (T, N, 192) and out.shape == (T, N, 128)
+            and w_kv.shape == (N, 256, 512) and kv_cache.shape[1:] == (pb,) and block_table.dim() == 2
+            and block_table.shape[0] == B and sched.shape == plan.sched.shape and q.is_contiguous() and out.is_contiguous()
+            and w_kv.is_contiguous() and kv_cache.is_contiguous() and block_table.is_contiguous() and sched.is_contiguous()
+            and workspace.is_contiguous()):
+        _require("q", q, bf16, T, N, 192)
+        _require("kv_cache", kv_cache, u8, None, pb)
+        _require("block_table", block_table, i32, B, None)
+        _require("w_kv", w_kv, bf16, N, 256, 512)
+        _require("sched", sched, i32, *plan.sched.shape)
+        _require("workspace", workspace, u8, *workspace.shape)
+        _require("out", out, bf16, T, N, 128)
+    if lse is not None:
+        _require("lse", lse, f32, T, N)
+    _check(load().mla_chunk_attention(q.data_ptr(), kv_cache.data_ptr(), layout, kv_cache.shape[0], page_size,
+                                      block_table.data_ptr(), block_table.shape[1], w_kv.data_ptr(), float(sm_scale),
+                                      ctypes.byref(plan.info), sched.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                      out.data_ptr(), _ptr(lse), _stream(stream)))
+
+
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2}
+
+
+def mla_linear(x, weight, out, bias=None, activation: str | None = None, residual=None, status=None, stream=None):
+    """out = act(x weight^T + bias) + residual: x bf16 [T, K] and residual bf16 [T, M] (or None) by the strides of their rows,
+    weight bf16 [M, K], bias bf16 [M] or None, activation None, "silu" or "gelu"; out bf16 [T, M] by its rows' stride, which may
+    be the residual itself. K and M are multiples of 8. status: optional device uint32 [1]."""
+    _require_one_device(x, weight, out, bias, residual, status)
+    bf16 = _types()[0]
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be None, 'silu' or 'gelu', not {activation!r}")
+    if x.dim() != 2 or weight.dim() != 2:
+        raise ValueError("x and weight must have two dimensions")
+    (T, K), M = x.shape, weight.shape[0]
+    if not (x.dtype is weight.dtype is out.dtype is bf16 and weight.shape == (M, K) and out.shape == (T, M)
+            and weight.is_contiguous()):
+        _require("x", x, bf16, T, K, contiguous=False)
+        _require("weight", weight, bf16, M, K)
+        _require("out", out, bf16, T, M, contiguous=False)
+    if bias is not None:
+        _require("bias", bias, bf16, M)
+    xs, x1 = x.stride()
+    os, o1 = out.stride()
+    rs, r1 = (os, 1)
+    if residual is not None:
+        _require("residual", residual, bf16, T, M, contiguous=False)
+        rs, r1 = residual.stride()
+    if T > 0 and not (x1 == o1 == r1 == 1):
+        raise ValueError("x, residual and out must have their last elements adjacent")
+    _require_status(status)
+    _check(load().mla_linear(x.data_ptr(), xs, weight.data_ptr(), _ptr(bias), _ptr(residual), rs, ACTIVATIONS[activation], T, K,
+                             M, out.data_ptr(), os, _ptr(status), _stream(stream)))
 
 
 def mla_kv_read(kv_cache, layout: int, page_size: int, slots, rows, status=None, stream=None):

@@ -19,8 +19,9 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmla_decode_gb300.so")
 
 SOURCES = ["api.cpp", "plan.cpp", "decode_sm103.cu", "decode_pair_sm103.cu", "decode_pair_fp4_sm103.cu",
-           "aux_sm103.cu", "vup_sm103.cu", "qkv_sm103.cu", "noalloc_sm103.cu"]
-HEADERS = ["mla_kernels.h", "ptx_sm103.cuh", "decode_common.cuh", "combine_row.cuh", "fp4_row.cuh", "kv_row.cuh"]
+           "aux_sm103.cu", "vup_sm103.cu", "qkv_sm103.cu", "noalloc_sm103.cu", "gemm_sm103.cu", "chunk_sm103.cu",
+           "axes_sm103.cu", "layer_api.cpp", "chunk_plan.cpp"]
+HEADERS = ["mla_kernels.h", "api_common.h", "ptx_sm103.cuh", "decode_common.cuh", "combine_row.cuh", "fp4_row.cuh", "kv_row.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -11,12 +11,15 @@
 #include <string>
 #include <vector>
 
+#include "api_common.h"
 #include "mla_decode.h"
 #include "mla_kernels.h"
 
 namespace {
-
 thread_local std::string g_last_error = "no error";
+}
+
+namespace mla {
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -32,6 +35,17 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(MLA_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+}  // namespace mla
+
+namespace {
+
+using mla::ByteRange;
+using mla::cuda_fail;
+using mla::current_sm_count;
+using mla::fail;
+using mla::layout_geometry;
+using mla::overlap;
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 int log2i(int x) {
@@ -39,6 +53,10 @@ int log2i(int x) {
   while ((1 << l) < x) ++l;
   return l;
 }
+
+}  // namespace
+
+namespace mla {
 
 int layout_geometry(int layout, int page_size, int64_t* row_bytes, int64_t* page_bytes, int* dqk) {
   switch (layout) {
@@ -72,16 +90,15 @@ int layout_geometry(int layout, int page_size, int64_t* row_bytes, int64_t* page
   }
 }
 
+}  // namespace mla
+
+namespace {
+
 // Byte range [lo, hi) that rows by strides (elements of 2 bytes) cover.
-struct ByteRange {
-  uintptr_t lo, hi;
-};
 ByteRange strided_range(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t elems) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
   return {lo, lo + 2 * static_cast<uintptr_t>((n0 - 1) * s0 + (n1 - 1) * s1 + elems)};
 }
-bool overlap(const ByteRange& a, const ByteRange& b) { return a.lo < b.hi && b.lo < a.hi; }
-
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
@@ -139,6 +156,10 @@ int pair_cluster_capacity(mla_kv_layout layout, int* n) {
   return 0;
 }
 
+}  // namespace
+
+namespace mla {
+
 int current_sm_count(int* n) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -148,9 +169,20 @@ int current_sm_count(int* n) {
   return 0;
 }
 
-}  // namespace
+int encode_bf16_map(const char* what, CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                    const cuuint64_t* strides, const cuuint32_t* box) {
+  int err = 0;
+  EncodeTiledFn encode = get_encode_fn(&err);
+  if (err) return fail(MLA_ERR_CUDA, "%s: cuTensorMapEncodeTiled is unavailable", what);
+  const cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  std::memset(map, 0, sizeof *map);
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims,
+                            strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MLA_ERR_CUDA, "%s: encoding the tensor map failed (%d)", what, static_cast<int>(r));
+  return 0;
+}
 
-namespace mla {
 // Lets other translation units of the library report a failure through mla_last_error().
 int set_last_error(int code, const char* msg) {
   g_last_error = msg;
@@ -577,51 +609,56 @@ int mla_kv_write_norm_rope(const void* raw, const int32_t* slots, const int32_t*
   return MLA_OK;
 }
 
-int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
-                      int64_t q_pe_token_stride, int64_t q_pe_head_stride, int32_t q_norm, const void* q_norm_weight,
-                      float q_eps, const void* kv_raw, int64_t kv_row_stride, const int32_t* slots,
-                      const int32_t* positions, const void* kv_norm_weight, float kv_eps, const float* freqs,
-                      int32_t max_pos, int32_t num_tokens, int32_t num_heads, void* q_out, void* kv_cache,
-                      mla_kv_layout layout, int64_t num_pages, int32_t page_size, uint32_t* status, void* stream) {
-  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: num_tokens < 0");
-  if (num_tokens == 0) return MLA_OK;
+}  // extern "C"
+
+namespace {
+// The checks that mla_qkv_norm_rope and mla_qkv_norm_rope_axes share, and the parameters of their launch. q_width: elements
+// of a query row, its last 64 RoPE (0: the layout's); `axes` position lists. *nope_here: the queries' NoPE part is q_out's own.
+int qkv_params(const char* name, const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
+               int64_t q_pe_token_stride, int64_t q_pe_head_stride, int32_t q_width, int32_t q_norm, const void* q_norm_weight,
+               float q_eps, const void* kv_raw, int64_t kv_row_stride, const int32_t* slots, const int32_t* positions,
+               int32_t axes, const void* kv_norm_weight, float kv_eps, const float* freqs, int32_t max_pos, int32_t num_tokens,
+               int32_t num_heads, void* q_out, void* kv_cache, mla_kv_layout layout, int64_t num_pages, int32_t page_size,
+               uint32_t* status, mla::QkvParams* params, bool* q_nope_here) {
   if (!q_nope || !q_pe || !kv_raw || !slots || !positions || !kv_norm_weight || !freqs || !q_out || !kv_cache)
-    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: NULL pointer");
+    return fail(MLA_ERR_INVALID_ARG, "%s: NULL pointer", name);
   int64_t rb, pb;
   int dqk;
   if (layout_geometry(layout, page_size, &rb, &pb, &dqk) != 0)
-    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: unknown layout %d", static_cast<int>(layout));
+    return fail(MLA_ERR_INVALID_ARG, "%s: unknown layout %d", name, static_cast<int>(layout));
   if (!pow2(page_size))
-    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: page_size %d not a power of two", page_size);
+    return fail(MLA_ERR_INVALID_ARG, "%s: page_size %d not a power of two", name, page_size);
   if (num_heads < 1 || num_pages < 1 || max_pos < 1)
-    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: num_heads, num_pages and max_pos must be >= 1");
+    return fail(MLA_ERR_INVALID_ARG, "%s: num_heads, num_pages and max_pos must be >= 1", name);
   if (static_cast<int64_t>(num_tokens) * num_heads >= (1ll << 31))
-    return fail(MLA_ERR_UNSUPPORTED, "mla_qkv_norm_rope: too many query rows");
+    return fail(MLA_ERR_UNSUPPORTED, "%s: too many query rows", name);
   if (!(kv_eps >= 0.f) || !(kv_eps < 1e30f) || (q_norm && (!(q_eps >= 0.f) || !(q_eps < 1e30f))))
-    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: eps must be a finite number >= 0");
+    return fail(MLA_ERR_INVALID_ARG, "%s: eps must be a finite number >= 0", name);
   if (!q_norm && q_norm_weight != nullptr)
-    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: q_norm_weight given without q_norm");
+    return fail(MLA_ERR_INVALID_ARG, "%s: q_norm_weight given without q_norm", name);
+  const int row = dqk;  // of the cache
+  if (q_width != 0) dqk = q_width;
   // a dimension of size one has whatever stride its history left: taken as that of rows that follow one another
   if (num_tokens == 1) {
     q_nope_token_stride = q_pe_token_stride = static_cast<int64_t>(num_heads) * dqk;
-    kv_row_stride = dqk;
+    kv_row_stride = row;
   }
   if (num_heads == 1) q_nope_head_stride = q_pe_head_stride = dqk;
   const int64_t strides[5] = {q_nope_token_stride, q_nope_head_stride, q_pe_token_stride, q_pe_head_stride,
                               kv_row_stride};
   for (int64_t s : strides)
     if (s < 0 || s % 8 != 0 || s >= (1ll << 40))
-      return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: stride %lld must be a multiple of 8 elements >= 0",
+      return fail(MLA_ERR_INVALID_ARG, "%s: stride %lld must be a multiple of 8 elements >= 0", name,
                   static_cast<long long>(s));
   for (int i = 0; i < 5; ++i)  // (so that the ranges below fit 64 bits)
     if (strides[i] > (1ll << 46) / ((i == 1 || i == 3) ? num_heads : num_tokens))
-      return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: stride %lld is past any memory",
+      return fail(MLA_ERR_INVALID_ARG, "%s: stride %lld is past any memory", name,
                   static_cast<long long>(strides[i]));
   if (!aligned16(q_nope) || !aligned16(q_pe) || !aligned16(q_norm_weight) || !aligned16(kv_raw) ||
       !aligned16(kv_norm_weight) || !aligned16(freqs) || !aligned16(q_out) || !aligned16(kv_cache))
-    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: pointers must be 16-byte aligned");
+    return fail(MLA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", name);
   // q_out may be the queries' own memory, row for row; any other overlap would race
-  const int nope = dqk == 512 ? 448 : 512;
+  const int nope = dqk - 64;
   const int64_t T = num_tokens, N = num_heads;
   const ByteRange out = strided_range(q_out, T, N * dqk, N, dqk, dqk);
   const uint16_t* qo = static_cast<const uint16_t*>(q_out);
@@ -629,20 +666,20 @@ int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q
   const bool pe_here = q_pe == qo + nope && q_pe_token_stride == N * dqk && q_pe_head_stride == dqk;
   if ((!nope_here && overlap(out, strided_range(q_nope, T, q_nope_token_stride, N, q_nope_head_stride, nope))) ||
       (!pe_here && overlap(out, strided_range(q_pe, T, q_pe_token_stride, N, q_pe_head_stride, 64))) ||
-      overlap(out, strided_range(kv_raw, T, kv_row_stride, 1, 0, dqk)))
-    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: q_out overlaps an input other than row for row");
+      overlap(out, strided_range(kv_raw, T, kv_row_stride, 1, 0, row)))
+    return fail(MLA_ERR_INVALID_ARG, "%s: q_out overlaps an input other than row for row", name);
   const uintptr_t cache = reinterpret_cast<uintptr_t>(kv_cache);
   const ByteRange kv = {cache, cache + static_cast<uintptr_t>(num_pages) * static_cast<uintptr_t>(pb)};
   if (overlap(kv, out) || overlap(kv, strided_range(q_nope, T, q_nope_token_stride, N, q_nope_head_stride, nope)) ||
       overlap(kv, strided_range(q_pe, T, q_pe_token_stride, N, q_pe_head_stride, 64)) ||
-      overlap(kv, strided_range(kv_raw, T, kv_row_stride, 1, 0, dqk)))
-    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: kv_cache overlaps the queries or the rows");
+      overlap(kv, strided_range(kv_raw, T, kv_row_stride, 1, 0, row)))
+    return fail(MLA_ERR_INVALID_ARG, "%s: kv_cache overlaps the queries or the rows", name);
   const int64_t index_bytes = 4 * T;
   const struct {
     const void* p;
     int64_t bytes;
   } small[] = {{slots, index_bytes},
-               {positions, index_bytes},
+               {positions, axes * index_bytes},
                {kv_norm_weight, 1024},
                {q_norm_weight, 1024},
                {freqs, static_cast<int64_t>(max_pos) * 256}};
@@ -651,9 +688,9 @@ int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q
     const uintptr_t lo = reinterpret_cast<uintptr_t>(in.p);
     const ByteRange r = {lo, lo + static_cast<uintptr_t>(in.bytes)};
     if (overlap(out, r) || overlap(kv, r))
-      return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: q_out or kv_cache overlaps slots, positions, a gain or freqs");
+      return fail(MLA_ERR_INVALID_ARG, "%s: q_out or kv_cache overlaps slots, positions, a gain or freqs", name);
   }
-  mla::QkvParams p;
+  mla::QkvParams& p = *params;
   std::memset(&p, 0, sizeof p);
   p.q_nope = static_cast<const uint16_t*>(q_nope);
   p.q_pe = static_cast<const uint16_t*>(q_pe);
@@ -681,8 +718,72 @@ int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q
   p.heads = num_heads;
   p.layout = static_cast<int>(layout);
   p.page_size = page_size;
+  *q_nope_here = nope_here;
+  return MLA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+int mla_qkv_norm_rope(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
+                      int64_t q_pe_token_stride, int64_t q_pe_head_stride, int32_t q_norm, const void* q_norm_weight,
+                      float q_eps, const void* kv_raw, int64_t kv_row_stride, const int32_t* slots,
+                      const int32_t* positions, const void* kv_norm_weight, float kv_eps, const float* freqs,
+                      int32_t max_pos, int32_t num_tokens, int32_t num_heads, void* q_out, void* kv_cache,
+                      mla_kv_layout layout, int64_t num_pages, int32_t page_size, uint32_t* status, void* stream) {
+  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope: num_tokens < 0");
+  if (num_tokens == 0) return MLA_OK;
+  mla::QkvParams p;
+  bool nope_here;
+  if (int rc = qkv_params("mla_qkv_norm_rope", q_nope, q_nope_token_stride, q_nope_head_stride, q_pe, q_pe_token_stride,
+                          q_pe_head_stride, 0, q_norm, q_norm_weight, q_eps, kv_raw, kv_row_stride, slots, positions, 1,
+                          kv_norm_weight, kv_eps, freqs, max_pos, num_tokens, num_heads, q_out, kv_cache, layout, num_pages,
+                          page_size, status, &p, &nope_here))
+    return rc;
   cudaError_t e = mla::launch_qkv_norm_rope(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "mla_qkv_norm_rope: launch");
+  return MLA_OK;
+}
+
+int mla_qkv_norm_rope_axes(const void* q_nope, int64_t q_nope_token_stride, int64_t q_nope_head_stride, const void* q_pe,
+                           int64_t q_pe_token_stride, int64_t q_pe_head_stride, int32_t q_width, int32_t q_norm,
+                           const void* q_norm_weight, float q_eps, const void* kv_raw, int64_t kv_row_stride,
+                           const int32_t* slots, const int32_t* positions, int32_t num_axes, const int32_t* axis_of_pair,
+                           const void* kv_norm_weight, float kv_eps, const float* freqs, int32_t max_pos, int32_t num_tokens,
+                           int32_t num_heads, void* q_out, void* kv_cache, mla_kv_layout layout, int64_t num_pages,
+                           int32_t page_size, uint32_t* status, void* stream) {
+  if (num_tokens < 0) return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope_axes: num_tokens < 0");
+  if (num_tokens == 0) return MLA_OK;
+  if (axis_of_pair == nullptr) return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope_axes: NULL pointer");
+  if (num_axes < 1 || num_axes > 4)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_qkv_norm_rope_axes: %d axes, not 1 to 4", num_axes);
+  mla::AxesParams a;
+  std::memset(&a, 0, sizeof a);
+  for (int i = 0; i < 32; ++i) {
+    if (axis_of_pair[i] < 0 || axis_of_pair[i] >= num_axes)
+      return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope_axes: pair %d has axis %d of %d", i, axis_of_pair[i], num_axes);
+    a.axis_of_pair |= static_cast<uint64_t>(axis_of_pair[i]) << (2 * i);
+    a.used_axes |= 1u << axis_of_pair[i];
+  }
+  int64_t rb, pb;
+  int dqk;
+  if (layout_geometry(layout, page_size, &rb, &pb, &dqk) != 0)
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope_axes: unknown layout %d", static_cast<int>(layout));
+  if (q_width != dqk && !(q_width == 192 && dqk == 576))
+    return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope_axes: q_width %d is neither the row's %d nor 192 beside 576-wide rows",
+                q_width, dqk);
+  if (q_norm && q_width == 192)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_qkv_norm_rope_axes: 192-wide queries are rotated only");
+  bool nope_here;
+  if (int rc = qkv_params("mla_qkv_norm_rope_axes", q_nope, q_nope_token_stride, q_nope_head_stride, q_pe, q_pe_token_stride,
+                          q_pe_head_stride, q_width, q_norm, q_norm_weight, q_eps, kv_raw, kv_row_stride, slots, positions,
+                          num_axes, kv_norm_weight, kv_eps, freqs, max_pos, num_tokens, num_heads, q_out, kv_cache, layout,
+                          num_pages, page_size, status, &a.qkv, &nope_here))
+    return rc;
+  a.q_width = q_width;
+  a.copy_nope = q_norm || !nope_here;
+  cudaError_t e = mla::launch_qkv_norm_rope_axes(a, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "mla_qkv_norm_rope_axes: launch");
   return MLA_OK;
 }
 

@@ -34,6 +34,30 @@ __device__ __forceinline__ float fast_exp2(float x) {
   return y;
 }
 
+// the largest of three; a NaN gives way to a number
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// (a.x, a.y) * (b, b) + (c.x, c.y), and a + b, two lanes an instruction
+__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
+  float2 r;
+  asm("{\n .reg .b64 p, q, s, d;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %4};\n mov.b64 s, {%5, %6};\n"
+      " fma.rn.f32x2 d, p, q, s;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n .reg .b64 p, q, d;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n add.rn.f32x2 d, p, q;\n"
+      " mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // mbar_wait (and mbar_wait_cluster) in few instructions, bounded the same way. The roles of a CTA run at once from
 // one instruction cache, and those functions inlined at each wait were a third of the 4-bit pair kernel's code
 // (instruction fetches were a sixth of all stalls; a call instead costs the registers that live across it: 132 us

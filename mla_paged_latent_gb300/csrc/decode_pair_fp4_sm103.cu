@@ -116,29 +116,6 @@ __device__ __forceinline__ void mma_bf16_pair_lo(uint32_t d, uint32_t a_lo, uint
       : "memory");
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// (a.x, a.y) * (b, b) + (c.x, c.y), and a + b, two lanes an instruction
-__device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
-  float2 r;
-  asm("{\n .reg .b64 p, q, s, d;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %4};\n mov.b64 s, {%5, %6};\n"
-      " fma.rn.f32x2 d, p, q, s;\n mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
-  return r;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 r;
-  asm("{\n .reg .b64 p, q, d;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n add.rn.f32x2 d, p, q;\n"
-      " mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(r.x), "=f"(r.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return r;
-}
-
 // 16 bytes of global memory to shared memory, past the registers; zeros where `on` is false.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");

@@ -1,0 +1,424 @@
+// Matrix products with an epilogue: y = act(x W^T + bias) + residual, bf16 in and out, fp32 sums.
+//
+// x [T, K] and W [M, K] are K-major, so both operands come from memory in the tensor cores' own order (128-byte swizzled
+// slabs of 64 elements of K, by TMA; what lies past an extent arrives as zeros). Bias, activation and residual are applied
+// to the fp32 sum and the result is rounded to bf16 once.
+//
+// gemm_pair_kernel: many rows. Two SMs work as one tensor-core pair (tcgen05 .cta_group::2) on a tile of 256 rows x 256
+// columns: each holds its 128 rows of x and half of W's 256 rows of a slab, 32 KB a step of 64 in K for 2 x 256 x 256 x 64
+// operations, half of what two single SMs would move. Sums lie in TMEM twice, so that one tile's epilogue runs under the
+// next one's products. Bound by the tensor cores.
+//
+// gemm_narrow_kernel: few rows. Bound by W's bytes, so W takes the M side of the instruction (128 of its rows a CTA) and
+// the rows of x the N side (16 to 128), and K is split over the CTAs of a cluster, whose sums meet through distributed
+// shared memory in the order of their ranks: no workspace, no atomics, the same result every time.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "decode_common.cuh"
+#include "mla_kernels.h"
+#include "ptx_sm103.cuh"
+
+namespace mla {
+namespace {
+
+__device__ __forceinline__ float activate(float y, int act) {
+  if (act == 1) return __fdividef(y, 1.f + __expf(-y));  // silu
+  // gelu y Phi(y); erfc keeps its relative precision where 1 + erf would cancel
+  if (act == 2) return 0.5f * y * erfcf(y * -0.70710678118654752f);
+  return y;
+}
+
+// ----------------------------------------------------------------------------- CTA pairs
+constexpr int kGemmThreads = 192;              // TMA, MMA, 4 epilogue warps
+constexpr int kGemmStages = 6;
+constexpr uint32_t kGemmA = 128 * 128;         // this CTA's 128 rows of x, 64 of K
+constexpr uint32_t kGemmB = 128 * 128;         // its half of W's 256 rows
+constexpr uint32_t kGemmStage = kGemmA + kGemmB;
+constexpr uint32_t kGemmOffStaging = kGemmStages * kGemmStage;
+constexpr uint32_t kGemmSlab = 32 * 128;       // 32 rows x 64 columns of the result: one warp's store
+constexpr uint32_t kGemmOffMisc = kGemmOffStaging + 4 * 2 * kGemmSlab;
+
+struct GemmMisc {
+  uint64_t full[kGemmStages], empty[kGemmStages];  // full: in the even CTA, both CTAs' bytes
+  uint64_t acc_full[2], acc_empty[2];              // acc_empty: in the even CTA, 8 warps
+  uint64_t last;
+  uint32_t tmem_base;
+  int abort;
+  unsigned int status;  // where the caller gave none
+};
+constexpr size_t kGemmSmem = kGemmOffMisc + sizeof(GemmMisc) + 1024;
+static_assert(kGemmSmem <= 232448, "shared memory budget of one CTA");
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+    gemm_pair_kernel(const __grid_constant__ GemmParams P, const __grid_constant__ CUtensorMap x_map,
+                     const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap y_map) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_addr(smem);
+  GemmMisc* misc = reinterpret_cast<GemmMisc*>(smem + kGemmOffMisc);
+  volatile int* abort_flag = &misc->abort;
+  unsigned int* status = P.status != nullptr ? P.status : &misc->status;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  auto lead = [&](uint64_t* b) -> uint32_t { return map_shared_rank(smem_addr(b), 0); };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kGemmStages; ++s) {
+      mbar_init(smem_addr(&misc->full[s]), 2);
+      mbar_init(smem_addr(&misc->empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_addr(&misc->acc_full[b]), 1);
+      mbar_init(smem_addr(&misc->acc_empty[b]), 8);
+    }
+    mbar_init(smem_addr(&misc->last), 1);
+    misc->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_addr(&misc->tmem_base), 512);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers exist before any remote arrive
+  tc_fence_after();
+  pdl_trigger();
+  pdl_wait();
+  const uint32_t tmem = misc->tmem_base;
+  const int tiles = P.m_tiles * P.n_tiles;
+  const int step = static_cast<int>(num_clusters_x());
+  // Tiles in bands of `band` row tiles, row tiles fastest: the pairs that run at once share both operands through L2.
+  auto place = [&](int t, int* m0, int* n0) {
+    const int b = t / (P.band * P.n_tiles), r = t - b * P.band * P.n_tiles;
+    const int h = min(P.band, P.m_tiles - b * P.band);
+    *m0 = (b * P.band + r % h) * 256;
+    *n0 = (r / h) * 256;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&x_map);
+      tma_prefetch_desc(&w_map);
+      int it = 0;
+      bool ok = true;
+      for (int t = cluster_id_x(); t < tiles && ok; t += step) {
+        int m0, n0;
+        place(t, &m0, &n0);
+        for (int k = 0; k < P.k_blocks; ++k, ++it) {
+          const int s = it % kGemmStages;
+          const uint32_t a = sb + s * kGemmStage;
+          if (it >= kGemmStages &&
+              !wait_bar(smem_addr(&misc->empty[s]), (it / kGemmStages - 1) & 1, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = lead(&misc->full[s]);
+          mbar_arrive_expect_tx_cluster(full, kGemmStage);
+          tma_load_2d_pair(a, &x_map, 64 * k, m0 + 128 * rank, full);
+          tma_load_2d_pair(a + kGemmA, &w_map, 64 * k, P.w_row0 + n0 + 128 * rank, full);
+        }
+      }
+      if (*abort_flag && rank == 0)  // copies still in flight land on this CTA's barriers: wait for them (bounded)
+        for (int k = 1; k <= kGemmStages && it - k >= 0; ++k)
+          mbar_wait_drain_cluster(smem_addr(&misc->full[(it - k) % kGemmStages]), ((it - k) / kGemmStages) & 1);
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, 0, 0);
+      const uint64_t kmaj = sdesc_sw128(0, 16, 1024);
+      int it = 0, u = 0;
+      bool ok = true;
+      for (int t = cluster_id_x(); t < tiles && ok; t += step, ++u) {
+        const int buf = u & 1;
+        if (u >= 2 && !wait_bar(smem_addr(&misc->acc_empty[buf]), ((u >> 1) - 1) & 1, abort_flag, status)) break;
+        tc_fence_after();
+        for (int k = 0; k < P.k_blocks; ++k, ++it) {
+          const int s = it % kGemmStages;
+          if (!wait_bar(smem_addr(&misc->full[s]), (it / kGemmStages) & 1, abort_flag, status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t a = kmaj | ((sb + s * kGemmStage) >> 4);
+          const uint64_t b = kmaj | ((sb + s * kGemmStage + kGemmA) >> 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mma_bf16_pair(tmem + buf * 256, a + 2 * i, b + 2 * i, idesc, (k | i) ? 1u : 0u);
+          mma_commit_pair(smem_addr(&misc->empty[s]), 3);
+        }
+        if (ok) mma_commit_pair(smem_addr(&misc->acc_full[buf]), 3);
+      }
+      mma_commit_pair(smem_addr(&misc->last), 1);
+      mbar_wait_drain_cluster(smem_addr(&misc->last), 0);
+    }
+  } else {
+    // Epilogue: a warp reaches the TMEM lanes 32 (warp % 4) .. + 31, one row a lane. 64 columns at a time go through the
+    // warp's own two 4-KB slabs to a TMA store, so that rows leave as whole 128-byte lines.
+    const int quarter = warp & 3;
+    const uint32_t staging = sb + kGemmOffStaging + quarter * 2 * kGemmSlab;
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+    int u = 0, stores = 0;
+    for (int t = cluster_id_x(); t < tiles; t += step, ++u) {
+      int m0, n0;
+      place(t, &m0, &n0);
+      const int buf = u & 1;
+      const int row0 = m0 + 128 * rank + 32 * quarter;
+      if (!wait_bar(smem_addr(&misc->acc_full[buf]), (u >> 1) & 1, abort_flag, status)) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        const int col0 = n0 + 64 * c;
+        if (row0 >= P.rows || col0 >= P.cols) break;  // (the same in all lanes)
+        const int row = row0 + lane;
+        const int chunks = min(8, (P.cols - col0) >> 3);  // of 8 columns
+        uint32_t acc[64];
+        tmem_ld32(tmem + buf * 256 + lane_off + 64 * c, acc);
+        tmem_ld32(tmem + buf * 256 + lane_off + 64 * c + 32, acc + 32);
+        uint4 res[8];
+        const bool add = P.residual != nullptr && row < P.rows;
+        const uint16_t* rp = P.residual + row * P.residual_stride + col0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          res[q] = add && q < chunks ? *reinterpret_cast<const uint4*>(rp + 8 * q) : make_uint4(0, 0, 0, 0);
+        tmem_wait_ld();
+        if (stores >= 2) {
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+        }
+        const uint32_t slab = staging + (stores & 1) * kGemmSlab;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint4 bu = P.bias != nullptr && q < chunks ? *reinterpret_cast<const uint4*>(P.bias + col0 + 8 * q)
+                                                           : make_uint4(0, 0, 0, 0);
+          const uint32_t bh[4] = {bu.x, bu.y, bu.z, bu.w}, rh[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float y0 = __uint_as_float(acc[8 * q + 2 * i]), y1 = __uint_as_float(acc[8 * q + 2 * i + 1]);
+            if (P.bias != nullptr) {
+              y0 += __uint_as_float(bh[i] << 16);
+              y1 += __uint_as_float(bh[i] & 0xFFFF0000u);
+            }
+            if (P.act != 0) {
+              y0 = activate(y0, P.act);
+              y1 = activate(y1, P.act);
+            }
+            if (add) {
+              y0 += __uint_as_float(rh[i] << 16);
+              y1 += __uint_as_float(rh[i] & 0xFFFF0000u);
+            }
+            o[i] = f32x2_to_bf16x2(y0, y1);
+          }
+          st_shared_v4(slab + lane * 128 + ((q ^ (lane & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&y_map, slab, col0, row0);
+          bulk_commit();
+        }
+        ++stores;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(lead(&misc->acc_empty[buf]));
+    }
+    if (lane == 0) bulk_wait<0>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // the even CTA's MMAs into both CTAs' TMEM have completed
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ----------------------------------------------------------------------------- few rows
+constexpr int kNarrowThreads = 192;
+
+struct NarrowMisc {
+  uint64_t full[16], empty[16], acc_full;
+  uint32_t tmem_base;
+  int abort;
+  unsigned int status;
+};
+
+// NT rows of x a CTA. Stages fill 96 KB, so that two CTAs share an SM and one's first loads run under the other's last
+// sums.
+template <int NT>
+struct Narrow {
+  static constexpr uint32_t kW = 128 * 128;
+  static constexpr uint32_t kX = NT * 128;
+  static constexpr uint32_t kStage = kW + kX;
+  static constexpr int kStages = 98304 / kStage;
+  static constexpr uint32_t kOffMisc = kStages * kStage;
+  static constexpr size_t kSmem = kOffMisc + sizeof(NarrowMisc) + 1024;
+  static_assert(kStages <= 16 && NT * 128 * 4 <= kOffMisc, "");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kNarrowThreads)
+    gemm_narrow_kernel(const __grid_constant__ GemmParams P, const __grid_constant__ CUtensorMap x_map,
+                       const __grid_constant__ CUtensorMap w_map) {
+  using C = Narrow<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sb = smem_addr(smem);
+  NarrowMisc* misc = reinterpret_cast<NarrowMisc*>(smem + C::kOffMisc);
+  volatile int* abort_flag = &misc->abort;
+  unsigned int* status = P.status != nullptr ? P.status : &misc->status;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int parts = P.split;  // CTAs of the cluster
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(smem_addr(&misc->full[s]), 1);
+      mbar_init(smem_addr(&misc->empty[s]), 1);
+    }
+    mbar_init(smem_addr(&misc->acc_full), 1);
+    misc->abort = 0;
+    fence_mbar_init();
+  }
+  constexpr uint32_t kCols = NT < 32 ? 32 : NT;
+  if (warp == 1) {
+    tmem_alloc(smem_addr(&misc->tmem_base), kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_trigger();
+  pdl_wait();
+  const uint32_t tmem = misc->tmem_base;
+  const int tile = static_cast<int>(blockIdx.x) / parts;
+  const int f0 = (tile % P.n_tiles) * 128, t0 = (tile / P.n_tiles) * NT;
+  const int k0 = static_cast<int>(static_cast<int64_t>(P.k_blocks) * rank / parts);
+  const int k1 = static_cast<int>(static_cast<int64_t>(P.k_blocks) * (rank + 1) / parts);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&x_map);
+      tma_prefetch_desc(&w_map);
+      int it = 0;
+      for (int k = k0; k < k1; ++k, ++it) {
+        const int s = it % C::kStages;
+        if (it >= C::kStages && !wait_bar(smem_addr(&misc->empty[s]), (it / C::kStages - 1) & 1, abort_flag, status))
+          break;
+        const uint32_t full = smem_addr(&misc->full[s]);
+        mbar_arrive_expect_tx(full, C::kStage);
+        tma_load_2d(sb + s * C::kStage, &w_map, 64 * k, f0, full);
+        tma_load_2d(sb + s * C::kStage + C::kW, &x_map, 64 * k, t0, full);
+      }
+      if (*abort_flag)
+        for (int k = 1; k <= C::kStages && it - k >= 0; ++k)
+          mbar_wait_drain(smem_addr(&misc->full[(it - k) % C::kStages]), ((it - k) / C::kStages) & 1);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(128, NT, 0, 0);
+      const uint64_t kmaj = sdesc_sw128(0, 16, 1024);
+      int it = 0;
+      for (int k = k0; k < k1; ++k, ++it) {
+        const int s = it % C::kStages;
+        if (!wait_bar(smem_addr(&misc->full[s]), (it / C::kStages) & 1, abort_flag, status)) break;
+        tc_fence_after();
+        const uint64_t a = kmaj | ((sb + s * C::kStage) >> 4);
+        const uint64_t b = kmaj | ((sb + s * C::kStage + C::kW) >> 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mma_bf16_ss(tmem, a + 2 * i, b + 2 * i, idesc, (it | i) ? 1u : 0u);
+        mma_commit(smem_addr(&misc->empty[s]));
+      }
+      mma_commit(smem_addr(&misc->acc_full));
+    }
+  } else {
+    // this CTA's sums to its own shared memory [row of x][feature] (the stages are free: every product has completed)
+    const int quarter = warp & 3;
+    const bool ok = wait_bar(smem_addr(&misc->acc_full), 0, abort_flag, status);
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < NT; c += 16) {
+      uint32_t r[16];
+      tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        reinterpret_cast<float*>(smem)[(c + i) * 128 + quarter * 32 + lane] =
+            ok && k1 > k0 ? __uint_as_float(r[i]) : 0.f;
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync_all();
+  // rank r sums and writes every parts-th row: 64 threads a row, two features each
+  for (int i = (threadIdx.x >> 6) * parts + rank; i < NT && t0 + i < P.rows; i += (kNarrowThreads >> 6) * parts) {
+    const int f = 2 * (threadIdx.x & 63);
+    if (f0 + f >= P.cols) continue;
+    const uint32_t at = sb + (i * 128 + f) * 4;
+    float y0 = 0.f, y1 = 0.f;
+    for (int p = 0; p < parts; ++p) {
+      const uint32_t peer = map_shared_rank(at, p);
+      y0 += ld_shared_cluster_f32(peer);
+      y1 += ld_shared_cluster_f32(peer + 4);
+    }
+    if (P.bias != nullptr) {
+      const uint32_t b = *reinterpret_cast<const uint32_t*>(P.bias + f0 + f);
+      y0 += __uint_as_float(b << 16);
+      y1 += __uint_as_float(b & 0xFFFF0000u);
+    }
+    if (P.act != 0) {
+      y0 = activate(y0, P.act);
+      y1 = activate(y1, P.act);
+    }
+    if (P.residual != nullptr) {
+      const uint32_t r = *reinterpret_cast<const uint32_t*>(P.residual + (t0 + i) * P.residual_stride + f0 + f);
+      y0 += __uint_as_float(r << 16);
+      y1 += __uint_as_float(r & 0xFFFF0000u);
+    }
+    *reinterpret_cast<uint32_t*>(P.out + static_cast<int64_t>(t0 + i) * P.out_stride + f0 + f) = f32x2_to_bf16x2(y0, y1);
+  }
+  cluster_sync_all();  // no CTA leaves while a peer reads its sums
+  if (warp == 1) tmem_dealloc(tmem, kCols);
+}
+
+template <int NT>
+cudaError_t narrow(const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map, int grid, cudaStream_t stream) {
+  auto kern = gemm_narrow_kernel<NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Narrow<NT>::kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kNarrowThreads);
+  cfg.dynamicSmemBytes = Narrow<NT>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, p, x_map, w_map);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_pair(const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,
+                             const CUtensorMap& y_map, int clusters, cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(gemm_pair_kernel, dim3(2 * clusters), dim3(kGemmThreads), kGemmSmem, stream, p, x_map, w_map, y_map);
+}
+
+cudaError_t launch_gemm_narrow(int rows_a_cta, const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,
+                               int grid, cudaStream_t stream) {
+  switch (rows_a_cta) {
+    case 16: return narrow<16>(p, x_map, w_map, grid, stream);
+    case 32: return narrow<32>(p, x_map, w_map, grid, stream);
+    case 64: return narrow<64>(p, x_map, w_map, grid, stream);
+    default: return narrow<128>(p, x_map, w_map, grid, stream);
+  }
+}
+
+}  // namespace mla

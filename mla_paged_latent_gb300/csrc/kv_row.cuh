@@ -172,9 +172,10 @@ __device__ __forceinline__ void write_any_row(const uint16_t* x, int lane, uint8
 // RMSNorm of the 512 latent elements and RoPE of the 64 RoPE elements of one raw row x
 // (16-byte aligned), in fp32, rounded once to bf16 into srow (shared memory; all lanes of the warp
 // take part, and it ends with a __syncwarp). Lane l holds latent elements [16 l, 16 l + 16) and
-// RoPE pair l of the 576-wide layouts; f is the position's row of the (cos, sin) table.
-__device__ __forceinline__ void norm_rope_row(const uint16_t* x, const uint16_t* w, float eps,
-                                              const float* f, int width, int lane, uint16_t* srow) {
+// RoPE pair l of the 576-wide layouts; angle(i) is pair i's (cos, sin).
+template <class Angle>
+__device__ __forceinline__ void norm_rope_row_by(const uint16_t* x, const uint16_t* w, float eps,
+                                                 Angle angle, int width, int lane, uint16_t* srow) {
   float v[16];
   {
     const uint4 a = reinterpret_cast<const uint4*>(x)[2 * lane];
@@ -206,8 +207,8 @@ __device__ __forceinline__ void norm_rope_row(const uint16_t* x, const uint16_t*
     // 512-wide row: elements 448..511 (lanes 28-31) are the RoPE part, rotated after the norm
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int i = 8 * (lane - 28) + k;
-      const float c = f[2 * i], s = f[2 * i + 1];
+      const float2 cs = angle(8 * (lane - 28) + k);
+      const float c = cs.x, s = cs.y;
       const float x0 = v[2 * k], x1 = v[2 * k + 1];
       v[2 * k] = x0 * c - x1 * s;
       v[2 * k + 1] = x0 * s + x1 * c;
@@ -222,10 +223,66 @@ __device__ __forceinline__ void norm_rope_row(const uint16_t* x, const uint16_t*
     // k_pe (elements 512..575) is rotated as it comes, without the norm
     const uint32_t two = reinterpret_cast<const uint32_t*>(x + 512)[lane];
     const float x0 = bf16_to_f32(two & 0xFFFFu), x1 = bf16_to_f32(two >> 16);
-    const float c = f[2 * lane], s = f[2 * lane + 1];
+    const float2 cs = angle(lane);
+    const float c = cs.x, s = cs.y;
     reinterpret_cast<uint32_t*>(srow + 512)[lane] = f32x2_to_bf16x2(x0 * c - x1 * s, x0 * s + x1 * c);
   }
   __syncwarp();
+}
+
+// The same with f the position's row of the (cos, sin) table.
+__device__ __forceinline__ void norm_rope_row(const uint16_t* x, const uint16_t* w, float eps,
+                                              const float* f, int width, int lane, uint16_t* srow) {
+  norm_rope_row_by(x, w, eps, [&](int i) { return make_float2(f[2 * i], f[2 * i + 1]); }, width, lane, srow);
+}
+
+// The row at offset `off` of the page pg, decoded to bf16 into dst, by one warp. A lane takes eight elements a step, so
+// loads and stores of a warp are contiguous.
+template <int LAYOUT>
+__device__ __forceinline__ void read_row(const uint8_t* pg, int off, int page_size, int lane, uint4* dst) {
+  constexpr int kNope = row_nope(LAYOUT), kRowBytes = row_stored_bytes(LAYOUT);
+  constexpr int kCodeBytes = LAYOUT == 0 ? 1024 : LAYOUT <= 2 ? kNope : kNope / 2;
+  const uint8_t* src = pg + (int64_t)off * kRowBytes;
+  const uint8_t* sc = pg + (int64_t)page_size * kRowBytes + (int64_t)off * row_scale_slot(LAYOUT);
+  // every load before the first store, which may alias them for all that the compiler knows
+  uint4 pe = make_uint4(0, 0, 0, 0);
+  if (lane < 8) pe = reinterpret_cast<const uint4*>(src + kCodeBytes)[lane];
+  uint4 raw[2];      // elements 8c .. 8c + 7, c = lane + 32 h: 16, 8 or 4 bytes
+  uint32_t sb[2];    // and their scale byte
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = lane + 32 * h;
+    if (8 * c >= kNope) break;
+    if (LAYOUT == 0) {
+      raw[h] = reinterpret_cast<const uint4*>(src)[c];
+    } else if (LAYOUT <= 2) {
+      const uint2 w = reinterpret_cast<const uint2*>(src)[c];
+      raw[h] = make_uint4(w.x, w.y, 0, 0);
+      sb[h] = sc[c >> 3];
+    } else {
+      raw[h] = make_uint4(reinterpret_cast<const uint32_t*>(src)[c], 0, 0, 0);
+      sb[h] = sc[c >> 2];
+    }
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int c = lane + 32 * h;
+    if (8 * c >= kNope) break;
+    if (LAYOUT == 0) {
+      dst[c] = raw[h];
+    } else if (LAYOUT <= 2) {
+      const float s = ue8m0_to_f32(sb[h]);
+      const float2 a = e4m3x2_to_f32x2(raw[h].x & 0xFFFFu), b = e4m3x2_to_f32x2(raw[h].x >> 16);
+      const float2 d = e4m3x2_to_f32x2(raw[h].y & 0xFFFFu), e = e4m3x2_to_f32x2(raw[h].y >> 16);
+      dst[c] = make_uint4(f32x2_to_bf16x2(a.x * s, a.y * s), f32x2_to_bf16x2(b.x * s, b.y * s),
+                          f32x2_to_bf16x2(d.x * s, d.y * s), f32x2_to_bf16x2(e.x * s, e.y * s));
+    } else {
+      uint32_t o[4];
+      fp4x8_to_bf16(raw[h].x, fp4_scale(sb[h]), o);
+      dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  if (lane < 8) dst[kNope / 8 + lane] = pe;
 }
 
 }  // namespace mla

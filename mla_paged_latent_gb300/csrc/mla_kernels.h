@@ -136,6 +136,60 @@ cudaError_t launch_combine_v_up(const float* part_out, const float* part_lse, co
 cudaError_t launch_kv_gather(const uint8_t* kv, int layout, int64_t num_pages, int page_size, int64_t page_bytes,
                              const int32_t* bt_row, int max_pages, int length, float* out, cudaStream_t stream);
 
+// The same with positions of several axes, a table of the axis of each pair, and per-head queries (mla_qkv_norm_rope_axes).
+struct AxesParams {
+  QkvParams qkv;                  // positions: [axes, T]
+  uint64_t axis_of_pair;          // two bits a pair
+  uint32_t used_axes;             // one bit an axis
+  int32_t q_width;                // 192, or the layout's row width
+  int32_t copy_nope;              // the queries' NoPE part has to be written (it is not q_out's own, or is normalised)
+};
+cudaError_t launch_qkv_norm_rope_axes(const AxesParams& p, cudaStream_t stream);
+
+// Matrix products with an epilogue (gemm_sm103.cu): y = act(x W^T + bias) + residual.
+struct GemmParams {
+  const uint16_t* bias;           // bf16 [cols] or null
+  const uint16_t* residual;       // bf16 [rows, cols], residual_stride elements apart, or null
+  int64_t residual_stride;
+  uint16_t* out;                  // the narrow kernel's output (the pair kernel's goes through its tensor map)
+  int64_t out_stride;
+  unsigned int* status;           // or null
+  int32_t rows, cols, k_blocks;   // k_blocks: steps of 64 in K
+  int32_t act;                    // 0 none, 1 silu, 2 gelu
+  int32_t m_tiles, n_tiles, band; // pair: tiles of 256 x 256; narrow: n_tiles of 128 columns
+  int32_t w_row0;                 // pair: first row of W
+  int32_t split;                  // narrow: CTAs that share a tile's K
+};
+cudaError_t launch_gemm_pair(const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,
+                             const CUtensorMap& y_map, int clusters, cudaStream_t stream);
+cudaError_t launch_gemm_narrow(int rows_a_cta, const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,
+                               int grid, cudaStream_t stream);
+
+// Attention of a chunk of new tokens (chunk_sm103.cu).
+struct ChunkParams {
+  const uint8_t* kv;              // paged cache
+  const int32_t* block_table;     // [batch, max_pages]
+  uint16_t* rows;                 // bf16 [kv_rows, 576]
+  const int32_t* requests;        // [batch, 4]: q_start, q_len, kv_start, kv_len
+  const int32_t* tile_req;        // [kv_rows / 128]: the request of each 128 rows
+  const int32_t* pair_items;      // [pairs + 1]
+  const int32_t* items;           // [items, 8]: request, q0, head, first KV tile, last + 1, slot or -1
+  const int32_t* merges;          // [merges, 8]: request, q0, head, first slot, pieces
+  uint16_t* out;                  // bf16 [T, heads, 128]
+  float* lse;                     // [T, heads] or null
+  float* part_out;                // [slots, 512, 128]
+  float* part_lse;                // [slots, 512]
+  unsigned int* status;
+  int64_t num_pages, page_bytes;
+  int32_t page_size, log2_ps, max_pages;
+  int32_t kv_rows, heads, head0, group_heads, causal;
+  float scale_log2;
+};
+cudaError_t launch_chunk_rows(int layout, const ChunkParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_attention(const ChunkParams& p, const CUtensorMap& q_map, const CUtensorMap& kv_map,
+                                   const CUtensorMap& rope_map, int pairs, cudaStream_t stream);
+cudaError_t launch_chunk_merge(const ChunkParams& p, int merges, cudaStream_t stream);
+
 // Host split-KV plan (rule documented on mla_decode_plan in include/mla_decode.h).
 struct PlanResult {
   std::vector<int32_t> sched;        // [partitions * 8]
@@ -174,6 +228,14 @@ size_t workspace_bytes_for(int64_t total_splits, int64_t rows_per_req);
 __host__ __device__ inline int request_len(const DecodeParams& P, int r) {
   return P.seqlens != nullptr ? P.seqlens[r] : P.uniform_len;
 }
+
+// Host plan of a chunk's attention (rule documented on mla_chunk_plan in include/mla_decode.h): the sections of ChunkParams.
+struct ChunkPlan {
+  std::vector<int32_t> requests, tile_req, pair_items, items, merges;
+  int32_t slots = 0;
+};
+ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int batch, int heads, bool causal, int group,
+                          int num_sms);
 
 PlanResult make_plan(const int32_t* seqlens, int batch, int sq, int heads, int topk, int min_splits, int num_sms);
 
