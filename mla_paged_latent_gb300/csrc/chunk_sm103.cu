@@ -12,6 +12,7 @@
 //   chunk_attention_kernel;
 //   chunk_merge_kernel where a query tile was split over the rows.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "decode_common.cuh"
@@ -62,12 +63,12 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
 // Single SMs would need all of K and V in each: 80 KB a tile instead of 40, more than shared memory brings in under the
 // products, and only one tile and a half fit beside Q.
 // TMEM: S of the two sub-tiles (128 columns each; P as bf16 pairs takes the first 64 once S has been read) and O (128 each).
-// Products are issued in the order PV0(j) S0(j+1) PV1(j) S1(j+1): S(j+1) follows the PV(j) that reads P from the same
-// columns, and its completion says that O holds tile j, so a rescale of O needs no barrier of its own.
+// A thread for each sub-tile issues PV(j) S(j+1) in turn: S(j+1) follows the PV(j) that reads P from the same columns, and
+// its completion says that O holds tile j, so a rescale of O needs no barrier of its own.
 // P is rounded to bf16, an operand of the tensor cores; maxima, sums and O are fp32. The running maximum moves (and O is
 // rescaled) only when a tile exceeds it by 2^32, so a row's sum stays below rows x 2^32 x max |V|.
 // Shared memory per CTA: Q 2 x 48 KB, and 3 stages of K (64 rows x 192) and V (128 rows x 64 dims), 40 KB each.
-//   warp 0      TMA            warp 1      TMEM, MMA issue (even CTA)
+//   warp 0      TMA            warps 1, 2  MMA issue of sub-tile 0 and 1 (even CTA); warp 1 TMEM
 //   warps 4-7   softmax and epilogue of sub-tile 0, warps 8-11 of sub-tile 1: a query row a thread
 constexpr int kChunkThreads = 384;
 constexpr uint32_t kQSlab = 128 * 128;
@@ -79,19 +80,38 @@ constexpr int kKvStages = 3;
 constexpr uint32_t kOffK = 2 * kQSub;
 constexpr uint32_t kOffV = kOffK + kKvStages * kKBytes;
 constexpr uint32_t kOffChunkMisc = kOffV + kKvStages * kVBytes;
-constexpr float kChunkRescaleLog2 = 32.0f;
+constexpr float kWeightLog2 = 7.0f, kWeightMaxLog2 = 15.0f;
 
 struct ChunkMisc {
   uint64_t q_full[2], q_empty[2];                  // full barriers and p_full, o_free: in the even CTA, both CTAs arrive
-  uint64_t k_full[kKvStages], k_empty[kKvStages];  // the others: in each CTA, by multicast commits
+  uint64_t k_full[kKvStages], k_empty[kKvStages];  // the others: in each CTA (empty: its two sub-tiles arrive)
   uint64_t v_full[kKvStages], v_empty[kKvStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t s_full[2], p_full[4], o_full[2], o_free[2];  // p_full: halves of the KV tile, of each sub-tile
+  uint64_t turn[2];                                // of the two MMA threads
   uint64_t last;
   uint32_t tmem_base;
   int abort;
 };
 constexpr size_t kChunkSmem = kOffChunkMisc + sizeof(ChunkMisc) + 1024;
 static_assert(kChunkSmem <= 232448, "shared memory budget of one CTA");
+
+// mma_bf16_pair and mma_bf16_pair_ts with the descriptors of shared memory given by their low words (the start address; an
+// offset within shared memory does not carry out of them): fewer instructions an MMA in the issuers.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
+__device__ __forceinline__ void mma_ss_lo(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_lo(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 
 struct Unit {
   int q_start, q0, n, kv_start, len, head, tb, slot;
@@ -145,17 +165,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
       mbar_init(here(misc->q_full[s]), 2);
       mbar_init(here(misc->q_empty[s]), 1);
       mbar_init(here(misc->s_full[s]), 1);
-      mbar_init(here(misc->p_full[s]), 8);
+      mbar_init(here(misc->p_full[2 * s]), 8);
+      mbar_init(here(misc->p_full[2 * s + 1]), 8);
       mbar_init(here(misc->o_full[s]), 1);
       mbar_init(here(misc->o_free[s]), 8);
+      mbar_init(here(misc->turn[s]), 1);
     }
     for (int s = 0; s < kKvStages; ++s) {
       mbar_init(here(misc->k_full[s]), 2);
-      mbar_init(here(misc->k_empty[s]), 1);
+      mbar_init(here(misc->k_empty[s]), 2);
       mbar_init(here(misc->v_full[s]), 2);
-      mbar_init(here(misc->v_empty[s]), 1);
+      mbar_init(here(misc->v_empty[s]), 2);
     }
-    mbar_init(here(misc->last), 1);
+    mbar_init(here(misc->last), 2);
     misc->abort = 0;
     fence_mbar_init();
   }
@@ -174,8 +196,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
   const int item0 = P.pair_items[pair], item1 = P.pair_items[pair + 1];
 
   if (warp < 4) {
-    // 128 x 88 + 256 x 208 = the launch's 384 x 168 registers
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // 128 x 72 + 256 x 216 = the launch's 384 x 168 registers
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 && lane == 0) {
       tma_prefetch_desc(&q_map);
       tma_prefetch_desc(&kv_map);
@@ -238,80 +260,117 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
           mbar_wait_drain_cluster(here(misc->v_full[st]), 1);
         }
       }
-    } else if (warp == 1 && rank == 0 && lane == 0) {
+    } else if (warp < 3 && rank == 0 && lane == 0) {
+      // The two threads take turns, a tile each: sub-tiles that begin a tile at once would also need their P at once, and the
+      // tensor cores would wait for both softmaxes.
+      auto issuer = [&](auto sub) {
+      constexpr int s = decltype(sub)::value;
       constexpr uint32_t idesc_s = idesc_bf16_f32(256, 128, 0, 0);
-      constexpr uint32_t idesc_o = idesc_bf16_f32(256, 128, 0, 1);  // V: MN-major, 64 dims of each CTA
-      const uint64_t kmaj = sdesc_sw128(0, 16, 1024);
-      const uint64_t vmaj = sdesc_sw128(0, kVBytes, 1024);
-      int it = 0;
-      int units[2] = {0, 0}, scores[2] = {0, 0};  // per sub-tile: units begun, score tiles whose P has been waited for
+      constexpr uint32_t idesc_o = idesc_f16_f32(256, 128, 0, 1);  // V: MN-major, 64 dims of each CTA
+      // low words of the descriptors: start address, and a leading offset that neither layout uses
+      const uint32_t q = ((sb + s * kQSub) >> 4) | (1u << 16), k0 = ((sb + kOffK) >> 4) | (1u << 16),
+                     v0 = ((sb + kOffV) >> 4) | (1u << 16);
+      const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128;
+      int it = 0, units = 0, scores = 0, turns = 0;  // KV tiles, units begun, score tiles whose P has been waited for, turns taken
       bool ok = true;
       for (int i = item0; i < item1 && ok; ++i) {
         const Unit u = read_unit(P, i);
-        const int nt = max(u.tiles[0], u.tiles[1]);
-        // the last of the sub-tiles that use tile j
-        auto last_user = [&](int s, int j) { return s == 1 || j >= u.tiles[1]; };
-        auto issue_s = [&](int s, int j) {
-          const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
-          if (!wait(misc->k_full[st], use)) return false;
-          tc_fence_after();
-          const uint64_t q = kmaj | ((sb + s * kQSub) >> 4);
-          const uint64_t k = kmaj | ((sb + kOffK + st * kKBytes) >> 4);
+        const int nt = max(u.tiles[0], u.tiles[1]), tiles = u.tiles[s];
+        auto issue_s = [&](int j) {  // K of tile j has landed
+          const uint32_t k = k0 + (it + j) % kKvStages * (kKBytes >> 4);
 #pragma unroll
-          for (int x = 0; x < 12; ++x)
-            mma_bf16_pair(tmem + s * 128, q + (x >> 2) * (kQSlab >> 4) + (x & 3) * 2,
-                          k + (x >> 2) * (kKSlab >> 4) + (x & 3) * 2, idesc_s, x ? 1u : 0u);
+          for (int x = 0; x < 12; ++x) {
+            mma_ss_lo(t_s, q + (x >> 2) * (kQSlab >> 4) + (x & 3) * 2, k + (x >> 2) * (kKSlab >> 4) + (x & 3) * 2, idesc_s,
+                      x ? 1u : 0u);
+            // (the other thread sees its turn about when the rest has been issued)
+            if (x == 8 && j > 0) mbar_arrive(here(misc->turn[1 - s]));
+          }
           mma_commit_pair(here(misc->s_full[s]), 3);
-          if (last_user(s, j)) mma_commit_pair(here(misc->k_empty[st]), 3);
-          if (j + 1 == u.tiles[s]) mma_commit_pair(here(misc->q_empty[s]), 3);
-          return true;
+          if (j + 1 == tiles) mma_commit_pair(here(misc->q_empty[s]), 3);
         };
-        for (int s = 0; s < 2 && ok; ++s)
-          if (u.tiles[s] > 0) ok = wait(misc->q_full[s], units[s]) && issue_s(s, 0);
-        for (int j = 0; j < nt && ok; ++j) {
+        auto k_landed = [&](int j) { return wait(misc->k_full[(it + j) % kKvStages], (it + j) / kKvStages); };
+        if (tiles > 0) {
+          ok = wait(misc->q_full[s], units) && k_landed(0);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(0);
+        }
+        for (int j = 0; j < nt; ++j) {
           const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
+          if (j >= tiles) {  // the other sub-tile's alone
+            if (!(ok = wait(misc->turn[s], s == 0 ? turns - 1 : turns))) break;
+            ++turns;
+            mbar_arrive(here(misc->turn[1 - s]));
+            continue;
+          }
+          // Everything but P first: a thread that tests a barrier waits until the instructions that it has queued are
+          // dispatched, and a commit costs as much as one or two of them, so neither stands between P's arrival, PV and
+          // the next S (the softmax warps pass on the stages, which their own barriers say have been read).
+          ok = wait(misc->v_full[st], use);
+          if (ok && j + 1 < tiles) ok = k_landed(j + 1);
+          if (ok && j == 0 && units > 0) ok = wait(misc->o_free[s], units - 1);
+          if (ok) ok = wait(misc->p_full[2 * s], scores);
+          if (ok) ok = wait(misc->turn[s], s == 0 ? turns - 1 : turns);
+          if (!ok) break;
+          ++turns;
+          tc_fence_after();
+          const uint32_t v = v0 + st * (kVBytes >> 4);
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (!ok || j >= u.tiles[s]) continue;
-            ok = wait(misc->p_full[s], scores[s]);
-            if (ok && j == 0 && units[s] > 0) ok = wait(misc->o_free[s], units[s] - 1);
-            if (ok) ok = wait(misc->v_full[st], use);
-            if (!ok) continue;
-            ++scores[s];
-            tc_fence_after();
-            const uint64_t v = vmaj | ((sb + kOffV + st * kVBytes) >> 4);
+          for (int x = 0; x < 4; ++x) mma_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), idesc_o, (j | x) ? 1u : 0u);
+          if (!(ok = wait(misc->p_full[2 * s + 1], scores))) break;
+          tc_fence_after();
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-              mma_bf16_pair_ts(tmem + 256 + s * 128, tmem + s * 128 + 8 * x, v + x * (2048 >> 4), idesc_o,
-                               (j | x) ? 1u : 0u);
-            if (last_user(s, j)) mma_commit_pair(here(misc->v_empty[st]), 3);
-            if (j + 1 == u.tiles[s]) mma_commit_pair(here(misc->o_full[s]), 3);
-            else ok = issue_s(s, j + 1);
+          for (int x = 4; x < 8; ++x) mma_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), idesc_o, 1u);
+          ++scores;
+          if (j + 1 < tiles) {
+            issue_s(j + 1);
+          } else {
+            mma_commit_pair(here(misc->o_full[s]), 3);
+            mbar_arrive(here(misc->turn[1 - s]));
           }
         }
         it += nt;
-        for (int s = 0; s < 2; ++s) units[s] += u.tiles[s] > 0;
+        units += tiles > 0;
       }
       mma_commit_pair(here(misc->last), 1);
       mbar_wait_drain_cluster(here(misc->last), 0);
+      };
+      if (warp == 1) issuer(std::integral_constant<int, 0>());
+      else issuer(std::integral_constant<int, 1>());
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     const int s = (warp - 4) >> 2, quarter = warp & 3;
     const int mine = 256 * s + 128 * rank + 32 * quarter + lane;  // row of the unit
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t t_s = tmem + lane_off + s * 128, t_o = tmem + lane_off + 256 + s * 128;
-    const float2 scale2 = make_float2(P.scale_log2, P.scale_log2);
-    int scores = 0, units = 0;
+    const uint32_t p_bar[2] = {lead(misc->p_full[2 * s]), lead(misc->p_full[2 * s + 1])};
+    int scores = 0, units = 0, it = 0;
     bool ok = true;
     for (int i = item0; i < item1 && ok; ++i) {
       const Unit u = read_unit(P, i);
       if (u.head >= P.group_heads) continue;
-      const int row = u.q0 + mine;  // query of the request
-      const int lim = row_limit(P.causal, u.len, u.n, row);
-      const int tiles = u.tiles[s];
-      float m_run = -INFINITY, l_run = 0.f;
+      const int tiles = u.tiles[s], others = u.tiles[1 - s];
+      const int lim = row_limit(P.causal, u.len, u.n, u.q0 + mine) - u.tb * 128;  // rows that this query sees, from tb on
+      // The stage of K or V of tile j has been read by this sub-tile's products, and by the other's if it has none there:
+      // each of two arrivals says so for one of them.
+      auto pass_on = [&](uint64_t (&empty)[kKvStages], int j) {
+        if (quarter == 0 && lane == 0) {
+          const uint32_t b = here(empty[(it + j) % kKvStages]);
+          mbar_arrive(b);
+          if (j >= others) mbar_arrive(b);
+        }
+        __syncwarp();
+      };
+      // Weights are 2^(score + e - ref) with e the exponent of their 32 rows' values and ref such that they stay below 2^15;
+      // the sum takes e back out.
+      float ref = -INFINITY, l_run = 0.f;
+      const float4* exps = reinterpret_cast<const float4*>(P.value_exp + static_cast<int64_t>(u.head) * (P.kv_rows >> 5) +
+                                                           (u.kv_start >> 5)) + u.tb;
+      float4 e_next = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (tiles > 0) e_next = exps[0];
       for (int j = 0; j < tiles; ++j) {
+        const float e[4] = {e_next.x, e_next.y, e_next.z, e_next.w};
         if (!wait(misc->s_full[s], scores)) {
           ok = false;
           break;
@@ -322,72 +381,88 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_ld32(t_s + 32 * k, x + 32 * k);
         tmem_wait_ld();
-        const int nv = lim - (u.tb + j) * 128;  // columns that this row sees
+        if (j + 1 < tiles) e_next = exps[j + 1];  // (not before: the wait would be for this load too)
+        const int nv = lim - j * 128;  // columns that this row sees
         if (__any_sync(0xffffffffu, nv < 128)) {
 #pragma unroll
           for (int k = 0; k < 128; ++k)
             if (k >= nv) x[k] = 0xFF800000u;
         }
-        float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float top = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < 64; ++k)
-          m4[k & 3] = max3(m4[k & 3], __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-        const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * P.scale_log2;
-        const bool raise = mt > m_run + kChunkRescaleLog2;
+        for (int g = 0; g < 4; ++g) {
+          float m = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            m = max3(m, __uint_as_float(x[32 * g + 2 * k]), __uint_as_float(x[32 * g + 2 * k + 1]));
+          top = fmaxf(top, fmaf(m, P.scale_log2, e[g]));
+        }
+        const bool raise = top > ref + kWeightMaxLog2;
         if (__any_sync(0xffffffffu, raise)) {
-          const float a = raise ? fast_exp2(m_run - mt) : 1.f;  // (0 for the first rows that a query sees)
+          const float a = raise ? fast_exp2(ref - (top - kWeightLog2)) : 1.f;  // (0 for the first rows that a query sees)
           l_run *= a;
-          if (raise) m_run = mt;
+          if (raise) ref = top - kWeightLog2;
           if (j > 0) {
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              uint32_t o[32];
-              tmem_ld32(t_o + 32 * k, o);
+            for (int k = 0; k < 8; ++k) {  // (16 columns: the scores fill the registers)
+              uint32_t o[16];
+              tmem_ld16(t_o + 16 * k, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-              tmem_st32(t_o + 32 * k, o);
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * a);
+              tmem_st16(t_o + 16 * k, o);
             }
           }
         }
-        const float m_use = m_run == -INFINITY ? 0.f : m_run;
-        const float2 neg = make_float2(-m_use, -m_use);
-        float2 sum[2] = {make_float2(l_run, 0.f), make_float2(0.f, 0.f)};
+        const float ref_use = ref == -INFINITY ? 0.f : ref;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          uint32_t p[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float2 v = fma2(make_float2(__uint_as_float(x[64 * h + 2 * k]), __uint_as_float(x[64 * h + 2 * k + 1])),
-                                  scale2.x, neg);
-            const float2 e = make_float2(fast_exp2(v.x), fast_exp2(v.y));
-            sum[k & 1] = add2(sum[k & 1], e);
-            p[k] = f32x2_to_bf16x2(e.x, e.y);
+          for (int gg = 0; gg < 2; ++gg) {
+            const int g = 2 * h + gg;
+            uint32_t p[16];
+            const float off = e[g] - ref_use;
+            const float2 off2 = make_float2(off, off);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 v = fma2(make_float2(__uint_as_float(x[32 * g + 2 * k]), __uint_as_float(x[32 * g + 2 * k + 1])),
+                                    P.scale_log2, off2);
+              const float2 w = make_float2(fast_exp2(v.x), fast_exp2(v.y));
+              sum[k & 1] = add2(sum[k & 1], w);
+              p[k] = f32x2_to_f16x2(w.x, w.y);
+            }
+            const float2 t = add2(sum[0], sum[1]);
+            l_run = fmaf(t.x + t.y, fast_exp2(-e[g]), l_run);
+            tmem_st16(t_s + 16 * g, p);
           }
-          tmem_st32(t_s + 32 * h, p);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(p_bar[h]);
+          __syncwarp();
         }
-        const float2 t = add2(sum[0], sum[1]);
-        l_run = t.x + t.y;
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead(misc->p_full[s]));
+        pass_on(misc->k_empty, j);  // (only now: P is waited for, the stages have two tiles' time)
+        if (j > 0) pass_on(misc->v_empty, j - 1);
       }
       if (!ok) break;
       // Out, 32 bytes a store. A row that sees nothing is zeros with an lse of -infinity; a NaN sum stays NaN.
       const bool empty = l_run == 0.f;
       const float inv = empty ? 0.f : 1.0f / l_run;
-      const float lse = empty ? -INFINITY : (m_run + log2f(l_run)) * 0.6931471805599453f;
-      const bool live = row < u.n;
+      const float lse = empty ? -INFINITY : (ref + log2f(l_run)) * 0.6931471805599453f;
+      const Unit w = read_unit(P, i);  // (again: no register holds it while the scores fill them)
+      const int row = w.q0 + mine;
+      const bool live = row < w.n;
       if (tiles > 0) {
         if (!wait(misc->o_full[s], units)) break;
         ++units;
+        pass_on(misc->v_empty, tiles - 1);
         tc_fence_after();
       }
-      const int64_t at = static_cast<int64_t>(u.q_start + row) * P.heads + P.head0 + u.head;  // row of out
-      const int64_t part = static_cast<int64_t>(u.slot) * 512 + mine;
+      const int64_t at = static_cast<int64_t>(w.q_start + row) * P.heads + P.head0 + w.head;  // row of out
+      const int64_t part = static_cast<int64_t>(w.slot) * 512 + mine;
       if (live) {
-        if (u.slot >= 0) P.part_lse[part] = lse;
+        if (w.slot >= 0) P.part_lse[part] = lse;
         else if (P.lse != nullptr) P.lse[at] = lse;
       }
 #pragma unroll 1
@@ -400,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
         }
 #pragma unroll
         for (int e = 0; e < 32; ++e) o[e] = empty ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
-        if (live && u.slot >= 0) {
+        if (live && w.slot >= 0) {
           float* dst = P.part_out + part * 128 + 32 * k;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -425,6 +500,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(lead(misc->o_free[s]));
       }
+      it += max(w.tiles[0], w.tiles[1]);
     }
   }
   tc_fence_before();

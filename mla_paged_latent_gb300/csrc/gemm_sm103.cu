@@ -30,18 +30,18 @@ __device__ __forceinline__ float activate(float y, int act) {
 }
 
 // ----------------------------------------------------------------------------- CTA pairs
-constexpr int kGemmThreads = 192;              // TMA, MMA, 4 epilogue warps
-constexpr int kGemmStages = 6;
+constexpr int kGemmThreads = 320;              // TMA, MMA, 8 epilogue warps
+constexpr int kGemmStages = 5;
 constexpr uint32_t kGemmA = 128 * 128;         // this CTA's 128 rows of x, 64 of K
 constexpr uint32_t kGemmB = 128 * 128;         // its half of W's 256 rows
 constexpr uint32_t kGemmStage = kGemmA + kGemmB;
 constexpr uint32_t kGemmOffStaging = kGemmStages * kGemmStage;
 constexpr uint32_t kGemmSlab = 32 * 128;       // 32 rows x 64 columns of the result: one warp's store
-constexpr uint32_t kGemmOffMisc = kGemmOffStaging + 4 * 2 * kGemmSlab;
+constexpr uint32_t kGemmOffMisc = kGemmOffStaging + 8 * 2 * kGemmSlab;
 
 struct GemmMisc {
   uint64_t full[kGemmStages], empty[kGemmStages];  // full: in the even CTA, both CTAs' bytes
-  uint64_t acc_full[2], acc_empty[2];              // acc_empty: in the even CTA, 8 warps
+  uint64_t acc_full[2], acc_empty[2];              // acc_empty: in the even CTA, 16 warps
   uint64_t last;
   uint32_t tmem_base;
   int abort;
@@ -50,6 +50,30 @@ struct GemmMisc {
 constexpr size_t kGemmSmem = kGemmOffMisc + sizeof(GemmMisc) + 1024;
 static_assert(kGemmSmem <= 232448, "shared memory budget of one CTA");
 
+// What the epilogue does: bias, residual and no activation; an activation too; or keys and values of the heads.
+enum { kPlain = 0, kActivated = 1, kKeysValues = 2 };
+
+// 32 rows x 64 columns, a row a lane, as 16-bit pairs to the warp's slab and from there to memory by TMA, so that rows leave
+// as whole 128-byte lines.
+__device__ __forceinline__ void store_slab(const CUtensorMap* map, uint32_t staging, int stores, int lane, const uint32_t (&o)[32],
+                                           int col0, int row0) {
+  if (stores >= 2) {
+    if (lane == 0) bulk_wait_read<1>();
+    __syncwarp();
+  }
+  const uint32_t slab = staging + (stores & 1) * kGemmSlab;
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    st_shared_v4(slab + lane * 128 + ((q ^ (lane & 7)) << 4), make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, slab, col0, row0);
+    bulk_commit();
+  }
+}
+
+template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_pair_kernel(const __grid_constant__ GemmParams P, const __grid_constant__ CUtensorMap x_map,
                      const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap y_map) {
@@ -70,7 +94,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&misc->acc_full[b]), 1);
-      mbar_init(smem_addr(&misc->acc_empty[b]), 8);
+      mbar_init(smem_addr(&misc->acc_empty[b]), 16);
     }
     mbar_init(smem_addr(&misc->last), 1);
     misc->abort = 0;
@@ -153,10 +177,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       mbar_wait_drain_cluster(smem_addr(&misc->last), 0);
     }
   } else {
-    // Epilogue: a warp reaches the TMEM lanes 32 (warp % 4) .. + 31, one row a lane. 64 columns at a time go through the
-    // warp's own two 4-KB slabs to a TMA store, so that rows leave as whole 128-byte lines.
-    const int quarter = warp & 3;
-    const uint32_t staging = sb + kGemmOffStaging + quarter * 2 * kGemmSlab;
+    // Epilogue: a warp reaches the TMEM lanes 32 (warp % 4) .. + 31, one row a lane, and takes half of the tile's columns.
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t staging = sb + kGemmOffStaging + (warp - 2) * 2 * kGemmSlab;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     int u = 0, stores = 0;
     for (int t = cluster_id_x(); t < tiles; t += step, ++u) {
@@ -164,61 +187,83 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       place(t, &m0, &n0);
       const int buf = u & 1;
       const int row0 = m0 + 128 * rank + 32 * quarter;
+      const uint32_t src = tmem + buf * 256 + lane_off + 128 * half;
       if (!wait_bar(smem_addr(&misc->acc_full[buf]), (u >> 1) & 1, abort_flag, status)) break;
       tc_fence_after();
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        const int col0 = n0 + 64 * c;
-        if (row0 >= P.rows || col0 >= P.cols) break;  // (the same in all lanes)
-        const int row = row0 + lane;
-        const int chunks = min(8, (P.cols - col0) >> 3);  // of 8 columns
-        uint32_t acc[64];
-        tmem_ld32(tmem + buf * 256 + lane_off + 64 * c, acc);
-        tmem_ld32(tmem + buf * 256 + lane_off + 64 * c + 32, acc + 32);
-        uint4 res[8];
-        const bool add = P.residual != nullptr && row < P.rows;
-        const uint16_t* rp = P.residual + row * P.residual_stride + col0;
+      if (KIND == kKeysValues) {
+        // a tile is one head: 128 columns of its keys, 128 of its values. Values leave as fp16, 32 rows scaled by a power of
+        // two of their own that brings their largest to 2^13 .. 2^14 (three bits more than bf16 for each product with a softmax weight, whatever
+        // the values' range); an infinity or NaN does not count.
+        if (row0 < P.rows) {
+          uint32_t acc[128], o[32];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          res[q] = add && q < chunks ? *reinterpret_cast<const uint4*>(rp + 8 * q) : make_uint4(0, 0, 0, 0);
-        tmem_wait_ld();
-        if (stores >= 2) {
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
-        }
-        const uint32_t slab = staging + (stores & 1) * kGemmSlab;
+          for (int k = 0; k < 4; ++k) tmem_ld32(src + 32 * k, acc + 32 * k);
+          tmem_wait_ld();
+          float scale = 1.f;
+          if (half == 1) {
+            uint32_t top = 0;  // magnitudes compare as integers
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const uint4 bu = P.bias != nullptr && q < chunks ? *reinterpret_cast<const uint4*>(P.bias + col0 + 8 * q)
-                                                           : make_uint4(0, 0, 0, 0);
-          const uint32_t bh[4] = {bu.x, bu.y, bu.z, bu.w}, rh[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float y0 = __uint_as_float(acc[8 * q + 2 * i]), y1 = __uint_as_float(acc[8 * q + 2 * i + 1]);
-            if (P.bias != nullptr) {
-              y0 += __uint_as_float(bh[i] << 16);
-              y1 += __uint_as_float(bh[i] & 0xFFFF0000u);
+            for (int k = 0; k < 128; ++k) {
+              const uint32_t v = acc[k] & 0x7FFFFFFFu;
+              top = max(top, v < 0x7F800000u ? v : 0u);
             }
-            if (P.act != 0) {
-              y0 = activate(y0, P.act);
-              y1 = activate(y1, P.act);
-            }
-            if (add) {
-              y0 += __uint_as_float(rh[i] << 16);
-              y1 += __uint_as_float(rh[i] & 0xFFFF0000u);
-            }
-            o[i] = f32x2_to_bf16x2(y0, y1);
+            top = __reduce_max_sync(0xffffffffu, top);
+            const int e = min(max(static_cast<int>(top >> 23) - 127 - 13, kValueExpMin), kValueExpMax);
+            scale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            if (lane == 0) P.value_exp[static_cast<int64_t>(n0 >> 8) * P.value_exp_stride + (row0 >> 5)] = static_cast<float>(e);
           }
-          st_shared_v4(slab + lane * 128 + ((q ^ (lane & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float a = __uint_as_float(acc[64 * c + 2 * k]), b = __uint_as_float(acc[64 * c + 2 * k + 1]);
+              o[k] = half == 0 ? f32x2_to_bf16x2(a, b) : f32x2_to_f16x2(a * scale, b * scale);
+            }
+            store_slab(&y_map, staging, stores++, lane, o, n0 + 128 * half + 64 * c, row0);
+          }
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_2d(&y_map, slab, col0, row0);
-          bulk_commit();
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int col0 = n0 + 128 * half + 64 * c;
+          if (row0 >= P.rows || col0 >= P.cols) break;  // (the same in all lanes)
+          const int row = row0 + lane;
+          const int chunks = min(8, (P.cols - col0) >> 3);  // of 8 columns
+          uint32_t acc[64], o[32];
+          tmem_ld32(src + 64 * c, acc);
+          tmem_ld32(src + 64 * c + 32, acc + 32);
+          uint4 res[8];
+          const bool add = P.residual != nullptr && row < P.rows;
+          const uint16_t* rp = P.residual + row * P.residual_stride + col0;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            res[q] = add && q < chunks ? *reinterpret_cast<const uint4*>(rp + 8 * q) : make_uint4(0, 0, 0, 0);
+          tmem_wait_ld();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint4 bu = P.bias != nullptr && q < chunks ? *reinterpret_cast<const uint4*>(P.bias + col0 + 8 * q)
+                                                             : make_uint4(0, 0, 0, 0);
+            const uint32_t bh[4] = {bu.x, bu.y, bu.z, bu.w}, rh[4] = {res[q].x, res[q].y, res[q].z, res[q].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float y0 = __uint_as_float(acc[8 * q + 2 * i]), y1 = __uint_as_float(acc[8 * q + 2 * i + 1]);
+              if (P.bias != nullptr) {
+                y0 += __uint_as_float(bh[i] << 16);
+                y1 += __uint_as_float(bh[i] & 0xFFFF0000u);
+              }
+              if (KIND == kActivated) {
+                y0 = activate(y0, P.act);
+                y1 = activate(y1, P.act);
+              }
+              if (add) {
+                y0 += __uint_as_float(rh[i] << 16);
+                y1 += __uint_as_float(rh[i] & 0xFFFF0000u);
+              }
+              o[4 * q + i] = f32x2_to_bf16x2(y0, y1);
+            }
+          }
+          store_slab(&y_map, staging, stores++, lane, o, col0, row0);
         }
-        ++stores;
       }
       tc_fence_before();
       __syncwarp();
@@ -406,9 +451,13 @@ cudaError_t narrow(const GemmParams& p, const CUtensorMap& x_map, const CUtensor
 
 cudaError_t launch_gemm_pair(const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,
                              const CUtensorMap& y_map, int clusters, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(gemm_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(gemm_pair_kernel, dim3(2 * clusters), dim3(kGemmThreads), kGemmSmem, stream, p, x_map, w_map, y_map);
+  auto go = [&](auto kern) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(2 * clusters), dim3(kGemmThreads), kGemmSmem, stream, p, x_map, w_map, y_map);
+  };
+  if (p.value_exp != nullptr) return go(gemm_pair_kernel<kKeysValues>);
+  return p.act == 0 ? go(gemm_pair_kernel<kPlain>) : go(gemm_pair_kernel<kActivated>);
 }
 
 cudaError_t launch_gemm_narrow(int rows_a_cta, const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,

@@ -34,14 +34,15 @@ int rows_map(const char* what, CUtensorMap* map, const void* base, int64_t cols,
 
 // Where the parts of a chunk's workspace begin (bytes).
 struct ChunkSpace {
-  size_t rows, kv, part_out, part_lse, end;
+  size_t rows, kv, value_exp, part_out, part_lse, end;
 };
 ChunkSpace chunk_space(int64_t kv_rows, int64_t group, int64_t slots) {
   ChunkSpace s;
   const size_t n = static_cast<size_t>(kv_rows < 128 ? 128 : kv_rows);
   s.rows = MLA_WORKSPACE_HEADER;
   s.kv = s.rows + align256(n * 1152);
-  s.part_out = s.kv + n * static_cast<size_t>(group) * 512;
+  s.value_exp = s.kv + n * static_cast<size_t>(group) * 512;
+  s.part_out = s.value_exp + align256(n / 32 * static_cast<size_t>(group) * 4);
   s.part_lse = s.part_out + static_cast<size_t>(slots) * 512 * 128 * 4;
   s.end = s.part_lse + static_cast<size_t>(slots) * 512 * 4;
   return s;
@@ -180,6 +181,7 @@ int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layou
   p.merges = sched + at.merges;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
+  p.value_exp = reinterpret_cast<float*>(ws + space.value_exp);
   p.part_out = reinterpret_cast<float*>(ws + space.part_out);
   p.part_lse = reinterpret_cast<float*>(ws + space.part_lse);
   p.status = reinterpret_cast<unsigned int*>(ws);
@@ -223,6 +225,8 @@ int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layou
       mla::GemmParams g;
       std::memset(&g, 0, sizeof g);
       g.status = p.status;
+      g.value_exp = reinterpret_cast<float*>(ws + space.value_exp);
+      g.value_exp_stride = I.kv_rows / 32;
       g.rows = I.kv_rows;
       g.cols = p.group_heads * 256;
       g.k_blocks = 8;

@@ -154,6 +154,8 @@ struct GemmParams {
   uint16_t* out;                  // the narrow kernel's output (the pair kernel's goes through its tensor map)
   int64_t out_stride;
   unsigned int* status;           // or null
+  float* value_exp;               // pair: not null for keys and values of heads, [heads, value_exp_stride]: the power of two
+  int64_t value_exp_stride;       // that each 32 rows of a head's values are scaled down by
   int32_t rows, cols, k_blocks;   // k_blocks: steps of 64 in K
   int32_t act;                    // 0 none, 1 silu, 2 gelu
   int32_t m_tiles, n_tiles, band; // pair: tiles of 256 x 256; narrow: n_tiles of 128 columns
@@ -164,6 +166,9 @@ cudaError_t launch_gemm_pair(const GemmParams& p, const CUtensorMap& x_map, cons
                              const CUtensorMap& y_map, int clusters, cudaStream_t stream);
 cudaError_t launch_gemm_narrow(int rows_a_cta, const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,
                                int grid, cudaStream_t stream);
+
+// Range of a value exponent: values far below 1 need no larger scale for fp16 to hold them, and 2^-e is a normal number.
+constexpr int kValueExpMin = -24, kValueExpMax = 114;
 
 // Attention of a chunk of new tokens (chunk_sm103.cu).
 struct ChunkParams {
@@ -177,6 +182,7 @@ struct ChunkParams {
   const int32_t* merges;          // [merges, 8]: request, q0, head, first slot, pieces
   uint16_t* out;                  // bf16 [T, heads, 128]
   float* lse;                     // [T, heads] or null
+  const float* value_exp;         // [group, kv_rows / 32]: values are held times 2^-e
   float* part_out;                // [slots, 512, 128]
   float* part_lse;                // [slots, 512]
   unsigned int* status;

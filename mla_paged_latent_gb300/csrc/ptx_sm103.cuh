@@ -249,6 +249,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, in
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// The same with A and B fp16.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+  return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // Byte offset of element (row, k) inside a 128-B-swizzled slab of 64 bf16 per row
 // (the layout TMA's SWIZZLE_128B writes and the descriptors above read).
 __host__ __device__ __forceinline__ uint32_t sw128_offset(uint32_t row, uint32_t k) {
@@ -309,6 +314,11 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t two_codes) {
 __device__ __forceinline__ uint32_t f32x2_to_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32x2_to_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 // 2^(b - 127) as fp32 for a ue8m0 byte (0 -> 2^-127 subnormal, 255 -> NaN).
@@ -461,7 +471,7 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t cta_mask)
 }
 }  // namespace mla
 
-// ------------------------------------------------------------------ stores by TMA, A operands in TMEM, wide stores
+// ------------------------------------------------------------------ stores by TMA, wide stores, other CTAs' shared memory
 namespace mla {
 // Tile store from shared memory; elements past the tensor's extents are not written.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int c0, int c1) {
@@ -479,15 +489,6 @@ __device__ __forceinline__ void bulk_wait_read() {
 template <int N>
 __device__ __forceinline__ void bulk_wait() {
   asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
-}
-// D[tmem] (+)= A[tmem] * B over the pair: each CTA's rows of A (bf16 pairs, K / 2 columns) lie in its own TMEM.
-__device__ __forceinline__ void mma_bf16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                 uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
 }
 // 32 bytes, one sector.
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
