@@ -427,6 +427,13 @@ def mla_qkv_norm_rope(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, kv
                                     layout, kv_cache.shape[0], page_size, _ptr(status), _stream(stream)))
 
 
+@functools.lru_cache(maxsize=64)
+def _axis_words(axis_of_pair):
+    if len(axis_of_pair) != 32:
+        raise ValueError(f"axis_of_pair must name the axis of 32 pairs, not of {len(axis_of_pair)}")
+    return (ctypes.c_int32 * 32)(*axis_of_pair)
+
+
 def mla_qkv_norm_rope_axes(q_nope, q_pe, kv_raw, slots, positions, axis_of_pair, kv_norm_weight, kv_eps: float, freqs, q_out,
                            kv_cache, layout: int, page_size: int, q_norm_weight=None, q_eps: float | None = None,
                            status=None, stream=None):
@@ -457,8 +464,7 @@ def mla_qkv_norm_rope_axes(q_nope, q_pe, kv_raw, slots, positions, axis_of_pair,
         _require("kv_norm_weight", kv_norm_weight, bf16, 512)
         _require("freqs", freqs, f32, None, 64)
         _require("q_out", q_out, bf16, T, N, nope + 64)
-    if len(axis_of_pair) != 32:
-        raise ValueError(f"axis_of_pair must name the axis of 32 pairs, not of {len(axis_of_pair)}")
+    words = _axis_words(tuple(axis_of_pair))
     (qs, qh, q1), (ps, ph, p1), (rs, r1) = q_nope.stride(), q_pe.stride(), kv_raw.stride()
     if T > 0 and not (q1 == p1 == r1 == 1):
         raise ValueError("q_nope, q_pe and kv_raw must have their last elements adjacent")
@@ -468,7 +474,7 @@ def mla_qkv_norm_rope_axes(q_nope, q_pe, kv_raw, slots, positions, axis_of_pair,
     _check(load().mla_qkv_norm_rope_axes(
         q_nope.data_ptr(), qs, qh, q_pe.data_ptr(), ps, ph, nope + 64, q_eps is not None, _ptr(q_norm_weight),
         0.0 if q_eps is None else float(q_eps), kv_raw.data_ptr(), rs, slots.data_ptr(), positions.data_ptr(),
-        positions.shape[0], (ctypes.c_int32 * 32)(*axis_of_pair), kv_norm_weight.data_ptr(), float(kv_eps),
+        positions.shape[0], words, kv_norm_weight.data_ptr(), float(kv_eps),
         freqs.data_ptr(), freqs.shape[0], T, N, q_out.data_ptr(), kv_cache.data_ptr(), layout, kv_cache.shape[0], page_size,
         _ptr(status), _stream(stream)))
 

@@ -763,7 +763,6 @@ int mla_qkv_norm_rope_axes(const void* q_nope, int64_t q_nope_token_stride, int6
     if (axis_of_pair[i] < 0 || axis_of_pair[i] >= num_axes)
       return fail(MLA_ERR_INVALID_ARG, "mla_qkv_norm_rope_axes: pair %d has axis %d of %d", i, axis_of_pair[i], num_axes);
     a.axis_of_pair |= static_cast<uint64_t>(axis_of_pair[i]) << (2 * i);
-    a.used_axes |= 1u << axis_of_pair[i];
   }
   int64_t rb, pb;
   int dqk;

@@ -26,29 +26,20 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     f32x2_to_bf16x2(v[6], v[7]));
 }
 
-// The token's rows of the (cos, sin) table, one an axis. ok: every axis in use has a position inside the table; below: all
-// of them are negative (padding, with a negative slot).
-struct Angles {
-  const float* row[4];
-  uint64_t axis_of_pair;
-  bool ok, below;
-  __device__ __forceinline__ Angles(const AxesParams& P, int t) : axis_of_pair(P.axis_of_pair), ok(true), below(true) {
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      row[a] = P.qkv.freqs;
-      if (!((P.used_axes >> a) & 1u)) continue;
-      const int pos = P.qkv.positions[static_cast<int64_t>(a) * P.qkv.tokens + t];
-      ok &= pos >= 0 && pos < P.qkv.max_pos;
-      below &= pos < 0;
-      row[a] = P.qkv.freqs + static_cast<int64_t>(pos) * 64;
-    }
-  }
-  __device__ __forceinline__ float2 operator()(int i) const {
-    const uint32_t a = static_cast<uint32_t>(axis_of_pair >> (2 * i)) & 3u;
-    const float* f = a < 2u ? (a == 0u ? row[0] : row[1]) : (a == 2u ? row[2] : row[3]);
-    return reinterpret_cast<const float2*>(f)[i];
+// Where a token's pairs take their angles: lane i holds the position of pair i's axis.
+struct Places {
+  int pos;
+  bool ok, below;  // all of them inside the table; all negative (padding, with a negative slot)
+  __device__ __forceinline__ Places(const AxesParams& P, int t, int lane) {
+    const int axis = static_cast<int>(P.axis_of_pair >> (2 * lane)) & 3;
+    pos = P.qkv.positions[static_cast<int64_t>(axis) * P.qkv.tokens + t];
+    ok = __all_sync(0xffffffffu, pos >= 0 && pos < P.qkv.max_pos);
+    below = __all_sync(0xffffffffu, pos < 0);
   }
 };
+__device__ __forceinline__ float2 angle_at(const float* freqs, int pos, int pair) {
+  return reinterpret_cast<const float2*>(freqs)[static_cast<int64_t>(pos) * 32 + pair];
+}
 
 __device__ __forceinline__ uint32_t rotate2(uint32_t two, float2 cs) {
   const float x0 = __uint_as_float(two << 16), x1 = __uint_as_float(two & 0xFFFF0000u);
@@ -56,10 +47,10 @@ __device__ __forceinline__ uint32_t rotate2(uint32_t two, float2 cs) {
 }
 
 // The first blocks take the KV rows, one warp each, with the arithmetic of the other fused writes. The others take the
-// queries: a warp holds its token's angles in registers (they are the same for all heads) and goes through `per` heads.
-// Bound by the bytes and, for those, by the loads in flight.
+// queries: a warp has four heads of a token (192-wide rows) or one (the others). Bound by the bytes and, for those, by the
+// loads in flight: full occupancy, and a warp asks for its rows before it looks at the positions.
 template <int WIDTH>
-__global__ void __launch_bounds__(kAxesWarps * 32) axes_kernel(const __grid_constant__ AxesParams A, int per) {
+__global__ void __launch_bounds__(kAxesWarps * 32, 8) axes_kernel(const __grid_constant__ AxesParams A) {
   pdl_trigger();
   pdl_wait();
   const QkvParams& P = A.qkv;
@@ -71,116 +62,127 @@ __global__ void __launch_bounds__(kAxesWarps * 32) axes_kernel(const __grid_cons
     const int slot = P.slots[t];
     if (slot < 0) return;
     const int page = slot >> (31 - __clz(P.page_size));  // (a power of two)
-    const Angles angle(A, t);
-    const uint32_t bad = (page >= P.num_pages ? 4u : 0u) | (angle.ok ? 0u : 8u);
+    const Places at(A, t, lane);
+    const uint32_t bad = (page >= P.num_pages ? 4u : 0u) | (at.ok ? 0u : 8u);
     if (bad != 0u) {  // reported, not written
       if (lane == 0 && P.status != nullptr) atomicOr(P.status, bad);
       return;
     }
-    norm_rope_row_by(P.kv_raw + (int64_t)t * P.kv_row_stride, P.kv_weight, P.kv_eps, angle, row_width(P.layout), lane,
-                     srow[wi]);
+    const uint16_t* raw = P.kv_raw + (int64_t)t * P.kv_row_stride;
+    if (WIDTH == 512) {
+      int pos[8];  // of the pairs that lanes 28-31 turn
+#pragma unroll
+      for (int k = 0; k < 8; ++k) pos[k] = __shfl_sync(0xffffffffu, at.pos, 8 * (lane & 3) + k);
+      norm_rope_row_by(raw, P.kv_weight, P.kv_eps, [&](int i, int k) { return angle_at(P.freqs, pos[k], i); }, 512, lane, srow[wi]);
+    } else {
+      norm_rope_row_by(raw, P.kv_weight, P.kv_eps, [&](int i, int) { return angle_at(P.freqs, at.pos, i); }, 576, lane, srow[wi]);
+    }
     write_any_row(srow[wi], lane, P.kv, P.layout, page, slot & (P.page_size - 1), P.page_size, P.page_bytes);
     return;
   }
-  const int groups = (P.heads + per - 1) / per;  // of heads
-  const int64_t w = static_cast<int64_t>(blockIdx.x - P.kv_blocks) * kAxesWarps + wi;
-  if (w >= static_cast<int64_t>(P.tokens) * groups) return;
+  constexpr int kHeads = WIDTH == 192 ? 4 : 1;
+  // (the entry point keeps tokens * heads below 2^31)
+  const uint32_t groups = (P.heads + kHeads - 1) / kHeads;
+  const uint32_t w = (blockIdx.x - P.kv_blocks) * kAxesWarps + wi;
   const int t = static_cast<int>(w / groups);
-  const int n0 = static_cast<int>(w - static_cast<int64_t>(t) * groups) * per, n1 = min(n0 + per, P.heads);
-  const Angles angle(A, t);
-  if (!angle.ok) {  // left as it was; reported unless it is padding
-    if (lane == 0 && P.status != nullptr && !(angle.below && P.slots[t] < 0)) atomicOr(P.status, 8u);
-    return;
-  }
-  const uint16_t* qn = P.q_nope + t * P.nope_token_stride;
-  const uint16_t* qp = P.q_pe + t * P.pe_token_stride;
-  uint16_t* q = P.q_out + static_cast<int64_t>(t) * P.heads * WIDTH;
+  if (t >= P.tokens) return;
+  const int n0 = static_cast<int>(w - t * groups) * kHeads;
+  const uint16_t* qn = P.q_nope + t * P.nope_token_stride + n0 * P.nope_head_stride;
+  const uint16_t* qp = P.q_pe + t * P.pe_token_stride + n0 * P.pe_head_stride;
+  uint16_t* q = P.q_out + (static_cast<int64_t>(t) * P.heads + n0) * WIDTH;
+  auto report = [&](const Places& at) {  // rows left as they were; reported unless they are padding
+    if (lane == 0 && P.status != nullptr && !(at.below && P.slots[t] < 0)) atomicOr(P.status, 8u);
+  };
 
   if (WIDTH == 192) {
-    // four heads a step: 4 x 16 chunks of 16 bytes of the NoPE parts, two a lane, and 4 x 8 of the RoPE parts
-    const int c = lane & 7;
+    // 4 x 16 chunks of 16 bytes of the NoPE parts, two a lane, and 4 x 8 of the RoPE parts
+    const int left = P.heads - n0, h = lane >> 4, hp = lane >> 3, c = lane & 7;
+    uint4 u0, u1, up;
+    if (A.copy_nope) {
+      if (h < left) u0 = reinterpret_cast<const uint4*>(qn + h * P.nope_head_stride)[lane & 15];
+      if (h + 2 < left) u1 = reinterpret_cast<const uint4*>(qn + (h + 2) * P.nope_head_stride)[lane & 15];
+    }
+    if (hp < left) up = reinterpret_cast<const uint4*>(qp + hp * P.pe_head_stride)[c];
+    const Places at(A, t, lane);
+    if (!at.ok) return report(at);
     float2 cs[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) cs[k] = angle(4 * c + k);
-#pragma unroll 2
-    for (int n = n0; n < n1; n += 4) {
-      const int h0 = n + (lane >> 4), h1 = h0 + 2, hp = n + (lane >> 3);
-      uint4 u0, u1, up;
-      if (A.copy_nope) {
-        if (h0 < n1) u0 = reinterpret_cast<const uint4*>(qn + h0 * P.nope_head_stride)[lane & 15];
-        if (h1 < n1) u1 = reinterpret_cast<const uint4*>(qn + h1 * P.nope_head_stride)[lane & 15];
-      }
-      if (hp < n1) up = reinterpret_cast<const uint4*>(qp + hp * P.pe_head_stride)[c];
-      if (A.copy_nope) {
-        if (h0 < n1) reinterpret_cast<uint4*>(q + h0 * WIDTH)[lane & 15] = u0;
-        if (h1 < n1) reinterpret_cast<uint4*>(q + h1 * WIDTH)[lane & 15] = u1;
-      }
-      if (hp < n1)
-        reinterpret_cast<uint4*>(q + hp * WIDTH + 128)[c] =
-            make_uint4(rotate2(up.x, cs[0]), rotate2(up.y, cs[1]), rotate2(up.z, cs[2]), rotate2(up.w, cs[3]));
+    for (int k = 0; k < 4; ++k) cs[k] = angle_at(P.freqs, __shfl_sync(0xffffffffu, at.pos, 4 * c + k), 4 * c + k);
+    if (A.copy_nope) {
+      if (h < left) reinterpret_cast<uint4*>(q + h * WIDTH)[lane & 15] = u0;
+      if (h + 2 < left) reinterpret_cast<uint4*>(q + (h + 2) * WIDTH)[lane & 15] = u1;
     }
+    if (hp < left)
+      reinterpret_cast<uint4*>(q + hp * WIDTH + 128)[c] =
+          make_uint4(rotate2(up.x, cs[0]), rotate2(up.y, cs[1]), rotate2(up.z, cs[2]), rotate2(up.w, cs[3]));
     return;
   }
 
   // 64 chunks of 16 bytes, two a lane, normalised over their 512 elements where asked; the 576-wide rows' RoPE part is
   // a pair a lane, that of the 512-wide rows the last eight chunks
   const bool pe_lane = WIDTH == 512 && lane >= 24;
-  float2 cs[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    cs[k] = WIDTH == 576 ? (k == 0 ? angle(lane) : make_float2(1.f, 0.f)) : angle(4 * (lane & 7) + k);
-  for (int n = n0; n < n1; ++n) {
-    const uint16_t* an = qn + n * P.nope_head_stride;
-    const uint16_t* ap = qp + n * P.pe_head_stride;
-    const uint4 u0 = *reinterpret_cast<const uint4*>(an + 8 * lane);
-    const uint4 u1 = *reinterpret_cast<const uint4*>(pe_lane ? ap + 8 * (lane - 24) : an + 256 + 8 * lane);
-    uint32_t two = 0;
-    if (WIDTH == 576) two = reinterpret_cast<const uint32_t*>(ap)[lane];
-    uint4 o0 = u0, o1 = u1;
+  const bool nope = WIDTH == 512 || A.copy_nope;
+  uint4 u0, u1;
+  uint32_t two = 0;
+  if (nope) {
+    u0 = *reinterpret_cast<const uint4*>(qn + 8 * lane);
+    u1 = *reinterpret_cast<const uint4*>(pe_lane ? qp + 8 * (lane - 24) : qn + 256 + 8 * lane);
+  }
+  if (WIDTH == 576) two = reinterpret_cast<const uint32_t*>(qp)[lane];
+  const Places at(A, t, lane);
+  if (!at.ok) return report(at);
+  if (nope) {
     if (WIDTH == 512 || P.q_norm) {  // (a bf16 value goes through fp32 unchanged)
-      float a[8], b[8];
-      unpack8(u0, a);
-      unpack8(u1, b);
+      float rinv = 1.f;
+      float a[8];
       if (P.q_norm) {
-        float ss = 0.f;
+        float ss = 0.f, b[8];
+        unpack8(u0, a);
+        unpack8(u1, b);
 #pragma unroll
         for (int k = 0; k < 8; ++k) ss = fmaf(a[k], a[k], fmaf(b[k], b[k], ss));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float rinv = 1.0f / sqrtf(ss * (1.0f / 512.0f) + P.q_eps);
-        float wa[8], wb[8];
-        if (P.q_weight != nullptr) {
-          unpack8(reinterpret_cast<const uint4*>(P.q_weight)[lane], wa);
-          unpack8(reinterpret_cast<const uint4*>(P.q_weight)[32 + lane], wb);
-        }
+        rinv = 1.0f / sqrtf(ss * (1.0f / 512.0f) + P.q_eps);
+      }
+      // one chunk after the other: both at once would not fit the registers of full occupancy
+      auto scaled = [&](uint4 u, int chunk) {
+        unpack8(u, a);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          a[k] *= rinv;
-          b[k] *= rinv;
-          if (P.q_weight != nullptr) {
-            a[k] *= wa[k];
-            b[k] *= wb[k];
+        for (int k = 0; k < 8; ++k) a[k] *= rinv;
+        if (P.q_weight != nullptr) {
+          float g[8];
+          unpack8(reinterpret_cast<const uint4*>(P.q_weight)[chunk], g);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) a[k] *= g[k];
+        }
+      };
+      if (P.q_norm) {
+        scaled(u0, lane);
+        u0 = pack8(a);
+        scaled(u1, 32 + lane);
+      } else {
+        unpack8(u1, a);
+      }
+      if (WIDTH == 512) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = 4 * (lane & 7) + k;
+          const int pos = __shfl_sync(0xffffffffu, at.pos, i);
+          if (pe_lane) {
+            const float2 cs = angle_at(P.freqs, pos, i);
+            const float x0 = a[2 * k], x1 = a[2 * k + 1];
+            a[2 * k] = x0 * cs.x - x1 * cs.y;
+            a[2 * k + 1] = x0 * cs.y + x1 * cs.x;
           }
         }
       }
-      if (pe_lane) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x0 = b[2 * k], x1 = b[2 * k + 1];
-          b[2 * k] = x0 * cs[k].x - x1 * cs[k].y;
-          b[2 * k + 1] = x0 * cs[k].y + x1 * cs[k].x;
-        }
-      }
-      o0 = pack8(a);
-      o1 = pack8(b);
+      u1 = pack8(a);
     }
-    uint16_t* o = q + n * WIDTH;
-    if (A.copy_nope || WIDTH == 512) {
-      reinterpret_cast<uint4*>(o)[lane] = o0;
-      reinterpret_cast<uint4*>(o)[32 + lane] = o1;
-    }
-    if (WIDTH == 576) reinterpret_cast<uint32_t*>(o + 512)[lane] = rotate2(two, cs[0]);
+    reinterpret_cast<uint4*>(q)[lane] = u0;
+    reinterpret_cast<uint4*>(q)[32 + lane] = u1;
   }
+  if (WIDTH == 576) reinterpret_cast<uint32_t*>(q + 512)[lane] = rotate2(two, angle_at(P.freqs, at.pos, lane));
 }
 
 }  // namespace
@@ -188,12 +190,12 @@ __global__ void __launch_bounds__(kAxesWarps * 32) axes_kernel(const __grid_cons
 cudaError_t launch_qkv_norm_rope_axes(const AxesParams& p, cudaStream_t stream) {
   AxesParams a = p;
   a.qkv.kv_blocks = (p.qkv.tokens + kAxesWarps - 1) / kAxesWarps;
-  const int per = p.q_width == 192 ? 8 : 1;
+  const int per = p.q_width == 192 ? 4 : 1;
   const int64_t warps = static_cast<int64_t>(p.qkv.tokens) * ((p.qkv.heads + per - 1) / per);
   const dim3 grid(static_cast<unsigned>(a.qkv.kv_blocks + (warps + kAxesWarps - 1) / kAxesWarps)), block(kAxesWarps * 32);
-  if (p.q_width == 192) return launch_pdl(axes_kernel<192>, grid, block, 0, stream, a, per);
-  if (p.q_width == 576) return launch_pdl(axes_kernel<576>, grid, block, 0, stream, a, per);
-  return launch_pdl(axes_kernel<512>, grid, block, 0, stream, a, per);
+  if (p.q_width == 192) return launch_pdl(axes_kernel<192>, grid, block, 0, stream, a);
+  if (p.q_width == 576) return launch_pdl(axes_kernel<576>, grid, block, 0, stream, a);
+  return launch_pdl(axes_kernel<512>, grid, block, 0, stream, a);
 }
 
 }  // namespace mla

@@ -5,8 +5,8 @@
 // to the fp32 sum and the result is rounded to bf16 once.
 //
 // gemm_pair_kernel: many rows. Two SMs work as one tensor-core pair (tcgen05 .cta_group::2) on a tile of 256 rows x 256
-// columns: each holds its 128 rows of x and half of W's 256 rows of a slab, 32 KB a step of 64 in K for 2 x 256 x 256 x 64
-// operations, half of what two single SMs would move. Sums lie in TMEM twice, so that one tile's epilogue runs under the
+// columns (or fewer, a multiple of 32): each holds its 128 rows of x and half of W's 256 rows of a slab, 32 KB a step of 64 in K for
+// 2 x 256 x 256 x 64 operations, half of what two single SMs would move. Sums lie in TMEM twice, so that one tile's epilogue runs under the
 // next one's products. Bound by the tensor cores.
 //
 // gemm_narrow_kernel: few rows. Bound by W's bytes, so W takes the M side of the instruction (128 of its rows a CTA) and
@@ -22,22 +22,44 @@
 namespace mla {
 namespace {
 
-__device__ __forceinline__ float activate(float y, int act) {
-  if (act == 1) return __fdividef(y, 1.f + __expf(-y));  // silu
-  // gelu y Phi(y); erfc keeps its relative precision where 1 + erf would cancel
-  if (act == 2) return 0.5f * y * erfcf(y * -0.70710678118654752f);
-  return y;
+// What the epilogue does: bias and residual; an activation between them; or keys and values of the heads.
+enum { kPlain = 0, kSilu = 1, kGelu = 2, kKeysValues = 3 };
+
+// erfc(|z|) with a fractional error below 1.2e-7 (times what e^-z^2 loses for a rounded z^2): the Chebyshev fit of Press,
+// Teukolsky, Vetterling and Flannery, Numerical Recipes in C, 2nd ed., section 6.2 (erfcc).
+__device__ __forceinline__ float erfc_of_magnitude(float z) {
+  const float t = __fdividef(1.f, fmaf(0.5f, z, 1.f));
+  float p = 0.17087277f;
+  p = fmaf(t, p, -0.82215223f);
+  p = fmaf(t, p, 1.48851587f);
+  p = fmaf(t, p, -1.13520398f);
+  p = fmaf(t, p, 0.27886807f);
+  p = fmaf(t, p, -0.18628806f);
+  p = fmaf(t, p, 0.09678418f);
+  p = fmaf(t, p, 0.37409196f);
+  p = fmaf(t, p, 1.00002368f);
+  p = fmaf(t, p, -1.26551223f);
+  return t * __expf(fmaf(-z, z, p));
+}
+
+template <int KIND>
+__device__ __forceinline__ float activate(float y) {
+  if (KIND == kSilu) return __fdividef(y, 1.f + __expf(-y));
+  if (KIND != kGelu) return y;
+  // y Phi(y) = y erfc(-y / sqrt 2) / 2, from the side where nothing cancels
+  const float half = 0.5f * erfc_of_magnitude(fabsf(y) * 0.70710678118654752f);
+  return y * (y < 0.f ? half : 1.f - half);
 }
 
 // ----------------------------------------------------------------------------- CTA pairs
 constexpr int kGemmThreads = 320;              // TMA, MMA, 8 epilogue warps
-constexpr int kGemmStages = 5;
+constexpr int kGemmStages = 6;
 constexpr uint32_t kGemmA = 128 * 128;         // this CTA's 128 rows of x, 64 of K
 constexpr uint32_t kGemmB = 128 * 128;         // its half of W's 256 rows
 constexpr uint32_t kGemmStage = kGemmA + kGemmB;
 constexpr uint32_t kGemmOffStaging = kGemmStages * kGemmStage;
 constexpr uint32_t kGemmSlab = 32 * 128;       // 32 rows x 64 columns of the result: one warp's store
-constexpr uint32_t kGemmOffMisc = kGemmOffStaging + 8 * 2 * kGemmSlab;
+constexpr uint32_t kGemmOffMisc = kGemmOffStaging + 8 * kGemmSlab;
 
 struct GemmMisc {
   uint64_t full[kGemmStages], empty[kGemmStages];  // full: in the even CTA, both CTAs' bytes
@@ -50,18 +72,12 @@ struct GemmMisc {
 constexpr size_t kGemmSmem = kGemmOffMisc + sizeof(GemmMisc) + 1024;
 static_assert(kGemmSmem <= 232448, "shared memory budget of one CTA");
 
-// What the epilogue does: bias, residual and no activation; an activation too; or keys and values of the heads.
-enum { kPlain = 0, kActivated = 1, kKeysValues = 2 };
-
 // 32 rows x 64 columns, a row a lane, as 16-bit pairs to the warp's slab and from there to memory by TMA, so that rows leave
 // as whole 128-byte lines.
-__device__ __forceinline__ void store_slab(const CUtensorMap* map, uint32_t staging, int stores, int lane, const uint32_t (&o)[32],
-                                           int col0, int row0) {
-  if (stores >= 2) {
-    if (lane == 0) bulk_wait_read<1>();
-    __syncwarp();
-  }
-  const uint32_t slab = staging + (stores & 1) * kGemmSlab;
+__device__ __forceinline__ void store_slab(const CUtensorMap* map, uint32_t slab, int lane, const uint32_t (&o)[32], int col0,
+                                           int row0) {
+  if (lane == 0) bulk_wait_read<0>();
+  __syncwarp();
 #pragma unroll
   for (int q = 0; q < 8; ++q)
     st_shared_v4(slab + lane * 128 + ((q ^ (lane & 7)) << 4), make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
@@ -118,7 +134,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     const int b = t / (P.band * P.n_tiles), r = t - b * P.band * P.n_tiles;
     const int h = min(P.band, P.m_tiles - b * P.band);
     *m0 = (b * P.band + r % h) * 256;
-    *n0 = (r / h) * 256;
+    *n0 = (r / h) * P.tile_cols;
   };
 
   if (warp == 0) {
@@ -139,9 +155,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             break;
           }
           const uint32_t full = lead(&misc->full[s]);
-          mbar_arrive_expect_tx_cluster(full, kGemmStage);
+          mbar_arrive_expect_tx_cluster(full, kGemmA + P.tile_cols * 64);
           tma_load_2d_pair(a, &x_map, 64 * k, m0 + 128 * rank, full);
-          tma_load_2d_pair(a + kGemmA, &w_map, 64 * k, P.w_row0 + n0 + 128 * rank, full);
+          tma_load_2d_pair(a + kGemmA, &w_map, 64 * k, P.w_row0 + n0 + (P.tile_cols >> 1) * rank, full);
         }
       }
       if (*abort_flag && rank == 0)  // copies still in flight land on this CTA's barriers: wait for them (bounded)
@@ -149,45 +165,67 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           mbar_wait_drain_cluster(smem_addr(&misc->full[(it - k) % kGemmStages]), ((it - k) / kGemmStages) & 1);
     }
   } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, 0, 0);
+    // (the whole warp goes through the loop, so that descriptors stay in uniform registers)
+    if (rank == 0) {
+      const uint32_t idesc = idesc_bf16_f32(256, P.tile_cols, 0, 0);
       const uint64_t kmaj = sdesc_sw128(0, 16, 1024);
-      int it = 0, u = 0;
+      int s = 0, u = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int t = cluster_id_x(); t < tiles && ok; t += step, ++u) {
         const int buf = u & 1;
         if (u >= 2 && !wait_bar(smem_addr(&misc->acc_empty[buf]), ((u >> 1) - 1) & 1, abort_flag, status)) break;
         tc_fence_after();
-        for (int k = 0; k < P.k_blocks; ++k, ++it) {
-          const int s = it % kGemmStages;
-          if (!wait_bar(smem_addr(&misc->full[s]), (it / kGemmStages) & 1, abort_flag, status)) {
+        for (int k = 0; k < P.k_blocks; ++k) {
+          if (!wait_bar(smem_addr(&misc->full[s]), phase, abort_flag, status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint64_t a = kmaj | ((sb + s * kGemmStage) >> 4);
-          const uint64_t b = kmaj | ((sb + s * kGemmStage + kGemmA) >> 4);
+          if (elect_one()) {
+            const uint64_t a = kmaj | ((sb + s * kGemmStage) >> 4);
+            const uint64_t b = kmaj | ((sb + s * kGemmStage + kGemmA) >> 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mma_bf16_pair(tmem + buf * 256, a + 2 * i, b + 2 * i, idesc, (k | i) ? 1u : 0u);
-          mma_commit_pair(smem_addr(&misc->empty[s]), 3);
+            for (int i = 0; i < 4; ++i) mma_bf16_pair(tmem + buf * 256, a + 2 * i, b + 2 * i, idesc, (k | i) ? 1u : 0u);
+            mma_commit_pair(smem_addr(&misc->empty[s]), 3);
+          }
+          __syncwarp();
+          if (++s == kGemmStages) {
+            s = 0;
+            phase ^= 1;
+          }
         }
-        if (ok) mma_commit_pair(smem_addr(&misc->acc_full[buf]), 3);
+        if (ok && elect_one()) mma_commit_pair(smem_addr(&misc->acc_full[buf]), 3);
+        __syncwarp();
       }
-      mma_commit_pair(smem_addr(&misc->last), 1);
-      mbar_wait_drain_cluster(smem_addr(&misc->last), 0);
+      if (elect_one()) {
+        mma_commit_pair(smem_addr(&misc->last), 1);
+        mbar_wait_drain_cluster(smem_addr(&misc->last), 0);
+      }
+      __syncwarp();
     }
   } else {
-    // Epilogue: a warp reaches the TMEM lanes 32 (warp % 4) .. + 31, one row a lane, and takes half of the tile's columns.
+    // Epilogue: a warp reaches the TMEM lanes 32 (warp % 4) .. + 31, one row a lane, and takes half
+    // of the tile's columns (in products, every other 64).
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    const uint32_t staging = sb + kGemmOffStaging + (warp - 2) * 2 * kGemmSlab;
+    const uint32_t staging = sb + kGemmOffStaging + (warp - 2) * kGemmSlab;
     const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    int u = 0, stores = 0;
+    int u = 0;
+    uint4 res[8];
+    auto load_residual = [&](int m0, int col0, int width) {
+      const int row = m0 + 128 * rank + 32 * quarter + lane;
+      const int chunks = P.residual != nullptr && row < P.rows ? min(width, P.cols - col0) >> 3 : 0;
+      const uint16_t* rp = P.residual + row * P.residual_stride + col0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) res[q] = q < chunks ? *reinterpret_cast<const uint4*>(rp + 8 * q) : make_uint4(0, 0, 0, 0);
+    };
     for (int t = cluster_id_x(); t < tiles; t += step, ++u) {
       int m0, n0;
       place(t, &m0, &n0);
+      if (KIND != kKeysValues && u == 0) load_residual(m0, n0 + 64 * half, 64);
       const int buf = u & 1;
       const int row0 = m0 + 128 * rank + 32 * quarter;
-      const uint32_t src = tmem + buf * 256 + lane_off + 128 * half;
+      const uint32_t src = tmem + buf * 256 + lane_off;
       if (!wait_bar(smem_addr(&misc->acc_full[buf]), (u >> 1) & 1, abort_flag, status)) break;
       tc_fence_after();
       if (KIND == kKeysValues) {
@@ -197,7 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (row0 < P.rows) {
           uint32_t acc[128], o[32];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) tmem_ld32(src + 32 * k, acc + 32 * k);
+          for (int k = 0; k < 4; ++k) tmem_ld32(src + 128 * half + 32 * k, acc + 32 * k);
           tmem_wait_ld();
           float scale = 1.f;
           if (half == 1) {
@@ -219,25 +257,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
               const float a = __uint_as_float(acc[64 * c + 2 * k]), b = __uint_as_float(acc[64 * c + 2 * k + 1]);
               o[k] = half == 0 ? f32x2_to_bf16x2(a, b) : f32x2_to_f16x2(a * scale, b * scale);
             }
-            store_slab(&y_map, staging, stores++, lane, o, n0 + 128 * half + 64 * c, row0);
+            store_slab(&y_map, staging, lane, o, n0 + 128 * half + 64 * c, row0);
           }
         }
       } else {
 #pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          const int col0 = n0 + 128 * half + 64 * c;
+        for (int c = half; 64 * c < P.tile_cols; c += 2) {
+          const int col0 = n0 + 64 * c;
           if (row0 >= P.rows || col0 >= P.cols) break;  // (the same in all lanes)
           const int row = row0 + lane;
-          const int chunks = min(8, (P.cols - col0) >> 3);  // of 8 columns
+          const int width = min(64, P.tile_cols - 64 * c);           // 64, or 32 in the last of them
+          const int chunks = min(width, P.cols - col0) >> 3;         // of 8 columns
           uint32_t acc[64], o[32];
           tmem_ld32(src + 64 * c, acc);
           tmem_ld32(src + 64 * c + 32, acc + 32);
-          uint4 res[8];
-          const bool add = P.residual != nullptr && row < P.rows;
-          const uint16_t* rp = P.residual + row * P.residual_stride + col0;
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            res[q] = add && q < chunks ? *reinterpret_cast<const uint4*>(rp + 8 * q) : make_uint4(0, 0, 0, 0);
           tmem_wait_ld();
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
@@ -251,23 +284,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 y0 += __uint_as_float(bh[i] << 16);
                 y1 += __uint_as_float(bh[i] & 0xFFFF0000u);
               }
-              if (KIND == kActivated) {
-                y0 = activate(y0, P.act);
-                y1 = activate(y1, P.act);
-              }
-              if (add) {
+              y0 = activate<KIND>(y0);
+              y1 = activate<KIND>(y1);
+              if (P.residual != nullptr) {
                 y0 += __uint_as_float(rh[i] << 16);
                 y1 += __uint_as_float(rh[i] & 0xFFFF0000u);
               }
               o[4 * q + i] = f32x2_to_bf16x2(y0, y1);
             }
           }
-          store_slab(&y_map, staging, stores++, lane, o, col0, row0);
+          // the residual of the next columns, or of the next tile's first, while these leave
+          if (64 * (c + 2) < P.tile_cols) load_residual(m0, n0 + 64 * (c + 2), min(64, P.tile_cols - 64 * (c + 2)));
+          if (width == 64) {
+            store_slab(&y_map, staging, lane, o, col0, row0);
+          } else if (row < P.rows) {
+            uint16_t* dst = P.out + row * P.out_stride + col0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (q < chunks)
+                reinterpret_cast<uint4*>(dst)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          }
+          __syncwarp();
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(lead(&misc->acc_empty[buf]));
+      if (KIND != kKeysValues && t + step < tiles) {
+        place(t + step, &m0, &n0);
+        load_residual(m0, n0 + 64 * half, 64);
+      }
     }
     if (lane == 0) bulk_wait<0>();
   }
@@ -301,7 +347,8 @@ struct Narrow {
   static_assert(kStages <= 16 && NT * 128 * 4 <= kOffMisc, "");
 };
 
-template <int NT>
+// PARTS: CTAs of the cluster, which share K.
+template <int NT, int PARTS>
 __global__ void __launch_bounds__(kNarrowThreads)
     gemm_narrow_kernel(const __grid_constant__ GemmParams P, const __grid_constant__ CUtensorMap x_map,
                        const __grid_constant__ CUtensorMap w_map) {
@@ -314,7 +361,6 @@ __global__ void __launch_bounds__(kNarrowThreads)
   unsigned int* status = P.status != nullptr ? P.status : &misc->status;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
-  const int parts = P.split;  // CTAs of the cluster
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_addr(&misc->full[s]), 1);
@@ -335,10 +381,10 @@ __global__ void __launch_bounds__(kNarrowThreads)
   pdl_trigger();
   pdl_wait();
   const uint32_t tmem = misc->tmem_base;
-  const int tile = static_cast<int>(blockIdx.x) / parts;
+  const int tile = static_cast<int>(blockIdx.x) / PARTS;
   const int f0 = (tile % P.n_tiles) * 128, t0 = (tile / P.n_tiles) * NT;
-  const int k0 = static_cast<int>(static_cast<int64_t>(P.k_blocks) * rank / parts);
-  const int k1 = static_cast<int>(static_cast<int64_t>(P.k_blocks) * (rank + 1) / parts);
+  const int k0 = static_cast<int>(static_cast<int64_t>(P.k_blocks) * rank / PARTS);
+  const int k1 = static_cast<int>(static_cast<int64_t>(P.k_blocks) * (rank + 1) / PARTS);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -394,40 +440,80 @@ __global__ void __launch_bounds__(kNarrowThreads)
   }
   __syncthreads();
   cluster_sync_all();
-  // rank r sums and writes every parts-th row: 64 threads a row, two features each
-  for (int i = (threadIdx.x >> 6) * parts + rank; i < NT && t0 + i < P.rows; i += (kNarrowThreads >> 6) * parts) {
-    const int f = 2 * (threadIdx.x & 63);
-    if (f0 + f >= P.cols) continue;
-    const uint32_t at = sb + (i * 128 + f) * 4;
-    float y0 = 0.f, y1 = 0.f;
-    for (int p = 0; p < parts; ++p) {
-      const uint32_t peer = map_shared_rank(at, p);
-      y0 += ld_shared_cluster_f32(peer);
-      y1 += ld_shared_cluster_f32(peer + 4);
+  // Rank r sums and writes every PARTS-th row: a warp a row, four features a lane; its loads from the peers (and of the
+  // residual) are in flight together.
+  constexpr int kWarps = kNarrowThreads / 32, kAtOnce = 16 / PARTS;
+  const int f = 4 * lane;
+  const bool inside = f0 + f < P.cols;
+  float bias[4] = {0.f, 0.f, 0.f, 0.f};
+  if (P.bias != nullptr && inside) {
+    const uint2 b = *reinterpret_cast<const uint2*>(P.bias + f0 + f);
+    bias[0] = __uint_as_float(b.x << 16);
+    bias[1] = __uint_as_float(b.x & 0xFFFF0000u);
+    bias[2] = __uint_as_float(b.y << 16);
+    bias[3] = __uint_as_float(b.y & 0xFFFF0000u);
+  }
+  const int rows = min(NT, P.rows - t0);
+  for (int i0 = warp * PARTS + rank; i0 < rows; i0 += kAtOnce * kWarps * PARTS) {
+    float4 y[kAtOnce];
+    uint2 res[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kWarps * PARTS;
+      res[u] = make_uint2(0, 0);
+      if (P.residual != nullptr && i < rows && inside)
+        res[u] = *reinterpret_cast<const uint2*>(P.residual + (t0 + i) * P.residual_stride + f0 + f);
     }
-    if (P.bias != nullptr) {
-      const uint32_t b = *reinterpret_cast<const uint32_t*>(P.bias + f0 + f);
-      y0 += __uint_as_float(b << 16);
-      y1 += __uint_as_float(b & 0xFFFF0000u);
+    float4 v[PARTS][kAtOnce];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) {
+      const uint32_t peer = map_shared_rank(sb + f * 4, p);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const int i = i0 + u * kWarps * PARTS;
+        v[p][u] = i < rows ? ld_shared_cluster_v4(peer + i * 512) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
     }
-    if (P.act != 0) {
-      y0 = activate(y0, P.act);
-      y1 = activate(y1, P.act);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      y[u] = v[0][u];
+#pragma unroll
+      for (int p = 1; p < PARTS; ++p) {
+        y[u].x += v[p][u].x;
+        y[u].y += v[p][u].y;
+        y[u].z += v[p][u].z;
+        y[u].w += v[p][u].w;
+      }
     }
-    if (P.residual != nullptr) {
-      const uint32_t r = *reinterpret_cast<const uint32_t*>(P.residual + (t0 + i) * P.residual_stride + f0 + f);
-      y0 += __uint_as_float(r << 16);
-      y1 += __uint_as_float(r & 0xFFFF0000u);
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int i = i0 + u * kWarps * PARTS;
+      if (i >= rows || !inside) continue;
+      float v[4] = {y[u].x + bias[0], y[u].y + bias[1], y[u].z + bias[2], y[u].w + bias[3]};
+      if (P.act == kSilu) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = activate<kSilu>(v[k]);
+      } else if (P.act == kGelu) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = activate<kGelu>(v[k]);
+      }
+      if (P.residual != nullptr) {
+        v[0] += __uint_as_float(res[u].x << 16);
+        v[1] += __uint_as_float(res[u].x & 0xFFFF0000u);
+        v[2] += __uint_as_float(res[u].y << 16);
+        v[3] += __uint_as_float(res[u].y & 0xFFFF0000u);
+      }
+      *reinterpret_cast<uint2*>(P.out + (t0 + i) * P.out_stride + f0 + f) =
+          make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
     }
-    *reinterpret_cast<uint32_t*>(P.out + static_cast<int64_t>(t0 + i) * P.out_stride + f0 + f) = f32x2_to_bf16x2(y0, y1);
   }
   cluster_sync_all();  // no CTA leaves while a peer reads its sums
   if (warp == 1) tmem_dealloc(tmem, kCols);
 }
 
-template <int NT>
+template <int NT, int PARTS>
 cudaError_t narrow(const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map, int grid, cudaStream_t stream) {
-  auto kern = gemm_narrow_kernel<NT>;
+  auto kern = gemm_narrow_kernel<NT, PARTS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Narrow<NT>::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -439,12 +525,22 @@ cudaError_t narrow(const GemmParams& p, const CUtensorMap& x_map, const CUtensor
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[1].val.clusterDim.x = PARTS;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kern, p, x_map, w_map);
+}
+
+template <int NT>
+cudaError_t narrow_by(const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map, int grid, cudaStream_t stream) {
+  switch (p.split) {
+    case 1: return narrow<NT, 1>(p, x_map, w_map, grid, stream);
+    case 2: return narrow<NT, 2>(p, x_map, w_map, grid, stream);
+    case 4: return narrow<NT, 4>(p, x_map, w_map, grid, stream);
+    default: return narrow<NT, 8>(p, x_map, w_map, grid, stream);
+  }
 }
 
 }  // namespace
@@ -457,16 +553,16 @@ cudaError_t launch_gemm_pair(const GemmParams& p, const CUtensorMap& x_map, cons
     return launch_pdl(kern, dim3(2 * clusters), dim3(kGemmThreads), kGemmSmem, stream, p, x_map, w_map, y_map);
   };
   if (p.value_exp != nullptr) return go(gemm_pair_kernel<kKeysValues>);
-  return p.act == 0 ? go(gemm_pair_kernel<kPlain>) : go(gemm_pair_kernel<kActivated>);
+  return p.act == kPlain ? go(gemm_pair_kernel<kPlain>) : p.act == kSilu ? go(gemm_pair_kernel<kSilu>) : go(gemm_pair_kernel<kGelu>);
 }
 
 cudaError_t launch_gemm_narrow(int rows_a_cta, const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,
                                int grid, cudaStream_t stream) {
   switch (rows_a_cta) {
-    case 16: return narrow<16>(p, x_map, w_map, grid, stream);
-    case 32: return narrow<32>(p, x_map, w_map, grid, stream);
-    case 64: return narrow<64>(p, x_map, w_map, grid, stream);
-    default: return narrow<128>(p, x_map, w_map, grid, stream);
+    case 16: return narrow_by<16>(p, x_map, w_map, grid, stream);
+    case 32: return narrow_by<32>(p, x_map, w_map, grid, stream);
+    case 64: return narrow_by<64>(p, x_map, w_map, grid, stream);
+    default: return narrow_by<128>(p, x_map, w_map, grid, stream);
   }
 }
 

@@ -172,7 +172,7 @@ __device__ __forceinline__ void write_any_row(const uint16_t* x, int lane, uint8
 // RMSNorm of the 512 latent elements and RoPE of the 64 RoPE elements of one raw row x
 // (16-byte aligned), in fp32, rounded once to bf16 into srow (shared memory; all lanes of the warp
 // take part, and it ends with a __syncwarp). Lane l holds latent elements [16 l, 16 l + 16) and
-// RoPE pair l of the 576-wide layouts; angle(i) is pair i's (cos, sin).
+// RoPE pair l of the 576-wide layouts; angle(i, k) is pair i's (cos, sin), k-th of this lane's.
 template <class Angle>
 __device__ __forceinline__ void norm_rope_row_by(const uint16_t* x, const uint16_t* w, float eps,
                                                  Angle angle, int width, int lane, uint16_t* srow) {
@@ -207,7 +207,7 @@ __device__ __forceinline__ void norm_rope_row_by(const uint16_t* x, const uint16
     // 512-wide row: elements 448..511 (lanes 28-31) are the RoPE part, rotated after the norm
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float2 cs = angle(8 * (lane - 28) + k);
+      const float2 cs = angle(8 * (lane - 28) + k, k);
       const float c = cs.x, s = cs.y;
       const float x0 = v[2 * k], x1 = v[2 * k + 1];
       v[2 * k] = x0 * c - x1 * s;
@@ -223,7 +223,7 @@ __device__ __forceinline__ void norm_rope_row_by(const uint16_t* x, const uint16
     // k_pe (elements 512..575) is rotated as it comes, without the norm
     const uint32_t two = reinterpret_cast<const uint32_t*>(x + 512)[lane];
     const float x0 = bf16_to_f32(two & 0xFFFFu), x1 = bf16_to_f32(two >> 16);
-    const float2 cs = angle(lane);
+    const float2 cs = angle(lane, 0);
     const float c = cs.x, s = cs.y;
     reinterpret_cast<uint32_t*>(srow + 512)[lane] = f32x2_to_bf16x2(x0 * c - x1 * s, x0 * s + x1 * c);
   }
@@ -233,7 +233,7 @@ __device__ __forceinline__ void norm_rope_row_by(const uint16_t* x, const uint16
 // The same with f the position's row of the (cos, sin) table.
 __device__ __forceinline__ void norm_rope_row(const uint16_t* x, const uint16_t* w, float eps,
                                               const float* f, int width, int lane, uint16_t* srow) {
-  norm_rope_row_by(x, w, eps, [&](int i) { return make_float2(f[2 * i], f[2 * i + 1]); }, width, lane, srow);
+  norm_rope_row_by(x, w, eps, [&](int i, int) { return make_float2(f[2 * i], f[2 * i + 1]); }, width, lane, srow);
 }
 
 // The row at offset `off` of the page pg, decoded to bf16 into dst, by one warp. A lane takes eight elements a step, so

@@ -233,6 +233,7 @@ int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layou
       g.m_tiles = (g.rows + 255) / 256;
       g.n_tiles = p.group_heads;
       g.band = 8;
+      g.tile_cols = 256;
       g.w_row0 = head0 * 256;
       const int64_t tiles = static_cast<int64_t>(g.m_tiles) * g.n_tiles;
       e = mla::launch_gemm_pair(g, x_map, w_map, y_map, static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2), s);
@@ -296,26 +297,45 @@ int mla_linear(const void* x, int64_t x_stride, const void* weight, const void* 
   int num_sms = 0;
   if (int rc = mla::current_sm_count(&num_sms)) return rc;
   CUtensorMap x_map, w_map, y_map;
-  if (int rc = rows_map("mla_linear: weight", &w_map, weight, inner, outer, inner, 64, 128)) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (rows <= 128) {
+  // Few rows go to the kernel that splits K (64 x 4096 x 4096 in 11.2 us against 16.4 on pairs, 64 x 16384 x 8192 in 46
+  // against 62), unless K is too short to be worth its exchange of sums (128 x 512 x 2048: 7.0 against 5.5, 64 x 1544 x 6152:
+  // 10.3 against 9.8).
+  if (rows <= 32 || (rows <= 128 && g.k_blocks > 32)) {
     const int nt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
     if (int rc = rows_map("mla_linear: x", &x_map, x, inner, rows, x_stride, 64, nt)) return rc;
+    if (int rc = rows_map("mla_linear: weight", &w_map, weight, inner, outer, inner, 64, 128)) return rc;
     g.n_tiles = (outer + 127) / 128;
     g.m_tiles = 1;
     g.split = 1;
+    // CTAs enough for the SMs (two fit one), with eight steps of K each at least: 1 x 16384 x 8192 in 72, 49, 42 and 46 us at 1,
+    // 2, 4 and 8
     while (g.split < 8 && static_cast<int64_t>(g.n_tiles) * g.split < num_sms && g.k_blocks >= 8 * g.split) g.split *= 2;
     e = mla::launch_gemm_narrow(nt, g, x_map, w_map, g.n_tiles * g.split, s);
   } else {
     if (int rc = rows_map("mla_linear: x", &x_map, x, inner, rows, x_stride, 64, 128)) return rc;
     if (int rc = rows_map("mla_linear: out", &y_map, out, outer, rows, out_stride, 64, 32)) return rc;
+    const int64_t pairs = num_sms / 2;
     g.m_tiles = (rows + 255) / 256;
-    g.n_tiles = (outer + 255) / 256;
     g.band = 8;
-    const int64_t tiles = static_cast<int64_t>(g.m_tiles) * g.n_tiles;
+    // The tile's width with the shortest run: rounds over the pairs times a tile's time. That falls slowly with its columns
+    // (the steps in K cost nearly the same: 4096 x 4096 x 4096 in 19.3 us a round at 128 columns, 22.3 at 256), so what
+    // a narrower tile can win is a round: 1001 x 1544 x 6152 in two rounds, 30.5 us at 256 columns and 27.3 at 192.
+    int64_t best = 0, tiles = 0;
+    for (int cols = 256; cols >= 128; cols -= 32) {
+      const int64_t n = static_cast<int64_t>(g.m_tiles) * ((outer + cols - 1) / cols);
+      const int64_t time = (n + pairs - 1) / pairs * (cols + 400);
+      if (best == 0 || time < best) {
+        best = time;
+        tiles = n;
+        g.tile_cols = cols;
+      }
+    }
     if (tiles >= (1ll << 30)) return fail(MLA_ERR_UNSUPPORTED, "mla_linear: too many tiles");
-    e = mla::launch_gemm_pair(g, x_map, w_map, y_map, static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2), s);
+    g.n_tiles = (outer + g.tile_cols - 1) / g.tile_cols;
+    if (int rc = rows_map("mla_linear: weight", &w_map, weight, inner, outer, inner, 64, g.tile_cols / 2)) return rc;
+    e = mla::launch_gemm_pair(g, x_map, w_map, y_map, static_cast<int>(tiles < pairs ? tiles : pairs), s);
   }
   if (e != cudaSuccess) return cuda_fail(e, "mla_linear: launch");
   return MLA_OK;

@@ -140,7 +140,6 @@ cudaError_t launch_kv_gather(const uint8_t* kv, int layout, int64_t num_pages, i
 struct AxesParams {
   QkvParams qkv;                  // positions: [axes, T]
   uint64_t axis_of_pair;          // two bits a pair
-  uint32_t used_axes;             // one bit an axis
   int32_t q_width;                // 192, or the layout's row width
   int32_t copy_nope;              // the queries' NoPE part has to be written (it is not q_out's own, or is normalised)
 };
@@ -151,14 +150,15 @@ struct GemmParams {
   const uint16_t* bias;           // bf16 [cols] or null
   const uint16_t* residual;       // bf16 [rows, cols], residual_stride elements apart, or null
   int64_t residual_stride;
-  uint16_t* out;                  // the narrow kernel's output (the pair kernel's goes through its tensor map)
+  uint16_t* out;                  // (most of the pair kernel's output goes through its tensor map)
   int64_t out_stride;
   unsigned int* status;           // or null
   float* value_exp;               // pair: not null for keys and values of heads, [heads, value_exp_stride]: the power of two
   int64_t value_exp_stride;       // that each 32 rows of a head's values are scaled down by
   int32_t rows, cols, k_blocks;   // k_blocks: steps of 64 in K
   int32_t act;                    // 0 none, 1 silu, 2 gelu
-  int32_t m_tiles, n_tiles, band; // pair: tiles of 256 x 256; narrow: n_tiles of 128 columns
+  int32_t m_tiles, n_tiles, band; // pair: tiles of 256 x tile_cols; narrow: n_tiles of 128 columns
+  int32_t tile_cols;              // pair: 128 to 256, a multiple of 32 (its half: rows of W in a box of w_map)
   int32_t w_row0;                 // pair: first row of W
   int32_t split;                  // narrow: CTAs that share a tile's K
 };
