@@ -486,7 +486,7 @@ class ChunkPlan:
     batch: int
     heads: int
     group: int                   # heads whose keys and values are held at once
-    slots: int                   # partial results that are merged
+    slots: int                   # rows of partial results that are merged
     workspace_bytes: int
     info: _ChunkInfo
 

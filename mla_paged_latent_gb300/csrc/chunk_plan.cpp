@@ -14,16 +14,16 @@
 namespace mla {
 namespace {
 
-// In units of one sub-tile (256 queries) against one KV tile, about 0.7 us of a pair: what a unit costs besides its tiles
-// (loads of Q, the first scores, the epilogue), and what a merge has to save to be worth its launch and its partials.
-constexpr int64_t kUnitCost = 6;
-constexpr int64_t kMergeCost = 12;
-// A sub-tile alone takes longer than half of two whose products and softmax overlap.
-constexpr int64_t kAlone = 3, kBoth = 4;  // halves of a sub-tile
-constexpr int kMinTiles = 4;              // of a piece
+// Costs in tenths of what two sub-tiles (of 256 queries) take for a KV tile, measured in SM cycles: two sub-tiles whose products
+// and softmax run under each other take 3090, one alone 2780. What a unit costs besides (loads of Q, the first scores, the
+// epilogue), and what a merge has to save to be worth its launch and its partial results.
+constexpr int64_t kBoth = 10, kAlone = 9;
+constexpr int64_t kUnitCost = 25;
+constexpr int64_t kMergeCost = 50;
+constexpr int kMinTiles = 4;  // of a piece
 
 struct QueryTile {
-  int32_t req, q0;
+  int32_t req, q0, rows;  // rows: queries, up to 512
   int32_t tiles[2];  // KV tiles of the sub-tiles
 };
 
@@ -31,7 +31,7 @@ int64_t tiles_cost(const QueryTile& q, int begin, int end) {
   const int lo = std::min(q.tiles[0], q.tiles[1]), hi = std::max(q.tiles[0], q.tiles[1]);
   const int64_t both = std::max(0, std::min(lo, end) - begin);
   const int64_t alone = std::max(0, std::min(hi, end) - std::max(lo, begin));
-  return (both * kBoth + alone * kAlone + 1) / 2;
+  return both * kBoth + alone * kAlone;
 }
 
 }  // namespace
@@ -50,7 +50,7 @@ ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int bat
     const int32_t blocks = (len + 127) / 128;
     p.tile_req.insert(p.tile_req.end(), blocks, b);
     for (int32_t q0 = 0; q0 < n; q0 += 512) {
-      QueryTile q = {b, q0, {0, 0}};
+      QueryTile q = {b, q0, std::min(512, n - q0), {0, 0}};
       for (int s = 0; s < 2; ++s) {
         const int64_t last = std::min<int64_t>(static_cast<int64_t>(q0) + 256 * (s + 1), n) - 1;
         if (q0 + 256 * static_cast<int64_t>(s) >= n) continue;
@@ -86,7 +86,7 @@ ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int bat
     for (int i = 0; i < pairs; ++i) free.push(Free(0, i));
     int64_t end = 0;
     bool cut = false;
-    int32_t slot = 0;
+    int64_t slot = 0;  // rows of partial results
     for (int h = 0; h < group; ++h)
       for (const QueryTile& q : tiles) {
         const int n = std::max(q.tiles[0], q.tiles[1]);
@@ -98,7 +98,7 @@ ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int bat
           Free f = free.top();
           free.pop();
           if (lists) {
-            const int32_t item[8] = {q.req, q.q0, h, t0, t1, pieces > 1 ? slot + i : -1, 0, 0};
+            const int32_t item[8] = {q.req, q.q0, h, t0, t1, pieces > 1 ? static_cast<int32_t>(slot + static_cast<int64_t>(i) * q.rows) : -1, 0, 0};
             (*lists)[f.second].insert((*lists)[f.second].end(), item, item + 8);
           }
           f.first += tiles_cost(q, t0, t1) + kUnitCost;
@@ -107,14 +107,14 @@ ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int bat
         }
         if (pieces > 1) {
           if (lists) {
-            const int32_t merge[8] = {q.req, q.q0, h, slot, pieces, 0, 0, 0};
+            const int32_t merge[8] = {q.req, q.q0, h, static_cast<int32_t>(slot), pieces, 0, 0, 0};
             p.merges.insert(p.merges.end(), merge, merge + 8);
           }
-          slot += pieces;
+          slot += static_cast<int64_t>(pieces) * q.rows;
         }
       }
-    if (lists) p.slots = slot;
-    return end + (cut ? kMergeCost : 0);
+    if (lists) p.slots = static_cast<int32_t>(slot);
+    return slot >= (1ll << 31) ? INT64_MAX : end + (cut ? kMergeCost : 0);
   };
   // no cut, or the one that ends first among pieces of a pair's whole share and of parts of it
   int64_t best_cap = 0;

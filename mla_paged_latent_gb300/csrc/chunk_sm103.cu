@@ -460,7 +460,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
         tc_fence_after();
       }
       const int64_t at = static_cast<int64_t>(w.q_start + row) * P.heads + P.head0 + w.head;  // row of out
-      const int64_t part = static_cast<int64_t>(w.slot) * 512 + mine;
+      const int64_t part = static_cast<int64_t>(w.slot) + mine;
       if (live) {
         if (w.slot >= 0) P.part_lse[part] = lse;
         else if (P.lse != nullptr) P.lse[at] = lse;
@@ -523,11 +523,12 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
   const int4 a = reinterpret_cast<const int4*>(P.merges)[2 * tile];      // request, q0, head, first slot
   const int4 b = reinterpret_cast<const int4*>(P.merges)[2 * tile + 1];  // pieces
   const int4 r = reinterpret_cast<const int4*>(P.requests)[a.x];
-  if (a.z >= P.group_heads || a.y + mine >= r.y) return;
+  const int rows = min(512, r.y - a.y);
+  if (a.z >= P.group_heads || mine >= rows) return;
   float top = -INFINITY;
   bool any = false;
   for (int p = 0; p < b.x; ++p) {
-    const float l = P.part_lse[static_cast<int64_t>(a.w + p) * 512 + mine];
+    const float l = P.part_lse[a.w + static_cast<int64_t>(p) * rows + mine];
     top = fmaxf(top, l);
     any |= l != -INFINITY;
   }
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
   float total = 0.f;
   if (any)
     for (int p = 0; p < b.x; ++p) {
-      const int64_t part = static_cast<int64_t>(a.w + p) * 512 + mine;
+      const int64_t part = a.w + static_cast<int64_t>(p) * rows + mine;
       const float l = P.part_lse[part];
       if (l == -INFINITY) continue;
       const float w = expf(l - top);

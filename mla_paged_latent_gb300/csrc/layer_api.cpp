@@ -43,8 +43,8 @@ ChunkSpace chunk_space(int64_t kv_rows, int64_t group, int64_t slots) {
   s.kv = s.rows + align256(n * 1152);
   s.value_exp = s.kv + n * static_cast<size_t>(group) * 512;
   s.part_out = s.value_exp + align256(n / 32 * static_cast<size_t>(group) * 4);
-  s.part_lse = s.part_out + static_cast<size_t>(slots) * 512 * 128 * 4;
-  s.end = s.part_lse + static_cast<size_t>(slots) * 512 * 4;
+  s.part_lse = s.part_out + static_cast<size_t>(slots) * 128 * 4;
+  s.end = s.part_lse + static_cast<size_t>(slots) * 4;
   return s;
 }
 

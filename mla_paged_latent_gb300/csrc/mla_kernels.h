@@ -167,8 +167,8 @@ cudaError_t launch_gemm_pair(const GemmParams& p, const CUtensorMap& x_map, cons
 cudaError_t launch_gemm_narrow(int rows_a_cta, const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,
                                int grid, cudaStream_t stream);
 
-// Range of a value exponent: values far below 1 need no larger scale for fp16 to hold them, and 2^-e is a normal number.
-constexpr int kValueExpMin = -24, kValueExpMax = 114;
+// Range of a value exponent: 2^(120 - 7) between the weights of two groups of rows is still a normal number.
+constexpr int kValueExpMin = -60, kValueExpMax = 60;
 
 // Attention of a chunk of new tokens (chunk_sm103.cu).
 struct ChunkParams {
@@ -183,8 +183,8 @@ struct ChunkParams {
   uint16_t* out;                  // bf16 [T, heads, 128]
   float* lse;                     // [T, heads] or null
   const float* value_exp;         // [group, kv_rows / 32]: values are held times 2^-e
-  float* part_out;                // [slots, 512, 128]
-  float* part_lse;                // [slots, 512]
+  float* part_out;                // [slots, 128]: a row a query and piece
+  float* part_lse;                // [slots]
   unsigned int* status;
   int64_t num_pages, page_bytes;
   int32_t page_size, log2_ps, max_pages;

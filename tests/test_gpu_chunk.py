@@ -201,3 +201,44 @@ def test_another_stream_and_a_captured_call():
     torch.cuda.synchronize()
     fresh = run_chunk(q, cache, new, w, SCALE)
     assert torch.equal(out, fresh[0]) and torch.equal(lse, fresh[1])
+
+
+def scaled_values(seed, new, lens, heads, exponents):
+    """Scores from the RoPE part alone; the latent rows of each 32 times a power of two of their own."""
+    q, cache, w = make(seed, new, lens, heads)
+    w[:, :128] = 0
+    n = cache.pages * cache.page
+    rows = normal(generator(seed + 100), n, 576)
+    power = 2.0 ** exponents(n // 16).repeat_interleave(16).double()  # of a page: two of them are 32 rows of a request, or not
+    rows[:, :512] = (rows[:, :512].double() * power[:, None]).to(torch.bfloat16)
+    mla.mla_kv_write(rows, torch.arange(n, dtype=torch.int32, device="cuda"), cache.data, 0, cache.page)
+    return q, cache, w
+
+
+@pytest.mark.parametrize("lo, hi", [(-20, 20), (-70, -60), (55, 70), (-4, 60)])
+def test_values_of_very_different_size(lo, hi):
+    new, lens = [150, 1], [700, 333]
+    exps = lambda n: torch.randint(lo, hi + 1, (n,), generator=generator(18), device="cuda")  # noqa: E731
+    check(*scaled_values(19, new, lens, 2, exps)[:2], new, scaled_values(19, new, lens, 2, exps)[2], rms=False)
+
+
+def test_values_that_are_zero():
+    new, lens = [40], [200]
+    q, cache, w = make(20, new, lens, 2)
+    w[:, 128:] = 0
+    out, lse, _, _ = run_chunk(q, cache, new, w, SCALE)
+    assert (out == 0).all() and torch.isfinite(lse).all()
+
+
+def test_an_infinite_value_stays_one():
+    """One latent element infinite, in a row that all queries of its tile see: the values that it reaches are infinite or NaN (its
+    key is too), queries of other requests do not change."""
+    new, lens = [20, 20], [300, 200]
+    q, cache, w = make(21, new, lens, 1)
+    want = run_chunk(q, cache, new, w, SCALE)[0]
+    rows = normal(generator(22), 1, 576)
+    rows[0, 5] = float("inf")
+    slot = int(cache.table[0, 0]) * cache.page
+    mla.mla_kv_write(rows, torch.tensor([slot], dtype=torch.int32, device="cuda"), cache.data, 0, cache.page)
+    out = run_chunk(q, cache, new, w, SCALE)[0]
+    assert not torch.isfinite(out[:20]).any() and torch.equal(out[20:], want[20:])
