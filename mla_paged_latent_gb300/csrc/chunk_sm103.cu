@@ -452,7 +452,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
       const float lse = empty ? -INFINITY : (ref + log2f(l_run)) * 0.6931471805599453f;
       const Unit w = read_unit(P, i);  // (again: no register holds it while the scores fill them)
       const int row = w.q0 + mine;
-      const bool live = row < w.n;
+      const bool live = row < w.n && w.q_start + row < P.tokens;  // (whatever a schedule says)
       if (tiles > 0) {
         if (!wait(misc->o_full[s], units)) break;
         ++units;
@@ -524,28 +524,36 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
   const int4 b = reinterpret_cast<const int4*>(P.merges)[2 * tile + 1];  // pieces
   const int4 r = reinterpret_cast<const int4*>(P.requests)[a.x];
   const int rows = min(512, r.y - a.y);
-  if (a.z >= P.group_heads || mine >= rows) return;
+  if (a.z >= P.group_heads || mine >= rows || r.x + a.y + mine >= P.tokens) return;
+  const float* lses = P.part_lse + a.w + mine;  // of piece p: p * rows further
   float top = -INFINITY;
   bool any = false;
-  for (int p = 0; p < b.x; ++p) {
-    const float l = P.part_lse[a.w + static_cast<int64_t>(p) * rows + mine];
+  for (int p = lane; p < b.x; p += 32) {
+    const float l = lses[static_cast<int64_t>(p) * rows];
     top = fmaxf(top, l);
     any |= l != -INFINITY;
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  any = __any_sync(0xffffffffu, any);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float total = 0.f;
   if (any)
-    for (int p = 0; p < b.x; ++p) {
-      const int64_t part = a.w + static_cast<int64_t>(p) * rows + mine;
-      const float l = P.part_lse[part];
-      if (l == -INFINITY) continue;
-      const float w = expf(l - top);
-      const float4 v = reinterpret_cast<const float4*>(P.part_out + part * 128)[lane];
-      total += w;
-      acc.x = fmaf(w, v.x, acc.x);
-      acc.y = fmaf(w, v.y, acc.y);
-      acc.z = fmaf(w, v.z, acc.z);
-      acc.w = fmaf(w, v.w, acc.w);
+    for (int p0 = 0; p0 < b.x; p0 += 32) {
+      const float l = p0 + lane < b.x ? lses[static_cast<int64_t>(p0 + lane) * rows] : -INFINITY;
+      const float mine_w = l == -INFINITY ? 0.f : expf(l - top);
+      const int n = min(32, b.x - p0);
+      const float4* src = reinterpret_cast<const float4*>(P.part_out) + (a.w + static_cast<int64_t>(p0) * rows + mine) * 32 + lane;
+#pragma unroll 4
+      for (int p = 0; p < n; ++p) {
+        const float w = __shfl_sync(0xffffffffu, mine_w, p);
+        const float4 v = src[static_cast<int64_t>(p) * rows * 32];
+        total += w;
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+      }
     }
   const float inv = any ? 1.0f / total : 0.f;
   const int64_t at = static_cast<int64_t>(r.x + a.y + mine) * P.heads + P.head0 + a.z;

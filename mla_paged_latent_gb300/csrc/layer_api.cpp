@@ -191,6 +191,7 @@ int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layou
   while ((1 << p.log2_ps) < page_size) ++p.log2_ps;
   p.max_pages = max_pages;
   p.kv_rows = I.kv_rows;
+  p.tokens = I.tokens;
   p.heads = I.heads;
   p.causal = I.causal;
   p.scale_log2 = sm_scale * 1.4426950408889634f;

@@ -188,7 +188,7 @@ struct ChunkParams {
   unsigned int* status;
   int64_t num_pages, page_bytes;
   int32_t page_size, log2_ps, max_pages;
-  int32_t kv_rows, heads, head0, group_heads, causal;
+  int32_t kv_rows, tokens, heads, head0, group_heads, causal;
   float scale_log2;
 };
 cudaError_t launch_chunk_rows(int layout, const ChunkParams& p, cudaStream_t stream);
