@@ -23,7 +23,8 @@ constexpr int64_t kMergeCost = 25, kMergeRows = 1200;
 constexpr int kMinTiles = 4;  // of a piece
 
 struct QueryTile {
-  int32_t req, q0, rows;  // rows: queries, up to 512
+  int32_t request[4];  // q_start, q_len, kv_start, kv_len
+  int32_t q0, rows;    // rows: queries, up to 512
   int32_t tiles[2];  // KV tiles of the sub-tiles
   int longest() const { return std::max(tiles[0], tiles[1]); }
 };
@@ -41,17 +42,17 @@ ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int bat
                           int num_sms) {
   ChunkPlan p;
   const int pairs = std::max(1, num_sms / 2);
-  p.requests.resize(4 * static_cast<size_t>(batch));
   int32_t q_start = 0, kv_start = 0;
   std::vector<QueryTile> tiles;
   for (int b = 0; b < batch; ++b) {
     const int32_t n = q_lens[b], len = kv_lens[b];
-    const int32_t r[4] = {q_start, n, kv_start, len};
-    std::copy(r, r + 4, p.requests.begin() + 4 * b);
     const int32_t blocks = (len + 127) / 128;
-    p.tile_req.insert(p.tile_req.end(), blocks, b);
+    for (int32_t k = 0; k < blocks; ++k) {
+      const int32_t tile[4] = {b, 128 * k, len, 0};
+      p.kv_tiles.insert(p.kv_tiles.end(), tile, tile + 4);
+    }
     for (int32_t q0 = 0; q0 < n; q0 += 512) {
-      QueryTile q = {b, q0, std::min(512, n - q0), {0, 0}};
+      QueryTile q = {{q_start, n, kv_start, len}, q0, std::min(512, n - q0), {0, 0}};
       for (int s = 0; s < 2; ++s) {
         const int64_t last = std::min<int64_t>(static_cast<int64_t>(q0) + 256 * (s + 1), n) - 1;
         if (q0 + 256 * static_cast<int64_t>(s) >= n) continue;
@@ -159,11 +160,11 @@ ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int bat
     for (size_t k = 0; k < n; ++k) {
       const Piece& y = pieces[i + k];
       const int32_t at = n > 1 ? static_cast<int32_t>(slot + static_cast<int64_t>(k) * q.rows) : -1;
-      const int32_t item[8] = {q.req, q.q0, x.head, y.begin, y.end, at, 0, 0};
-      lists[y.pair].insert(lists[y.pair].end(), item, item + 8);
+      const int32_t item[12] = {q.request[0], q.request[1], q.request[2], q.request[3], q.q0, x.head, y.begin, y.end, at, 0, 0, 0};
+      lists[y.pair].insert(lists[y.pair].end(), item, item + 12);
     }
     if (n > 1) {
-      const int32_t merge[8] = {q.req, q.q0, x.head, static_cast<int32_t>(slot), static_cast<int32_t>(n), 0, 0, 0};
+      const int32_t merge[8] = {q.request[0] + q.q0, q.rows, x.head, static_cast<int32_t>(slot), static_cast<int32_t>(n), 0, 0, 0};
       p.merges.insert(p.merges.end(), merge, merge + 8);
       slot += static_cast<int64_t>(n) * q.rows;
     }
@@ -174,7 +175,7 @@ ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int bat
   for (const std::vector<int32_t>& l : lists) {
     if (l.empty()) continue;  // (a pair without work is not launched)
     p.items.insert(p.items.end(), l.begin(), l.end());
-    p.pair_items.push_back(static_cast<int32_t>(p.items.size() / 8));
+    p.pair_items.push_back(static_cast<int32_t>(p.items.size() / 12));
   }
   return p;
 }

@@ -32,12 +32,11 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= P.kv_rows) return;
-  const int req = P.tile_req[row >> 7];
-  const int4 r = reinterpret_cast<const int4*>(P.requests)[req];  // q_start, q_len, kv_start, kv_len
-  const int pos = row - r.z;
+  const int4 tile = reinterpret_cast<const int4*>(P.kv_tiles)[row >> 7];  // request, position of the first row, kv_len
+  const int req = tile.x, pos = tile.y + (row & 127);
   uint4* dst = reinterpret_cast<uint4*>(P.rows + static_cast<int64_t>(row) * 576);
   int page = -1;
-  if (pos < r.w) {
+  if (pos < tile.z) {
     const int pi = pos >> P.log2_ps;
     if (pi < P.max_pages) page = P.block_table[static_cast<int64_t>(req) * P.max_pages + pi];
     if (page < 0 || page >= P.num_pages) {  // reported, read as zeros
@@ -124,23 +123,23 @@ __device__ __forceinline__ int row_limit(int causal, int len, int n, int i) {
 }
 
 __device__ __forceinline__ Unit read_unit(const ChunkParams& P, int item) {
-  const int4 a = reinterpret_cast<const int4*>(P.items)[2 * item];      // request, q0, head, first tile
-  const int4 b = reinterpret_cast<const int4*>(P.items)[2 * item + 1];  // last tile + 1, slot or -1
-  const int4 r = reinterpret_cast<const int4*>(P.requests)[a.x];
+  const int4 r = reinterpret_cast<const int4*>(P.items)[3 * item];      // q_start, q_len, kv_start, kv_len
+  const int4 a = reinterpret_cast<const int4*>(P.items)[3 * item + 1];  // q0, head, first tile, last tile + 1
+  const int slot = P.items[12 * item + 8];                              // or -1
   Unit u;
   u.q_start = r.x;
   u.n = r.y;
   u.kv_start = r.z;
   u.len = r.w;
-  u.q0 = a.y;
-  u.head = a.z;
-  u.tb = a.w;
-  u.slot = b.y;
+  u.q0 = a.x;
+  u.head = a.y;
+  u.tb = a.z;
+  u.slot = slot;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     const int last = min(u.q0 + 256 * (s + 1), u.n) - 1;
     const int lim = row_limit(P.causal, u.len, u.n, last);
-    const int t = min(lim <= 0 ? 0 : (lim + 127) >> 7, b.x) - u.tb;
+    const int t = min(lim <= 0 ? 0 : (lim + 127) >> 7, a.w) - u.tb;
     u.tiles[s] = u.q0 + 256 * s >= u.n || u.head >= P.group_heads || t < 0 ? 0 : t;
   }
   return u;
@@ -180,6 +179,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
     mbar_init(here(misc->last), 2);
     misc->abort = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&q_map);
+    tma_prefetch_desc(&kv_map);
+    tma_prefetch_desc(&rope_map);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_addr(&misc->tmem_base), 512);
@@ -199,9 +201,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
     // 128 x 72 + 256 x 216 = the launch's 384 x 168 registers
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 && lane == 0) {
-      tma_prefetch_desc(&q_map);
-      tma_prefetch_desc(&kv_map);
-      tma_prefetch_desc(&rope_map);
       int it = 0;            // KV tiles loaded
       int qn[2] = {0, 0};    // query sub-tiles loaded
       bool ok = true;
@@ -520,11 +519,10 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
   const int tile = blockIdx.x >> 6;
   const int mine = (blockIdx.x & 63) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
-  const int4 a = reinterpret_cast<const int4*>(P.merges)[2 * tile];      // request, q0, head, first slot
+  const int4 a = reinterpret_cast<const int4*>(P.merges)[2 * tile];      // first token, tokens, head, first slot
   const int4 b = reinterpret_cast<const int4*>(P.merges)[2 * tile + 1];  // pieces
-  const int4 r = reinterpret_cast<const int4*>(P.requests)[a.x];
-  const int rows = min(512, r.y - a.y);
-  if (a.z >= P.group_heads || mine >= rows || r.x + a.y + mine >= P.tokens) return;
+  const int rows = a.y;
+  if (a.z >= P.group_heads || mine >= rows || a.x + mine >= P.tokens) return;
   const float* lses = P.part_lse + a.w + mine;  // of piece p: p * rows further
   float top = -INFINITY;
   bool any = false;
@@ -556,7 +554,7 @@ __global__ void __launch_bounds__(256) chunk_merge_kernel(const __grid_constant_
       }
     }
   const float inv = any ? 1.0f / total : 0.f;
-  const int64_t at = static_cast<int64_t>(r.x + a.y + mine) * P.heads + P.head0 + a.z;
+  const int64_t at = static_cast<int64_t>(a.x + mine) * P.heads + P.head0 + a.z;
   reinterpret_cast<uint2*>(P.out + at * 128)[lane] =
       make_uint2(f32x2_to_bf16x2(acc.x * inv, acc.y * inv), f32x2_to_bf16x2(acc.z * inv, acc.w * inv));
   if (lane == 0 && P.lse != nullptr) P.lse[at] = any ? top + logf(total) : -INFINITY;

@@ -115,6 +115,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     mbar_init(smem_addr(&misc->last), 1);
     misc->abort = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&x_map);
+    tma_prefetch_desc(&w_map);
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_addr(&misc->tmem_base), 512);
@@ -139,8 +141,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      tma_prefetch_desc(&x_map);
-      tma_prefetch_desc(&w_map);
       int it = 0;
       bool ok = true;
       for (int t = cluster_id_x(); t < tiles && ok; t += step) {
@@ -369,6 +369,8 @@ __global__ void __launch_bounds__(kNarrowThreads)
     mbar_init(smem_addr(&misc->acc_full), 1);
     misc->abort = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&x_map);
+    tma_prefetch_desc(&w_map);
   }
   constexpr uint32_t kCols = NT < 32 ? 32 : NT;
   if (warp == 1) {
@@ -388,8 +390,6 @@ __global__ void __launch_bounds__(kNarrowThreads)
 
   if (warp == 0) {
     if (lane == 0) {
-      tma_prefetch_desc(&x_map);
-      tma_prefetch_desc(&w_map);
       int it = 0;
       for (int k = k0; k < k1; ++k, ++it) {
         const int s = it % C::kStages;

@@ -50,15 +50,14 @@ ChunkSpace chunk_space(int64_t kv_rows, int64_t group, int64_t slots) {
 
 // Sections of the schedule (32-bit words), each a multiple of four.
 struct ChunkSections {
-  int64_t tile_req, pair_items, items, merges, end;
+  int64_t pair_items, items, merges, end;  // (the first begins at 0)
 };
 ChunkSections chunk_sections(const mla_chunk_info& i) {
   auto four = [](int64_t x) { return (x + 3) & ~int64_t(3); };
   ChunkSections s;
-  s.tile_req = 4 * static_cast<int64_t>(i.batch);
-  s.pair_items = s.tile_req + four(i.kv_rows / 128);
+  s.pair_items = 4 * static_cast<int64_t>(i.kv_rows / 128);
   s.items = s.pair_items + four(i.pairs + 1);
-  s.merges = s.items + 8 * static_cast<int64_t>(i.items);
+  s.merges = s.items + 12 * static_cast<int64_t>(i.items);
   s.end = s.merges + 8 * static_cast<int64_t>(i.merges);
   return s;
 }
@@ -98,7 +97,7 @@ int mla_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
     info->kv_rows = static_cast<int32_t>(rows);
     info->group = static_cast<int32_t>(group);
     info->pairs = static_cast<int32_t>(p.pair_items.size()) - 1;
-    info->items = static_cast<int32_t>(p.items.size() / 8);
+    info->items = static_cast<int32_t>(p.items.size() / 12);
     info->merges = static_cast<int32_t>(p.merges.size() / 8);
     info->slots = p.slots;
     const ChunkSections s = chunk_sections(*info);
@@ -112,8 +111,7 @@ int mla_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
     auto put = [&](int64_t at, const std::vector<int32_t>& v) {
       if (!v.empty()) std::memcpy(sched + at, v.data(), v.size() * 4);
     };
-    put(0, p.requests);
-    put(s.tile_req, p.tile_req);
+    put(0, p.kv_tiles);
     put(s.pair_items, p.pair_items);
     put(s.items, p.items);
     put(s.merges, p.merges);
@@ -174,8 +172,7 @@ int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layou
   p.kv = static_cast<const uint8_t*>(kv_cache);
   p.block_table = block_table;
   p.rows = reinterpret_cast<uint16_t*>(ws + space.rows);
-  p.requests = sched;
-  p.tile_req = sched + at.tile_req;
+  p.kv_tiles = sched;
   p.pair_items = sched + at.pair_items;
   p.items = sched + at.items;
   p.merges = sched + at.merges;

@@ -175,11 +175,11 @@ struct ChunkParams {
   const uint8_t* kv;              // paged cache
   const int32_t* block_table;     // [batch, max_pages]
   uint16_t* rows;                 // bf16 [kv_rows, 576]
-  const int32_t* requests;        // [batch, 4]: q_start, q_len, kv_start, kv_len
-  const int32_t* tile_req;        // [kv_rows / 128]: the request of each 128 rows
+  const int32_t* kv_tiles;        // [kv_rows / 128, 4]: request, position of the first row, kv_len
   const int32_t* pair_items;      // [pairs + 1]
-  const int32_t* items;           // [items, 8]: request, q0, head, first KV tile, last + 1, slot or -1
-  const int32_t* merges;          // [merges, 8]: request, q0, head, first slot, pieces
+  const int32_t* items;           // [items, 12]: q_start, q_len, kv_start, kv_len of the request; q0, head, first KV tile,
+                                  // last + 1; slot or -1
+  const int32_t* merges;          // [merges, 8]: first token, tokens, head, first slot; pieces
   uint16_t* out;                  // bf16 [T, heads, 128]
   float* lse;                     // [T, heads] or null
   const float* value_exp;         // [group, kv_rows / 32]: values are held times 2^-e
@@ -237,7 +237,7 @@ __host__ __device__ inline int request_len(const DecodeParams& P, int r) {
 
 // Host plan of a chunk's attention (rule documented on mla_chunk_plan in include/mla_decode.h): the sections of ChunkParams.
 struct ChunkPlan {
-  std::vector<int32_t> requests, tile_req, pair_items, items, merges;
+  std::vector<int32_t> kv_tiles, pair_items, items, merges;
   int32_t slots = 0;
 };
 ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int batch, int heads, bool causal, int group,

@@ -25,13 +25,10 @@ def lib():
 # ------------------------------------------------------------------------------- the plan
 def sections(plan):
     i, w = plan.info, plan.sched
-    pad = lambda n: (n + 3) // 4 * 4  # noqa: E731
-    a = 4 * i.batch
-    b = a + pad(i.kv_rows // 128)
-    c = b + pad(i.pairs + 1)
-    d = c + 8 * i.items
-    return (w[:a].reshape(-1, 4), w[a:a + i.kv_rows // 128], w[b:b + i.pairs + 1], w[c:d].reshape(-1, 8),
-            w[d:d + 8 * i.merges].reshape(-1, 8))
+    a = 4 * (i.kv_rows // 128)
+    b = a + (i.pairs + 1 + 3) // 4 * 4
+    c = b + 12 * i.items
+    return (w[:a].reshape(-1, 4), w[a:a + i.pairs + 1], w[b:c].reshape(-1, 12), w[c:c + 8 * i.merges].reshape(-1, 8))
 
 
 def tiles_of(n, length, q0, causal):
@@ -50,20 +47,23 @@ def test_every_query_and_tile_once(lib, seed):
     heads, causal, sms = int(rng.choice([1, 7, 16])), bool(rng.integers(2)), int(rng.choice([2, 8, 152]))
     plan = mla.mla_chunk_plan(q, kv, heads, causal, num_sms=sms)
     i = plan.info
-    requests, tile_req, pairs, items, merges = sections(plan)
+    kv_tiles, pairs, items, merges = sections(plan)
     blocks = -(-kv // 128)
-    assert np.array_equal(requests[:, 0], np.cumsum(q) - q) and np.array_equal(requests[:, 1], q)
-    assert np.array_equal(requests[:, 2], 128 * (np.cumsum(blocks) - blocks)) and np.array_equal(requests[:, 3], kv)
-    assert np.array_equal(tile_req, np.repeat(np.arange(batch), blocks))
+    q_start, kv_start = np.cumsum(q) - q, 128 * (np.cumsum(blocks) - blocks)
+    of = np.repeat(np.arange(batch), blocks)
+    assert np.array_equal(kv_tiles[:, 0], of) and np.array_equal(kv_tiles[:, 2], kv[of])
+    assert np.array_equal(kv_tiles[:, 1], 128 * np.arange(len(of)) - kv_start[of])
     assert (i.tokens, i.kv_rows, i.heads, i.group) == (q.sum(), 128 * blocks.sum(), heads, heads)
     assert i.pairs <= max(1, sms // 2) and pairs[0] == 0 and pairs[-1] == i.items
     assert (np.diff(pairs) > 0).all()
+    request = {int(q_start[b]): b for b in range(batch) if q[b]}  # those without queries have no items
     seen, parts = {}, {}
-    for req, q0, head, t0, t1, slot, _, _ in items.tolist():
-        key = (req, q0, head)
-        seen.setdefault(key, []).append((t0, t1))
+    for qs, n, ks, length, q0, head, t0, t1, slot, *_ in items.tolist():
+        b = request[qs]
+        assert (n, ks, length) == (q[b], kv_start[b], kv[b])
+        seen.setdefault((b, q0, head), []).append((t0, t1))
         if slot >= 0:
-            parts.setdefault(key, []).append(slot)
+            parts.setdefault((b, q0, head), []).append(slot)
     want = {(b, q0, h) for b in range(batch) for q0 in range(0, int(q[b]), 512) for h in range(heads)}
     assert set(seen) == want
     for (b, q0, h), ranges in seen.items():
@@ -71,15 +71,19 @@ def test_every_query_and_tile_once(lib, seed):
         assert ranges[0][0] == 0 and ranges[-1][1] == tiles_of(int(q[b]), int(kv[b]), q0, causal)
         assert all(x[1] == y[0] for x, y in zip(ranges, ranges[1:]))
         assert (len(ranges) > 1) == ((b, q0, h) in parts)
-    used = 0
-    assert {tuple(m[:3]) for m in merges.tolist()} == set(parts)
-    for b, q0, h, first, n, *_ in merges.tolist():
-        rows = min(512, int(q[b]) - q0)
-        assert sorted(parts[b, q0, h]) == [first + rows * k for k in range(n)]
+    used, starts = 0, []
+    assert len(merges) == len(parts)
+    for token, rows, h, first, n, *_ in merges.tolist():
+        b = int(np.searchsorted(q_start, token, "right")) - 1
+        while q[b] == 0 or token >= q_start[b] + q[b]:
+            b -= 1
+        q0 = token - int(q_start[b])
+        assert rows == min(512, int(q[b]) - q0) and sorted(parts[b, q0, h]) == [first + rows * k for k in range(n)]
         used += n * rows
+        starts.append((first, n * rows))
     assert used == plan.slots
-    starts = sorted((f, n * min(512, int(q[b]) - q0)) for b, q0, h, f, n, *_ in merges.tolist())
-    assert all(a + n <= c for (a, n), (c, _) in zip(starts, starts[1:]))
+    starts.sort()
+    assert all(x + n <= y for (x, n), (y, _) in zip(starts, starts[1:]))
 
 
 @pytest.mark.parametrize("heads, budget, group", [(16, 0, 1), (16, 512 * 128, 1), (16, 5 * 512 * 128, 4), (7, 3 * 512 * 128, 3),
