@@ -49,6 +49,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b), "f"(c.x), "f"(c.y));
   return r;
 }
+__device__ __forceinline__ float2 fma2v(float2 a, float2 b, float2 c) {  // a b + c, lane by lane
+  float2 r;
+  asm("{\n .reg .b64 p, q, s, d;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n mov.b64 s, {%6, %7};\n"
+      " fma.rn.f32x2 d, p, q, s;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 r;
   asm("{\n .reg .b64 p, q, d;\n mov.b64 p, {%2, %3};\n mov.b64 q, {%4, %5};\n add.rn.f32x2 d, p, q;\n"
