@@ -7,10 +7,12 @@
 // (row, head) once. Three steps on one stream, and a fourth where the rows are few:
 //   chunk_rows_kernel  the requests' rows, in order, as bf16 [rows, 576]; each request starts at a multiple of 128 and the
 //                      rows up to the next are zeros, so that a masked row is never what memory happened to hold;
-//   the product of the latent part with W (gemm_pair_kernel), K and V of a group of heads rounded to bf16 [rows, heads, 256]
+//   the product of the latent part with W (gemm_pair_kernel), K (bf16) and V (fp16) of a group of heads [rows, heads, 256]
 //                      (operands of the tensor cores; the sums are fp32), which attention then reads many times;
 //   chunk_attention_kernel;
 //   chunk_merge_kernel where a query tile was split over the rows.
+// One after the other on 2048 queries after 32768 bf16 rows at 128 heads: 13, 735 and 3168 us (1.79 PFLOP/s of 640 operations a
+// query, row and head; in a loop the power limit makes 4.3 ms of the three).
 #include <cstdint>
 #include <type_traits>
 #include <cuda_runtime.h>
@@ -24,7 +26,7 @@ namespace mla {
 namespace {
 
 // ----------------------------------------------------------------------------- rows
-// One warp a row. Bound by the bytes: the stored row in, 1152 bytes out.
+// One warp a row. Bound by the bytes: the stored row in, 1152 bytes out (65736 bf16 rows in 21 us, 7 TB/s in and out).
 template <int LAYOUT>
 __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__ ChunkParams P) {
   pdl_trigger();
@@ -61,11 +63,15 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
 //   O += P V    M = 256, N = 128 (each CTA holds 64 of the value dims), K = 128: 8 instructions, P from TMEM
 // Single SMs would need all of K and V in each: 80 KB a tile instead of 40, more than shared memory brings in under the
 // products, and only one tile and a half fit beside Q.
-// TMEM: S of the two sub-tiles (128 columns each; P as bf16 pairs takes the first 64 once S has been read) and O (128 each).
+// TMEM: S of the two sub-tiles (128 columns each; P as fp16 pairs takes the first 64 once S has been read) and O (128 each).
 // A thread for each sub-tile issues PV(j) S(j+1) in turn: S(j+1) follows the PV(j) that reads P from the same columns, and
 // its completion says that O holds tile j, so a rescale of O needs no barrier of its own.
-// P is rounded to bf16, an operand of the tensor cores; maxima, sums and O are fp32. The running maximum moves (and O is
-// rescaled) only when a tile exceeds it by 2^32, so a row's sum stays below rows x 2^32 x max |V|.
+// Bound by the tensor cores in the end: 2 x 1280 cycles of products a KV tile and unit, 3090 traced. One issuing thread took
+// 4790 (its barrier tests and commits stood between the products), two that run freely 5040 (both softmaxes at once); turns
+// 3730, stages passed on by the softmax warps 3560, P in halves and nothing spilled 3090.
+// P and V are fp16, operands of the tensor cores: V comes scaled by a power of two for every 32 rows, which P makes good, and P
+// is kept below 2^15 by a reference that moves (and O is rescaled) only when a tile exceeds it by 2^8. Both in bf16 are off by
+// 0.0027 of the result against 0.0020 (in the mean square; the result's own rounding is 0.0017). Maxima, sums and O are fp32.
 // Shared memory per CTA: Q 2 x 48 KB, and 3 stages of K (64 rows x 192) and V (128 rows x 64 dims), 40 KB each.
 //   warp 0      TMA            warps 1, 2  MMA issue of sub-tile 0 and 1 (even CTA); warp 1 TMEM
 //   warps 4-7   softmax and epilogue of sub-tile 0, warps 8-11 of sub-tile 1: a query row a thread
@@ -263,76 +269,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
       // The two threads take turns, a tile each: sub-tiles that begin a tile at once would also need their P at once, and the
       // tensor cores would wait for both softmaxes.
       auto issuer = [&](auto sub) {
-      constexpr int s = decltype(sub)::value;
-      constexpr uint32_t idesc_s = idesc_bf16_f32(256, 128, 0, 0);
-      constexpr uint32_t idesc_o = idesc_f16_f32(256, 128, 0, 1);  // V: MN-major, 64 dims of each CTA
-      // low words of the descriptors: start address, and a leading offset that neither layout uses
-      const uint32_t q = ((sb + s * kQSub) >> 4) | (1u << 16), k0 = ((sb + kOffK) >> 4) | (1u << 16),
-                     v0 = ((sb + kOffV) >> 4) | (1u << 16);
-      const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128;
-      int it = 0, units = 0, scores = 0, turns = 0;  // KV tiles, units begun, score tiles whose P has been waited for, turns taken
-      bool ok = true;
-      for (int i = item0; i < item1 && ok; ++i) {
-        const Unit u = read_unit(P, i);
-        const int nt = max(u.tiles[0], u.tiles[1]), tiles = u.tiles[s];
-        auto issue_s = [&](int j) {  // K of tile j has landed
-          const uint32_t k = k0 + (it + j) % kKvStages * (kKBytes >> 4);
+        constexpr int s = decltype(sub)::value;
+        constexpr uint32_t idesc_s = idesc_bf16_f32(256, 128, 0, 0);
+        constexpr uint32_t idesc_o = idesc_f16_f32(256, 128, 0, 1);  // V: MN-major, 64 dims of each CTA
+        // low words of the descriptors: start address, and a leading offset that neither layout uses
+        const uint32_t q = ((sb + s * kQSub) >> 4) | (1u << 16), k0 = ((sb + kOffK) >> 4) | (1u << 16),
+                       v0 = ((sb + kOffV) >> 4) | (1u << 16);
+        const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128;
+        int it = 0, units = 0, scores = 0, turns = 0;  // KV tiles, units begun, score tiles whose P has been waited for, turns taken
+        bool ok = true;
+        for (int i = item0; i < item1 && ok; ++i) {
+          const Unit u = read_unit(P, i);
+          const int nt = max(u.tiles[0], u.tiles[1]), tiles = u.tiles[s];
+          auto issue_s = [&](int j) {  // K of tile j has landed
+            const uint32_t k = k0 + (it + j) % kKvStages * (kKBytes >> 4);
 #pragma unroll
-          for (int x = 0; x < 12; ++x) {
-            mma_ss_lo(t_s, q + (x >> 2) * (kQSlab >> 4) + (x & 3) * 2, k + (x >> 2) * (kKSlab >> 4) + (x & 3) * 2, idesc_s,
-                      x ? 1u : 0u);
-            // (the other thread sees its turn about when the rest has been issued)
-            if (x == 8 && j > 0) mbar_arrive(here(misc->turn[1 - s]));
+            for (int x = 0; x < 12; ++x) {
+              mma_ss_lo(t_s, q + (x >> 2) * (kQSlab >> 4) + (x & 3) * 2, k + (x >> 2) * (kKSlab >> 4) + (x & 3) * 2, idesc_s,
+                        x ? 1u : 0u);
+              // (the other thread sees its turn about when the rest has been issued)
+              if (x == 8 && j > 0) mbar_arrive(here(misc->turn[1 - s]));
+            }
+            mma_commit_pair(here(misc->s_full[s]), 3);
+            if (j + 1 == tiles) mma_commit_pair(here(misc->q_empty[s]), 3);
+          };
+          auto k_landed = [&](int j) { return wait(misc->k_full[(it + j) % kKvStages], (it + j) / kKvStages); };
+          if (tiles > 0) {
+            ok = wait(misc->q_full[s], units) && k_landed(0);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(0);
           }
-          mma_commit_pair(here(misc->s_full[s]), 3);
-          if (j + 1 == tiles) mma_commit_pair(here(misc->q_empty[s]), 3);
-        };
-        auto k_landed = [&](int j) { return wait(misc->k_full[(it + j) % kKvStages], (it + j) / kKvStages); };
-        if (tiles > 0) {
-          ok = wait(misc->q_full[s], units) && k_landed(0);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(0);
-        }
-        for (int j = 0; j < nt; ++j) {
-          const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
-          if (j >= tiles) {  // the other sub-tile's alone
-            if (!(ok = wait(misc->turn[s], s == 0 ? turns - 1 : turns))) break;
+          for (int j = 0; j < nt; ++j) {
+            const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
+            if (j >= tiles) {  // the other sub-tile's alone
+              if (!(ok = wait(misc->turn[s], s == 0 ? turns - 1 : turns))) break;
+              ++turns;
+              mbar_arrive(here(misc->turn[1 - s]));
+              continue;
+            }
+            // Everything but P first: a thread that tests a barrier waits until the instructions that it has queued are
+            // dispatched, and a commit costs as much as one or two of them, so neither stands between P's arrival, PV and
+            // the next S (the softmax warps pass on the stages, which their own barriers say have been read).
+            ok = wait(misc->v_full[st], use);
+            if (ok && j + 1 < tiles) ok = k_landed(j + 1);
+            if (ok && j == 0 && units > 0) ok = wait(misc->o_free[s], units - 1);
+            if (ok) ok = wait(misc->p_full[2 * s], scores);
+            if (ok) ok = wait(misc->turn[s], s == 0 ? turns - 1 : turns);
+            if (!ok) break;
             ++turns;
-            mbar_arrive(here(misc->turn[1 - s]));
-            continue;
-          }
-          // Everything but P first: a thread that tests a barrier waits until the instructions that it has queued are
-          // dispatched, and a commit costs as much as one or two of them, so neither stands between P's arrival, PV and
-          // the next S (the softmax warps pass on the stages, which their own barriers say have been read).
-          ok = wait(misc->v_full[st], use);
-          if (ok && j + 1 < tiles) ok = k_landed(j + 1);
-          if (ok && j == 0 && units > 0) ok = wait(misc->o_free[s], units - 1);
-          if (ok) ok = wait(misc->p_full[2 * s], scores);
-          if (ok) ok = wait(misc->turn[s], s == 0 ? turns - 1 : turns);
-          if (!ok) break;
-          ++turns;
-          tc_fence_after();
-          const uint32_t v = v0 + st * (kVBytes >> 4);
+            tc_fence_after();
+            const uint32_t v = v0 + st * (kVBytes >> 4);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) mma_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), idesc_o, (j | x) ? 1u : 0u);
-          if (!(ok = wait(misc->p_full[2 * s + 1], scores))) break;
-          tc_fence_after();
+            for (int x = 0; x < 4; ++x) mma_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), idesc_o, (j | x) ? 1u : 0u);
+            if (!(ok = wait(misc->p_full[2 * s + 1], scores))) break;
+            tc_fence_after();
 #pragma unroll
-          for (int x = 4; x < 8; ++x) mma_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), idesc_o, 1u);
-          ++scores;
-          if (j + 1 < tiles) {
-            issue_s(j + 1);
-          } else {
-            mma_commit_pair(here(misc->o_full[s]), 3);
-            mbar_arrive(here(misc->turn[1 - s]));
+            for (int x = 4; x < 8; ++x) mma_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), idesc_o, 1u);
+            ++scores;
+            if (j + 1 < tiles) {
+              issue_s(j + 1);
+            } else {
+              mma_commit_pair(here(misc->o_full[s]), 3);
+              mbar_arrive(here(misc->turn[1 - s]));
+            }
           }
+          it += nt;
+          units += tiles > 0;
         }
-        it += nt;
-        units += tiles > 0;
-      }
-      mma_commit_pair(here(misc->last), 1);
-      mbar_wait_drain_cluster(here(misc->last), 0);
+        mma_commit_pair(here(misc->last), 1);
+        mbar_wait_drain_cluster(here(misc->last), 0);
       };
       if (warp == 1) issuer(std::integral_constant<int, 0>());
       else issuer(std::integral_constant<int, 1>());
