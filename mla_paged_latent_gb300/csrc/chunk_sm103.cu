@@ -100,23 +100,8 @@ struct ChunkMisc {
 constexpr size_t kChunkSmem = kOffChunkMisc + sizeof(ChunkMisc) + 1024;
 static_assert(kChunkSmem <= 232448, "shared memory budget of one CTA");
 
-// mma_bf16_pair and mma_bf16_pair_ts with the descriptors of shared memory given by their low words (the start address; an
-// offset within shared memory does not carry out of them): fewer instructions an MMA in the issuers.
-constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
-__device__ __forceinline__ void mma_ss_lo(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void mma_ts_lo(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
+// High word of every descriptor here: 1024 bytes between groups of eight rows, version 1, 128-byte swizzle.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 
 struct Unit {
   int q_start, q0, n, kv_start, len, head, tb, slot;
@@ -285,8 +270,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
             const uint32_t k = k0 + (it + j) % kKvStages * (kKBytes >> 4);
 #pragma unroll
             for (int x = 0; x < 12; ++x) {
-              mma_ss_lo(t_s, q + (x >> 2) * (kQSlab >> 4) + (x & 3) * 2, k + (x >> 2) * (kKSlab >> 4) + (x & 3) * 2, idesc_s,
-                        x ? 1u : 0u);
+              mma_bf16_pair_lo(t_s, q + (x >> 2) * (kQSlab >> 4) + (x & 3) * 2, kDescHi,
+                               k + (x >> 2) * (kKSlab >> 4) + (x & 3) * 2, kDescHi, idesc_s, x ? 1u : 0u);
               // (the other thread sees its turn about when the rest has been issued)
               if (x == 8 && j > 0) mbar_arrive(here(misc->turn[1 - s]));
             }
@@ -321,11 +306,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
             tc_fence_after();
             const uint32_t v = v0 + st * (kVBytes >> 4);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) mma_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), idesc_o, (j | x) ? 1u : 0u);
+            for (int x = 0; x < 4; ++x)
+              mma_bf16_pair_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), kDescHi, idesc_o, (j | x) ? 1u : 0u);
             if (!(ok = wait(misc->p_full[2 * s + 1], scores))) break;
             tc_fence_after();
 #pragma unroll
-            for (int x = 4; x < 8; ++x) mma_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), idesc_o, 1u);
+            for (int x = 4; x < 8; ++x)
+              mma_bf16_pair_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), kDescHi, idesc_o, 1u);
             ++scores;
             if (j + 1 < tiles) {
               issue_s(j + 1);

@@ -104,18 +104,6 @@ struct PairMisc {
 static_assert(Cfg<4>::kOffMisc + sizeof(PairMisc) + 1024 <= 232448, "shared memory budget of one CTA");
 static_assert(Cfg<3>::kOffMisc + sizeof(PairMisc) + 1024 <= 232448, "shared memory budget of one CTA");
 
-// mma_bf16_pair with the operands' descriptors given by their low words (the start address; an offset within shared
-// memory does not carry out of it): half the arithmetic of an MMA in the issuers, whose instructions wait their turn
-// among the other roles' (125 us against 128; PV held back behind the next tile's S instead: 132).
-__device__ __forceinline__ void mma_bf16_pair_lo(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
-                                                 uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
-      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // 16 bytes of global memory to shared memory, past the registers; zeros where `on` is false.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
