@@ -471,8 +471,9 @@ int mla_qkv_norm_rope_axes(const void* q_nope, int64_t q_nope_token_stride, int6
  * 2^18 a row and head once).
  *
  * A batch is a list of requests: request b has q_lens[b] new tokens and kv_lens[b] rows in the cache, those of the new tokens
- * last among them (they are appended before the call). Either may be 0. Its query i attends, causal, to rows
- * j <= kv_lens[b] - q_lens[b] + i, otherwise to all rows. A query that sees no row gives zeros and an lse of -infinity.
+ * last among them (they are appended before the call). Either may be 0 (a request without new tokens costs nothing: none of its
+ * rows is read). Its query i attends, causal, to rows j <= kv_lens[b] - q_lens[b] + i, otherwise to all rows. A query that sees
+ * no row gives zeros and an lse of -infinity.
  *
  * mla_chunk_plan (host): the schedule of a batch, for any number of calls (layers) with these lengths.
  *  q_lens, kv_lens host int32 [batch].
@@ -487,7 +488,7 @@ int mla_qkv_norm_rope_axes(const void* q_nope, int64_t q_nope_token_stride, int6
  */
 typedef struct {
   int32_t batch, heads, causal, tokens;   /* tokens: sum of q_lens */
-  int32_t kv_rows;                        /* rows of all requests, each rounded up to 128 */
+  int32_t kv_rows;                        /* rows of the requests with new tokens, each rounded up to 128 */
   int32_t group;                          /* heads expanded at once */
   int32_t pairs, items, merges, slots;
   int64_t sched_words;                    /* length of sched */

@@ -46,7 +46,7 @@ ChunkPlan make_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int bat
   std::vector<QueryTile> tiles;
   for (int b = 0; b < batch; ++b) {
     const int32_t n = q_lens[b], len = kv_lens[b];
-    const int32_t blocks = (len + 127) / 128;
+    const int32_t blocks = n > 0 ? static_cast<int32_t>((static_cast<int64_t>(len) + 127) / 128) : 0;
     for (int32_t k = 0; k < blocks; ++k) {
       const int32_t tile[4] = {b, 128 * k, len, 0};
       p.kv_tiles.insert(p.kv_tiles.end(), tile, tile + 4);

@@ -76,7 +76,7 @@ int mla_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
     if (q_lens[b] < 0 || kv_lens[b] < 0)
       return fail(MLA_ERR_INVALID_ARG, "mla_chunk_plan: lengths of request %d are %d and %d", b, q_lens[b], kv_lens[b]);
     tokens += q_lens[b];
-    rows += (static_cast<int64_t>(kv_lens[b]) + 127) / 128 * 128;
+    if (q_lens[b] > 0) rows += (static_cast<int64_t>(kv_lens[b]) + 127) / 128 * 128;
   }
   if (num_heads > 4096 || tokens * num_heads >= (1ll << 31) - 512 || rows >= (1ll << 31) - 512)
     return fail(MLA_ERR_UNSUPPORTED, "mla_chunk_plan: %lld tokens of %d heads over %lld rows are too many",
