@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import functools
+import operator
 import os
 import threading
 
@@ -431,6 +432,8 @@ def mla_qkv_norm_rope(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, kv
 def _axis_words(axis_of_pair):
     if len(axis_of_pair) != 32:
         raise ValueError(f"axis_of_pair must name the axis of 32 pairs, not of {len(axis_of_pair)}")
+    if not all(0 <= axis < 4 for axis in axis_of_pair):
+        raise ValueError(f"axis_of_pair must hold axes below 4, not {list(axis_of_pair)}")
     return (ctypes.c_int32 * 32)(*axis_of_pair)
 
 
@@ -464,7 +467,7 @@ def mla_qkv_norm_rope_axes(q_nope, q_pe, kv_raw, slots, positions, axis_of_pair,
         _require("kv_norm_weight", kv_norm_weight, bf16, 512)
         _require("freqs", freqs, f32, None, 64)
         _require("q_out", q_out, bf16, T, N, nope + 64)
-    words = _axis_words(tuple(axis_of_pair))
+    words = _axis_words(tuple(map(operator.index, axis_of_pair)))  # (whole numbers, whatever holds them)
     (qs, qh, q1), (ps, ph, p1), (rs, r1) = q_nope.stride(), q_pe.stride(), kv_raw.stride()
     if T > 0 and not (q1 == p1 == r1 == 1):
         raise ValueError("q_nope, q_pe and kv_raw must have their last elements adjacent")
@@ -498,8 +501,10 @@ def mla_chunk_plan(q_lens, kv_lens, num_heads: int, causal: bool = True, kv_budg
                    num_sms: int | None = None) -> ChunkPlan:
     """Host plan of a batch of chunks: request b has q_lens[b] new tokens, the last of its kv_lens[b] cached rows."""
     lib = load()
-    ql = np.ascontiguousarray(np.asarray(q_lens).astype(np.int32).ravel())
-    kl = np.ascontiguousarray(np.asarray(kv_lens).astype(np.int32).ravel())
+    q_lens, kv_lens = np.asarray(q_lens).ravel(), np.asarray(kv_lens).ravel()
+    ql, kl = np.ascontiguousarray(q_lens.astype(np.int32)), np.ascontiguousarray(kv_lens.astype(np.int32))
+    if not (np.array_equal(ql, q_lens) and np.array_equal(kl, kv_lens)):
+        raise ValueError("q_lens and kv_lens must be whole numbers of 32 bits")
     if ql.shape != kl.shape:
         raise ValueError(f"q_lens and kv_lens must have one entry a request, not {ql.shape[0]} and {kl.shape[0]}")
     if kv_budget < 0:

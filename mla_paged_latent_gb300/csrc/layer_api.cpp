@@ -267,7 +267,7 @@ int mla_linear(const void* x, int64_t x_stride, const void* weight, const void* 
   if (!residual) residual_stride = outer;
   const int64_t strides[3] = {x_stride, residual_stride, out_stride}, widths[3] = {inner, outer, outer};
   for (int i = 0; i < 3; ++i)
-    if (strides[i] < widths[i] || strides[i] % 8 != 0 || strides[i] >= (1ll << 36))
+    if (strides[i] < widths[i] || strides[i] % 8 != 0 || strides[i] > (1ll << 46) / rows)  // (past any memory)
       return fail(MLA_ERR_INVALID_ARG, "mla_linear: row stride %lld must be a multiple of 8 elements, at least %lld",
                   static_cast<long long>(strides[i]), static_cast<long long>(widths[i]));
   if (!aligned_to(x, 16) || !aligned_to(weight, 16) || !aligned_to(bias, 16) || !aligned_to(residual, 16) || !aligned_to(out, 16) ||

@@ -103,6 +103,9 @@ def test_plan_refuses(lib):
         mla.mla_chunk_plan([1, 2], [3], 4, num_sms=152)
     with pytest.raises(ValueError):
         mla.mla_chunk_plan([1], [3], 4, kv_budget=-1, num_sms=152)
+    for q, kv in (([2 ** 32 + 1], [2 ** 32 + 3]), ([1.5], [3]), ([1], [2.5])):
+        with pytest.raises(ValueError, match="whole numbers"):
+            mla.mla_chunk_plan(q, kv, 4, num_sms=152)
     info = mla._ChunkInfo()
     one = np.array([700], np.int32)
     buf = np.zeros(8, np.int32)
@@ -173,7 +176,7 @@ def test_linear_refuses(lib):
     assert linear_rc(lib, act=3) == -1 and linear_rc(lib, act=-1) == -1
     for name, wide in (("xs", 64), ("rs", 128), ("os", 128)):
         assert linear_rc(lib, **{name: wide - 8}) == -1 and linear_rc(lib, **{name: wide + 4}) == -1, name
-        assert linear_rc(lib, **{name: -wide}) == -1
+        assert linear_rc(lib, **{name: -wide}) == -1 and linear_rc(lib, rows=1 << 30, **{name: 1 << 35}) == -1
     for name in ("x", "w", "bias"):
         assert linear_rc(lib, out=linear_at[name]) == -1, name
     assert linear_rc(lib, out=at(4), os=136) == -1                       # the residual's memory, but not element for element
@@ -290,9 +293,43 @@ def test_the_binding_names_what_is_wrong(lib, monkeypatch):
                 freqs=torch.zeros(9, 64), out=bf(3, 2, 192), kv=torch.zeros(2, 8 * 1152, dtype=torch.uint8))
     for name, bad, what in (("qn", bf(3, 2, 100), "q_nope"), ("qp", bf(3, 2, 32), "q_pe"), ("raw", bf(3, 512), "kv_raw"),
                             ("slots", i32(4), "slots"), ("pos", i32(3), "positions"), ("pos", i32(3, 4), "positions"),
-                            ("pos", i32(3, 3).long(), "positions"), ("axes", [0] * 31, "32 pairs"), ("kw", bf(256), "kv_norm_weight"),
-                            ("freqs", torch.zeros(9, 32), "freqs"), ("out", bf(3, 2, 576), "q_out")):
+                            ("pos", i32(3, 3).long(), "positions"), ("axes", [0] * 31, "32 pairs"),
+                            ("axes", [2 ** 32] + [0] * 31, "axes below 4"), ("kw", bf(256), "kv_norm_weight"), ("freqs", torch.zeros(9, 32), "freqs"),
+                            ("out", bf(3, 2, 576), "q_out")):
         a = dict(good, **{name: bad})
         with pytest.raises(ValueError, match=what):
             mla.mla_qkv_norm_rope_axes(a["qn"], a["qp"], a["raw"], a["slots"], a["pos"], a["axes"], a["kw"], 1e-6, a["freqs"],
                                        a["out"], a["kv"], 0, 8)
+
+
+def test_axes_that_change_are_read_again(monkeypatch):
+    """One entry changed in place between two calls; and what is no whole number."""
+    monkeypatch.setattr(mla, "_require_one_device", lambda *t: None)
+    seen = []
+
+    class Lib:
+        def mla_qkv_norm_rope_axes(self, *args):
+            seen.append(list(args[15]))
+            return 0
+
+        def mla_page_bytes(self, layout, page, out):
+            out._obj.value = 8 * 1152
+            return 0
+
+    monkeypatch.setattr(mla, "load", lambda path=None: Lib())
+    monkeypatch.setattr(mla, "_stream", lambda s: None)
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    call = lambda axes: mla.mla_qkv_norm_rope_axes(  # noqa: E731
+        bf(3, 2, 128), bf(3, 2, 64), bf(3, 576), i32(3), i32(3, 3), axes, bf(512), 1e-6, torch.zeros(9, 64), bf(3, 2, 192),
+        torch.zeros(2, 8 * 1152, dtype=torch.uint8), 0, 8)
+    axes = list(torch.arange(32) % 3)
+    call(axes)
+    axes[5].fill_(0)
+    call(axes)
+    want = [i % 3 for i in range(32)]
+    assert seen[0] == want and seen[1] == want[:5] + [0] + want[6:]
+    call(np.arange(32) % 3)
+    assert seen[2] == want
+    with pytest.raises(TypeError):
+        call([0.0] * 32)
