@@ -294,8 +294,8 @@ def test_the_binding_names_what_is_wrong(lib, monkeypatch):
     for name, bad, what in (("qn", bf(3, 2, 100), "q_nope"), ("qp", bf(3, 2, 32), "q_pe"), ("raw", bf(3, 512), "kv_raw"),
                             ("slots", i32(4), "slots"), ("pos", i32(3), "positions"), ("pos", i32(3, 4), "positions"),
                             ("pos", i32(3, 3).long(), "positions"), ("axes", [0] * 31, "32 pairs"),
-                            ("axes", [2 ** 32] + [0] * 31, "axes below 4"), ("kw", bf(256), "kv_norm_weight"), ("freqs", torch.zeros(9, 32), "freqs"),
-                            ("out", bf(3, 2, 576), "q_out")):
+                            ("axes", [2 ** 32] + [0] * 31, "axes below 4"), ("kw", bf(256), "kv_norm_weight"),
+                            ("freqs", torch.zeros(9, 32), "freqs"), ("out", bf(3, 2, 576), "q_out")):
         a = dict(good, **{name: bad})
         with pytest.raises(ValueError, match=what):
             mla.mla_qkv_norm_rope_axes(a["qn"], a["qp"], a["raw"], a["slots"], a["pos"], a["axes"], a["kw"], 1e-6, a["freqs"],
