@@ -467,6 +467,12 @@ __global__ void __launch_bounds__(kNarrowThreads)
     tc_fence_before();
   }
   __syncthreads();
+  // TMEM goes before the peers are waited for: where this SM's or a peer's holds blocks of another kernel that want TMEM too,
+  // nobody waits for columns of a CTA that itself waits for one without
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
   cluster_sync_all();
   // Rank r sums and writes every PARTS-th row: a warp a row, four features a lane; its loads from the peers (and of the
   // residual) are in flight together.
@@ -538,7 +544,6 @@ __global__ void __launch_bounds__(kNarrowThreads)
     }
   }
   cluster_sync_all();  // no CTA leaves while a peer reads its sums
-  if (warp == 1) tmem_dealloc(tmem, kCols);
 }
 
 template <int NT, int PARTS>
