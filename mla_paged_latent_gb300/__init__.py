@@ -13,7 +13,6 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import functools
-import operator
 import os
 import threading
 
@@ -429,12 +428,10 @@ def mla_qkv_norm_rope(q_nope, q_pe, kv_raw, slots, positions, kv_norm_weight, kv
 
 
 @functools.lru_cache(maxsize=64)
-def _axis_words(axis_of_pair):
-    if len(axis_of_pair) != 32:
-        raise ValueError(f"axis_of_pair must name the axis of 32 pairs, not of {len(axis_of_pair)}")
-    if not all(0 <= axis < 4 for axis in axis_of_pair):
-        raise ValueError(f"axis_of_pair must hold axes below 4, not {list(axis_of_pair)}")
-    return (ctypes.c_int32 * 32)(*axis_of_pair)
+def _axis_words(axes: bytes):
+    if len(axes) != 32:
+        raise ValueError(f"axis_of_pair must name the axis of 32 pairs, not of {len(axes)}")
+    return (ctypes.c_int32 * 32)(*axes)
 
 
 def mla_qkv_norm_rope_axes(q_nope, q_pe, kv_raw, slots, positions, axis_of_pair, kv_norm_weight, kv_eps: float, freqs, q_out,
@@ -467,7 +464,11 @@ def mla_qkv_norm_rope_axes(q_nope, q_pe, kv_raw, slots, positions, axis_of_pair,
         _require("kv_norm_weight", kv_norm_weight, bf16, 512)
         _require("freqs", freqs, f32, None, 64)
         _require("q_out", q_out, bf16, T, N, nope + 64)
-    words = _axis_words(tuple(map(operator.index, axis_of_pair)))  # (whole numbers, whatever holds them)
+    try:
+        axes = bytes(tuple(axis_of_pair))  # whole numbers, whatever holds them (a microsecond less than one by one)
+    except ValueError:
+        raise ValueError(f"axis_of_pair must hold axes below 4, not {list(axis_of_pair)}") from None
+    words = _axis_words(axes)
     (qs, qh, q1), (ps, ph, p1), (rs, r1) = q_nope.stride(), q_pe.stride(), kv_raw.stride()
     if T > 0 and not (q1 == p1 == r1 == 1):
         raise ValueError("q_nope, q_pe and kv_raw must have their last elements adjacent")
