@@ -49,7 +49,8 @@ __device__ __forceinline__ uint32_t rotate2(uint32_t two, float2 cs) {
 // The first blocks take the KV rows, one warp each, with the arithmetic of the other fused writes. The others take the
 // queries: a warp has four heads of a token (192-wide rows) or one (the others). Bound by the bytes and, for those, by the
 // loads in flight: full occupancy, and a warp asks for its rows before it looks at the positions.
-template <int WIDTH>
+// NOPE: the queries' NoPE part is read and written, for it is not q_out's own or is normalised.
+template <int WIDTH, bool NOPE>
 __global__ void __launch_bounds__(kAxesWarps * 32, 8) axes_kernel(const __grid_constant__ AxesParams A) {
   pdl_trigger();
   pdl_wait();
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kAxesWarps * 32, 8) axes_kernel(const __grid_c
     // 4 x 16 chunks of 16 bytes of the NoPE parts, two a lane, and 4 x 8 of the RoPE parts
     const int left = P.heads - n0, h = lane >> 4, hp = lane >> 3, c = lane & 7;
     uint4 u0, u1, up;
-    if (A.copy_nope) {
+    if (NOPE) {
       if (h < left) u0 = reinterpret_cast<const uint4*>(qn + h * P.nope_head_stride)[lane & 15];
       if (h + 2 < left) u1 = reinterpret_cast<const uint4*>(qn + (h + 2) * P.nope_head_stride)[lane & 15];
     }
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kAxesWarps * 32, 8) axes_kernel(const __grid_c
     float2 cs[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) cs[k] = angle_at(P.freqs, __shfl_sync(0xffffffffu, at.pos, 4 * c + k), 4 * c + k);
-    if (A.copy_nope) {
+    if (NOPE) {
       if (h < left) reinterpret_cast<uint4*>(q + h * WIDTH)[lane & 15] = u0;
       if (h + 2 < left) reinterpret_cast<uint4*>(q + (h + 2) * WIDTH)[lane & 15] = u1;
     }
@@ -121,21 +122,18 @@ __global__ void __launch_bounds__(kAxesWarps * 32, 8) axes_kernel(const __grid_c
   // 64 chunks of 16 bytes, two a lane, normalised over their 512 elements where asked; the 576-wide rows' RoPE part is
   // a pair a lane, that of the 512-wide rows the last eight chunks
   const bool pe_lane = WIDTH == 512 && lane >= 24;
-  const bool nope = WIDTH == 512 || A.copy_nope;
-  uint4 u0, u1;
+  uint4 u0, u1 = make_uint4(0, 0, 0, 0);
   uint32_t two = 0;
-  if (nope) {
-    u0 = *reinterpret_cast<const uint4*>(qn + 8 * lane);
-    u1 = *reinterpret_cast<const uint4*>(pe_lane ? qp + 8 * (lane - 24) : qn + 256 + 8 * lane);
-  }
+  if (NOPE) u0 = *reinterpret_cast<const uint4*>(qn + 8 * lane);
+  if (NOPE || pe_lane) u1 = *reinterpret_cast<const uint4*>(pe_lane ? qp + 8 * (lane - 24) : qn + 256 + 8 * lane);
   if (WIDTH == 576) two = reinterpret_cast<const uint32_t*>(qp)[lane];
   const Places at(A, t, lane);
   if (!at.ok) return report(at);
-  if (nope) {
-    if (WIDTH == 512 || P.q_norm) {  // (a bf16 value goes through fp32 unchanged)
+  if (WIDTH == 512 || NOPE) {
+    if (WIDTH == 512 || P.q_norm) {  // (a bf16 number goes through fp32 unchanged)
       float rinv = 1.f;
       float a[8];
-      if (P.q_norm) {
+      if (NOPE && P.q_norm) {
         float ss = 0.f, b[8];
         unpack8(u0, a);
         unpack8(u1, b);
@@ -157,7 +155,7 @@ __global__ void __launch_bounds__(kAxesWarps * 32, 8) axes_kernel(const __grid_c
           for (int k = 0; k < 8; ++k) a[k] *= g[k];
         }
       };
-      if (P.q_norm) {
+      if (NOPE && P.q_norm) {
         scaled(u0, lane);
         u0 = pack8(a);
         scaled(u1, 32 + lane);
@@ -179,8 +177,8 @@ __global__ void __launch_bounds__(kAxesWarps * 32, 8) axes_kernel(const __grid_c
       }
       u1 = pack8(a);
     }
-    reinterpret_cast<uint4*>(q)[lane] = u0;
-    reinterpret_cast<uint4*>(q)[32 + lane] = u1;
+    if (NOPE) reinterpret_cast<uint4*>(q)[lane] = u0;
+    if (NOPE || pe_lane) reinterpret_cast<uint4*>(q)[32 + lane] = u1;
   }
   if (WIDTH == 576) reinterpret_cast<uint32_t*>(q + 512)[lane] = rotate2(two, angle_at(P.freqs, at.pos, lane));
 }
@@ -193,9 +191,10 @@ cudaError_t launch_qkv_norm_rope_axes(const AxesParams& p, cudaStream_t stream) 
   const int per = p.q_width == 192 ? 4 : 1;
   const int64_t warps = static_cast<int64_t>(p.qkv.tokens) * ((p.qkv.heads + per - 1) / per);
   const dim3 grid(static_cast<unsigned>(a.qkv.kv_blocks + (warps + kAxesWarps - 1) / kAxesWarps)), block(kAxesWarps * 32);
-  if (p.q_width == 192) return launch_pdl(axes_kernel<192>, grid, block, 0, stream, a);
-  if (p.q_width == 576) return launch_pdl(axes_kernel<576>, grid, block, 0, stream, a);
-  return launch_pdl(axes_kernel<512>, grid, block, 0, stream, a);
+  auto go = [&](auto kern) { return launch_pdl(kern, grid, block, 0, stream, a); };
+  if (p.q_width == 192) return go(p.copy_nope ? axes_kernel<192, true> : axes_kernel<192, false>);
+  if (p.q_width == 576) return go(p.copy_nope ? axes_kernel<576, true> : axes_kernel<576, false>);
+  return go(p.copy_nope ? axes_kernel<512, true> : axes_kernel<512, false>);
 }
 
 }  // namespace mla
