@@ -511,10 +511,11 @@ int mla_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
  *              at a time may use it.
  *  out         device bf16 [tokens, num_heads, 128], 32-byte aligned. lse device float [tokens, num_heads] or NULL: natural
  *              log of the sum of e^score.
- * K is rounded to bf16; V and the softmax weights to fp16, V times a power of two of its 32 rows and head, so that a value
- * keeps 11 bits down to 2^-28 of the largest of them (operands of the tensor cores); sums, maxima and the accumulator are fp32.
- * A score, and so lse, is off by up to 2^-8 of the sum of its terms' magnitudes for K's rounding. |V| must stay below 2^74:
- * larger values become infinite; below 2^-74 they lose bits. A NaN or infinity in a row makes NaN of query rows of the
+ * K is rounded to bf16. V and the softmax weights are rounded, by 32 rows of a request and head: to fp16 where the largest of their
+ * values is zero or in [2^-8, 2^7) (a value is then off by 2^-11 of itself or 2^-33 at most, a weight by 2^-11 of itself or 2^-32 of
+ * the query's largest), to bf16 otherwise (2^-8 of itself), whatever the size of other rows' values. Sums, maxima and the
+ * accumulator are fp32. A score, and so lse, is off by up to 2^-8 of the sum of its terms' magnitudes for K's rounding. |V| must stay
+ * below 2^80: larger values may become infinite. A NaN or infinity in a row makes NaN of query rows of the
  * request that do not see it too, if they are computed with its tile of 128 rows.
  */
 int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layout, int64_t num_pages, int32_t page_size,

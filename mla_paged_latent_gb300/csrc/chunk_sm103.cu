@@ -7,7 +7,7 @@
 // (row, head) once. Three steps on one stream, and a fourth where the rows are few:
 //   chunk_rows_kernel  the requests' rows, in order, as bf16 [rows, 576]; each request starts at a multiple of 128 and the
 //                      rows up to the next are zeros, so that a masked row is never what memory happened to hold;
-//   the product of the latent part with W (gemm_pair_kernel), K (bf16) and V (fp16) of a group of heads [rows, heads, 256]
+//   the product of the latent part with W (gemm_pair_kernel), K (bf16) and V (fp16 or bf16) of a group of heads [rows, heads, 256]
 //                      (operands of the tensor cores; the sums are fp32), which attention then reads many times;
 //   chunk_attention_kernel;
 //   chunk_merge_kernel where a query tile was split over the rows.
@@ -33,6 +33,8 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
   pdl_wait();
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i * P.group_heads < P.heads; i += 256) P.any_wide[i] = 0;
   if (row >= P.kv_rows) return;
   const int4 tile = reinterpret_cast<const int4*>(P.kv_tiles)[row >> 7];  // request, position of the first row, kv_len
   const int req = tile.x, pos = tile.y + (row & 127);
@@ -69,9 +71,11 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
 // Bound by the tensor cores in the end: 2 x 1280 cycles of products a KV tile and unit, 3090 traced. One issuing thread took
 // 4790 (its barrier tests and commits stood between the products), two that run freely 5040 (both softmaxes at once); turns
 // 3730, stages passed on by the softmax warps 3560, P in halves and nothing spilled 3090.
-// P and V are fp16, operands of the tensor cores: V comes scaled by a power of two for every 32 rows, which P makes good, and P
-// is kept below 2^15 by a reference that moves (and O is rescaled) only when a tile exceeds it by 2^8. Both in bf16 are off by
-// 0.0027 of the result against 0.0020 (in the mean square; the result's own rounding is 0.0017). Maxima, sums and O are fp32.
+// P and V are fp16 where the values of 32 rows are of a size that fp16 holds well, and bf16 where they are not (an instruction has
+// 16 rows, so its type may differ from the next one's): a scale of V for every 32 rows, which P makes good, would cost the weights of
+// rows whose values are smaller by far their bits. P is kept below 2^15 by a reference that moves (and O is rescaled) only
+// when a tile exceeds it by 2^8. Both in bf16 are off by 0.0027 of the result against 0.0020 (in the mean square; the result's own
+// rounding is 0.0017). Maxima, sums and O are fp32.
 // Shared memory per CTA: Q 2 x 48 KB, and 3 stages of K (64 rows x 192) and V (128 rows x 64 dims), 40 KB each.
 //   warp 0      TMA            warps 1, 2  MMA issue of sub-tile 0 and 1 (even CTA); warp 1 TMEM
 //   warps 4-7   softmax and epilogue of sub-tile 0, warps 8-11 of sub-tile 1: a query row a thread
@@ -136,6 +140,346 @@ __device__ __forceinline__ Unit read_unit(const ChunkParams& P, int item) {
   return u;
 }
 
+// Of each KV tile of a unit: four bytes, one for 32 rows, 1 where their values (and so their weights) are bf16.
+__device__ __forceinline__ const uint32_t* wide_groups(const ChunkParams& P, const Unit& u) {
+  return reinterpret_cast<const uint32_t*>(P.value_wide) + static_cast<int64_t>(u.head) * (P.kv_rows >> 7) + (u.kv_start >> 7) + u.tb;
+}
+
+// What the warps share.
+struct ChunkCta {
+  const ChunkParams& P;
+  ChunkMisc* misc;
+  uint32_t sb, tmem;   // shared memory, TMEM
+  int item0, item1;    // this pair's units
+  __device__ __forceinline__ uint32_t here(uint64_t& b) const { return smem_addr(&b); }
+  __device__ __forceinline__ uint32_t lead(uint64_t& b) const { return map_shared_rank(smem_addr(&b), 0); }
+  __device__ __forceinline__ bool wait(uint64_t& b, uint32_t parity) const {
+    return wait_bar(smem_addr(&b), parity & 1, &misc->abort, P.status);
+  }
+};
+
+// Warp 0, one thread: copies of Q, K and V.
+__device__ __forceinline__ void chunk_load(const ChunkCta& C, const CUtensorMap& q_map, const CUtensorMap& kv_map,
+                                           const CUtensorMap& rope_map) {
+  const ChunkParams& P = C.P;
+  ChunkMisc* misc = C.misc;
+  const int rank = static_cast<int>(cluster_ctarank());
+  int it = 0;            // KV tiles loaded
+  int qn[2] = {0, 0};    // query sub-tiles loaded
+  bool ok = true;
+  for (int i = C.item0; i < C.item1 && ok; ++i) {
+    const Unit u = read_unit(P, i);
+    const int head = P.head0 + u.head;
+    const int nt = max(u.tiles[0], u.tiles[1]);
+    auto load_q = [&](int s) {
+      if (u.tiles[s] == 0) return true;
+      if (qn[s] > 0 && !C.wait(misc->q_empty[s], qn[s] - 1)) return false;
+      const uint32_t full = C.lead(misc->q_full[s]);
+      mbar_arrive_expect_tx_cluster(full, kQSub);
+      for (int k = 0; k < 3; ++k)
+        tma_load_3d_pair(C.sb + s * kQSub + k * kQSlab, &q_map, 64 * k, head, u.q_start + u.q0 + 256 * s + 128 * rank,
+                         full);
+      ++qn[s];
+      return true;
+    };
+    auto load_k = [&](int j) {
+      const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
+      if (use > 0 && !C.wait(misc->k_empty[st], use - 1)) return false;
+      const uint32_t full = C.lead(misc->k_full[st]), at = C.sb + kOffK + st * kKBytes;
+      const int row = u.kv_start + (u.tb + j) * 128 + 64 * rank;
+      mbar_arrive_expect_tx_cluster(full, kKBytes);
+      tma_load_2d_pair(at, &kv_map, u.head * 256, row, full);
+      tma_load_2d_pair(at + kKSlab, &kv_map, u.head * 256 + 64, row, full);
+      tma_load_2d_pair(at + 2 * kKSlab, &rope_map, 512, row, full);
+      return true;
+    };
+    auto load_v = [&](int j) {
+      const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
+      if (use > 0 && !C.wait(misc->v_empty[st], use - 1)) return false;
+      const uint32_t full = C.lead(misc->v_full[st]), at = C.sb + kOffV + st * kVBytes;
+      const int row = u.kv_start + (u.tb + j) * 128, dim = u.head * 256 + 128 + 64 * rank;
+      mbar_arrive_expect_tx_cluster(full, kVBytes);
+      tma_load_2d_pair(at, &kv_map, dim, row, full);
+      tma_load_2d_pair(at + kVBytes / 2, &kv_map, dim, row + 64, full);
+      return true;
+    };
+    ok = load_q(0);
+    for (int j = 0; j < nt && ok; ++j) {
+      ok = load_k(j);
+      if (j == 0 && ok) ok = load_q(1);
+      if (ok) ok = load_v(j);
+    }
+    it += nt;
+  }
+  if (*static_cast<volatile int*>(&misc->abort) != 0 && rank == 0) {
+    // copies still in flight land on this CTA's barriers: wait for them (bounded)
+    for (int s = 0; s < 2; ++s)
+      if (qn[s] > 0) mbar_wait_drain_cluster(C.here(misc->q_full[s]), (qn[s] - 1) & 1);
+    for (int st = 0; st < kKvStages; ++st) {
+      mbar_wait_drain_cluster(C.here(misc->k_full[st]), 0);
+      mbar_wait_drain_cluster(C.here(misc->k_full[st]), 1);
+      mbar_wait_drain_cluster(C.here(misc->v_full[st]), 0);
+      mbar_wait_drain_cluster(C.here(misc->v_full[st]), 1);
+    }
+  }
+}
+
+// MIXED: values of some heads and rows are bf16, and so are their weights. Where none are, the types are constants: chosen at every
+// instruction and conversion they cost a whole prompt's attention 4 % (1627 us against 1690), a lone sub-tile 1 %; chosen by a
+// branch a tile still more.
+//
+// One thread a sub-tile s of the even CTA: the products.
+// The two threads take turns, a tile each: sub-tiles that begin a tile at once would also need their P at once, and the
+// tensor cores would wait for both softmaxes.
+template <int s, bool MIXED>
+__device__ __forceinline__ void chunk_issue(const ChunkCta& C) {
+  const ChunkParams& P = C.P;
+  ChunkMisc* misc = C.misc;
+  constexpr uint32_t idesc_s = idesc_bf16_f32(256, 128, 0, 0);
+  constexpr uint32_t idesc_o = idesc_f16_f32(256, 128, 0, 1);  // V: MN-major, 64 dims of each CTA
+  constexpr uint32_t idesc_wide = idesc_bf16_f32(256, 128, 0, 1);
+  // low words of the descriptors: start address, and a leading offset that neither layout uses
+  const uint32_t q = ((C.sb + s * kQSub) >> 4) | (1u << 16), k0 = ((C.sb + kOffK) >> 4) | (1u << 16),
+                 v0 = ((C.sb + kOffV) >> 4) | (1u << 16);
+  const uint32_t t_s = C.tmem + s * 128, t_o = C.tmem + 256 + s * 128;
+  int it = 0, units = 0, scores = 0, turns = 0;  // KV tiles, units begun, score tiles whose P has been waited for, turns taken
+  bool ok = true;
+  for (int i = C.item0; i < C.item1 && ok; ++i) {
+    const Unit u = read_unit(P, i);
+    const int nt = max(u.tiles[0], u.tiles[1]), tiles = u.tiles[s];
+    auto issue_s = [&](int j) {  // K of tile j has landed
+      const uint32_t k = k0 + (it + j) % kKvStages * (kKBytes >> 4);
+#pragma unroll
+      for (int x = 0; x < 12; ++x) {
+        mma_bf16_pair_lo(t_s, q + (x >> 2) * (kQSlab >> 4) + (x & 3) * 2, kDescHi,
+                         k + (x >> 2) * (kKSlab >> 4) + (x & 3) * 2, kDescHi, idesc_s, x ? 1u : 0u);
+        // (the other thread sees its turn about when the rest has been issued)
+        if (x == 8 && j > 0) mbar_arrive(C.here(misc->turn[1 - s]));
+      }
+      mma_commit_pair(C.here(misc->s_full[s]), 3);
+      if (j + 1 == tiles) mma_commit_pair(C.here(misc->q_empty[s]), 3);
+    };
+    auto k_landed = [&](int j) { return C.wait(misc->k_full[(it + j) % kKvStages], (it + j) / kKvStages); };
+    const uint32_t* wides = wide_groups(P, u);
+    uint32_t wide_next = 0;
+    if (tiles > 0) {
+      if (MIXED) wide_next = wides[0];
+      ok = C.wait(misc->q_full[s], units) && k_landed(0);
+      if (!ok) break;
+      tc_fence_after();
+      issue_s(0);
+    }
+    for (int j = 0; j < nt; ++j) {
+      const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
+      if (j >= tiles) {  // the other sub-tile's alone
+        if (!(ok = C.wait(misc->turn[s], s == 0 ? turns - 1 : turns))) break;
+        ++turns;
+        mbar_arrive(C.here(misc->turn[1 - s]));
+        continue;
+      }
+      // Everything but P first: a thread that tests a barrier waits until the instructions that it has queued are
+      // dispatched, and a commit costs as much as one or two of them, so neither stands between P's arrival, PV and
+      // the next S (the softmax warps pass on the stages, which their own barriers say have been read).
+      ok = C.wait(misc->v_full[st], use);
+      if (ok && j + 1 < tiles) ok = k_landed(j + 1);
+      if (ok && j == 0 && units > 0) ok = C.wait(misc->o_free[s], units - 1);
+      uint32_t idesc[4];  // of 32 rows each
+#pragma unroll
+      for (int g = 0; g < 4; ++g) idesc[g] = MIXED && (wide_next >> (8 * g) & 1) ? idesc_wide : idesc_o;
+      if (ok) ok = C.wait(misc->p_full[2 * s], scores);
+      if (ok) ok = C.wait(misc->turn[s], s == 0 ? turns - 1 : turns);
+      if (!ok) break;
+      ++turns;
+      tc_fence_after();
+      const uint32_t v = v0 + st * (kVBytes >> 4);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        mma_bf16_pair_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), kDescHi, idesc[x >> 1], (j | x) ? 1u : 0u);
+      if (!(ok = C.wait(misc->p_full[2 * s + 1], scores))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int x = 4; x < 8; ++x)
+        mma_bf16_pair_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), kDescHi, idesc[x >> 1], 1u);
+      if (MIXED && j + 1 < tiles) wide_next = wides[j + 1];
+      ++scores;
+      if (j + 1 < tiles) {
+        issue_s(j + 1);
+      } else {
+        mma_commit_pair(C.here(misc->o_full[s]), 3);
+        mbar_arrive(C.here(misc->turn[1 - s]));
+      }
+    }
+    it += nt;
+    units += tiles > 0;
+  }
+  mma_commit_pair(C.here(misc->last), 1);
+  mbar_wait_drain_cluster(C.here(misc->last), 0);
+}
+
+// Warps 4 to 11: softmax and epilogue, a query row a thread.
+template <bool MIXED>
+__device__ __forceinline__ void chunk_softmax(const ChunkCta& C) {
+  const ChunkParams& P = C.P;
+  ChunkMisc* misc = C.misc;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int s = (warp - 4) >> 2, quarter = warp & 3;
+  const int mine = 256 * s + 128 * rank + 32 * quarter + lane;  // row of the unit
+  const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t t_s = C.tmem + lane_off + s * 128, t_o = C.tmem + lane_off + 256 + s * 128;
+  const uint32_t p_bar[2] = {C.lead(misc->p_full[2 * s]), C.lead(misc->p_full[2 * s + 1])};
+  int scores = 0, units = 0, it = 0;
+  bool ok = true;
+  for (int i = C.item0; i < C.item1 && ok; ++i) {
+    const Unit u = read_unit(P, i);
+    if (u.head >= P.group_heads) continue;
+    const int tiles = u.tiles[s], others = u.tiles[1 - s];
+    const int lim = row_limit(P.causal, u.len, u.n, u.q0 + mine) - u.tb * 128;  // rows that this query sees, from tb on
+    // The stage of K or V of tile j has been read by this sub-tile's products, and by the other's if it has none there:
+    // each of two arrivals says so for one of them.
+    auto pass_on = [&](uint64_t (&empty)[kKvStages], int j) {
+      if (quarter == 0 && lane == 0) {
+        const uint32_t b = C.here(empty[(it + j) % kKvStages]);
+        mbar_arrive(b);
+        if (j >= others) mbar_arrive(b);
+      }
+      __syncwarp();
+    };
+    // Weights are 2^(score - ref) with ref such that they stay below 2^15.
+    float ref = -INFINITY, l_run = 0.f;
+    const uint32_t* wides = wide_groups(P, u);
+    uint32_t wide_next = 0;
+    if (MIXED && tiles > 0) wide_next = wides[0];
+    for (int j = 0; j < tiles; ++j) {
+      const uint32_t wide = wide_next;
+      if (!C.wait(misc->s_full[s], scores)) {
+        ok = false;
+        break;
+      }
+      ++scores;
+      tc_fence_after();
+      uint32_t x[128];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tmem_ld32(t_s + 32 * k, x + 32 * k);
+      tmem_wait_ld();
+      if (MIXED && j + 1 < tiles) wide_next = wides[j + 1];  // (not before: the wait would be for this load too)
+      const int nv = lim - j * 128;  // columns that this row sees
+      if (__any_sync(0xffffffffu, nv < 128)) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k >= nv) x[k] = 0xFF800000u;
+      }
+      float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < 64; ++k)
+        tops[k & 3] = max3(tops[k & 3], __uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+      const float top = P.scale_log2 * fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]);
+      const bool raise = top > ref + kWeightMaxLog2;
+      if (__any_sync(0xffffffffu, raise)) {
+        const float a = raise ? fast_exp2(ref - (top - kWeightLog2)) : 1.f;  // (0 for the first rows that a query sees)
+        l_run *= a;
+        if (raise) ref = top - kWeightLog2;
+        if (j > 0) {
+#pragma unroll 1
+          for (int k = 0; k < 8; ++k) {  // (16 columns: the scores fill the registers)
+            uint32_t o[16];
+            tmem_ld16(t_o + 16 * k, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * a);
+            tmem_st16(t_o + 16 * k, o);
+          }
+        }
+      }
+      const float ref_use = ref == -INFINITY ? 0.f : ref;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int gg = 0; gg < 2; ++gg) {
+          const int g = 2 * h + gg;
+          uint32_t p[16];
+          const float2 off2 = make_float2(-ref_use, -ref_use);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float2 v = fma2(make_float2(__uint_as_float(x[32 * g + 2 * k]), __uint_as_float(x[32 * g + 2 * k + 1])),
+                                  P.scale_log2, off2);
+            const float2 w = make_float2(fast_exp2(v.x), fast_exp2(v.y));
+            sum[k & 1] = add2(sum[k & 1], w);
+            p[k] = MIXED && (wide >> (8 * g) & 1) ? f32x2_to_bf16x2(w.x, w.y) : f32x2_to_f16x2(w.x, w.y);
+          }
+          const float2 t = add2(sum[0], sum[1]);
+          l_run += t.x + t.y;
+          tmem_st16(t_s + 16 * g, p);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(p_bar[h]);
+        __syncwarp();
+      }
+      pass_on(misc->k_empty, j);  // (only now: P is waited for, the stages have two tiles' time)
+      if (j > 0) pass_on(misc->v_empty, j - 1);
+    }
+    if (!ok) break;
+    // Out, 32 bytes a store. A row that sees nothing is zeros with an lse of -infinity; a NaN sum stays NaN.
+    const bool empty = l_run == 0.f;
+    const float inv = empty ? 0.f : 1.0f / (l_run * (1 << kValueLog2));
+    const float lse = empty ? -INFINITY : (ref + log2f(l_run)) * 0.6931471805599453f;
+    const Unit w = read_unit(P, i);  // (again: no register holds it while the scores fill them)
+    const int row = w.q0 + mine;
+    const bool live = row < w.n && w.q_start + row < P.tokens;  // (whatever a schedule says)
+    if (tiles > 0) {
+      if (!C.wait(misc->o_full[s], units)) break;
+      ++units;
+      pass_on(misc->v_empty, tiles - 1);
+      tc_fence_after();
+    }
+    const int64_t at = static_cast<int64_t>(w.q_start + row) * P.heads + P.head0 + w.head;  // row of out
+    const int64_t part = static_cast<int64_t>(w.slot) + mine;
+    if (live) {
+      if (w.slot >= 0) P.part_lse[part] = lse;
+      else if (P.lse != nullptr) P.lse[at] = lse;
+    }
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+      uint32_t o[32];
+      __syncwarp();
+      if (tiles > 0) {
+        tmem_ld32(t_o + 32 * k, o);
+        tmem_wait_ld();
+      }
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = empty ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
+      if (live && w.slot >= 0) {
+        float* dst = P.part_out + part * 128 + 32 * k;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t v[8] = {o[8 * e], o[8 * e + 1], o[8 * e + 2], o[8 * e + 3],
+                                 o[8 * e + 4], o[8 * e + 5], o[8 * e + 6], o[8 * e + 7]};
+          st_global_v8(dst + 8 * e, v);
+        }
+      } else if (live) {
+        uint16_t* dst = P.out + at * 128 + 32 * k;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          uint32_t v[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            v[y] = f32x2_to_bf16x2(__uint_as_float(o[16 * e + 2 * y]), __uint_as_float(o[16 * e + 2 * y + 1]));
+          st_global_v8(dst + 16 * e, v);
+        }
+      }
+    }
+    if (tiles > 0) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(C.lead(misc->o_free[s]));
+    }
+    it += max(w.tiles[0], w.tiles[1]);
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
     chunk_attention_kernel(const __grid_constant__ ChunkParams P, const __grid_constant__ CUtensorMap q_map,
                            const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap rope_map) {
@@ -143,12 +487,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sb = smem_addr(smem);
   ChunkMisc* misc = reinterpret_cast<ChunkMisc*>(smem + kOffChunkMisc);
-  volatile int* abort_flag = &misc->abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   auto here = [&](uint64_t& b) -> uint32_t { return smem_addr(&b); };
-  auto lead = [&](uint64_t& b) -> uint32_t { return map_shared_rank(smem_addr(&b), 0); };
-  auto wait = [&](uint64_t& b, uint32_t parity) -> bool { return wait_bar(smem_addr(&b), parity & 1, abort_flag, P.status); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -186,314 +527,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kChunkThreads, 1)
   pdl_wait();
   const uint32_t tmem = misc->tmem_base;
   const int pair = static_cast<int>(cluster_id_x());
-  const int item0 = P.pair_items[pair], item1 = P.pair_items[pair + 1];
-
+  const ChunkCta C = {P, misc, sb, tmem, P.pair_items[pair], P.pair_items[pair + 1]};
+  const bool mixed = *P.any_wide != 0;
   if (warp < 4) {
     // 128 x 72 + 256 x 216 = the launch's 384 x 168 registers
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 && lane == 0) {
-      int it = 0;            // KV tiles loaded
-      int qn[2] = {0, 0};    // query sub-tiles loaded
-      bool ok = true;
-      for (int i = item0; i < item1 && ok; ++i) {
-        const Unit u = read_unit(P, i);
-        const int head = P.head0 + u.head;
-        const int nt = max(u.tiles[0], u.tiles[1]);
-        auto load_q = [&](int s) {
-          if (u.tiles[s] == 0) return true;
-          if (qn[s] > 0 && !wait(misc->q_empty[s], qn[s] - 1)) return false;
-          const uint32_t full = lead(misc->q_full[s]);
-          mbar_arrive_expect_tx_cluster(full, kQSub);
-          for (int k = 0; k < 3; ++k)
-            tma_load_3d_pair(sb + s * kQSub + k * kQSlab, &q_map, 64 * k, head, u.q_start + u.q0 + 256 * s + 128 * rank,
-                             full);
-          ++qn[s];
-          return true;
-        };
-        auto load_k = [&](int j) {
-          const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
-          if (use > 0 && !wait(misc->k_empty[st], use - 1)) return false;
-          const uint32_t full = lead(misc->k_full[st]), at = sb + kOffK + st * kKBytes;
-          const int row = u.kv_start + (u.tb + j) * 128 + 64 * rank;
-          mbar_arrive_expect_tx_cluster(full, kKBytes);
-          tma_load_2d_pair(at, &kv_map, u.head * 256, row, full);
-          tma_load_2d_pair(at + kKSlab, &kv_map, u.head * 256 + 64, row, full);
-          tma_load_2d_pair(at + 2 * kKSlab, &rope_map, 512, row, full);
-          return true;
-        };
-        auto load_v = [&](int j) {
-          const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
-          if (use > 0 && !wait(misc->v_empty[st], use - 1)) return false;
-          const uint32_t full = lead(misc->v_full[st]), at = sb + kOffV + st * kVBytes;
-          const int row = u.kv_start + (u.tb + j) * 128, dim = u.head * 256 + 128 + 64 * rank;
-          mbar_arrive_expect_tx_cluster(full, kVBytes);
-          tma_load_2d_pair(at, &kv_map, dim, row, full);
-          tma_load_2d_pair(at + kVBytes / 2, &kv_map, dim, row + 64, full);
-          return true;
-        };
-        ok = load_q(0);
-        for (int j = 0; j < nt && ok; ++j) {
-          ok = load_k(j);
-          if (j == 0 && ok) ok = load_q(1);
-          if (ok) ok = load_v(j);
-        }
-        it += nt;
-      }
-      if (*abort_flag && rank == 0) {
-        // copies still in flight land on this CTA's barriers: wait for them (bounded)
-        for (int s = 0; s < 2; ++s)
-          if (qn[s] > 0) mbar_wait_drain_cluster(here(misc->q_full[s]), (qn[s] - 1) & 1);
-        for (int st = 0; st < kKvStages; ++st) {
-          mbar_wait_drain_cluster(here(misc->k_full[st]), 0);
-          mbar_wait_drain_cluster(here(misc->k_full[st]), 1);
-          mbar_wait_drain_cluster(here(misc->v_full[st]), 0);
-          mbar_wait_drain_cluster(here(misc->v_full[st]), 1);
-        }
-      }
+      chunk_load(C, q_map, kv_map, rope_map);
     } else if (warp < 3 && rank == 0 && lane == 0) {
-      // The two threads take turns, a tile each: sub-tiles that begin a tile at once would also need their P at once, and the
-      // tensor cores would wait for both softmaxes.
-      auto issuer = [&](auto sub) {
-        constexpr int s = decltype(sub)::value;
-        constexpr uint32_t idesc_s = idesc_bf16_f32(256, 128, 0, 0);
-        constexpr uint32_t idesc_o = idesc_f16_f32(256, 128, 0, 1);  // V: MN-major, 64 dims of each CTA
-        // low words of the descriptors: start address, and a leading offset that neither layout uses
-        const uint32_t q = ((sb + s * kQSub) >> 4) | (1u << 16), k0 = ((sb + kOffK) >> 4) | (1u << 16),
-                       v0 = ((sb + kOffV) >> 4) | (1u << 16);
-        const uint32_t t_s = tmem + s * 128, t_o = tmem + 256 + s * 128;
-        int it = 0, units = 0, scores = 0, turns = 0;  // KV tiles, units begun, score tiles whose P has been waited for, turns taken
-        bool ok = true;
-        for (int i = item0; i < item1 && ok; ++i) {
-          const Unit u = read_unit(P, i);
-          const int nt = max(u.tiles[0], u.tiles[1]), tiles = u.tiles[s];
-          auto issue_s = [&](int j) {  // K of tile j has landed
-            const uint32_t k = k0 + (it + j) % kKvStages * (kKBytes >> 4);
-#pragma unroll
-            for (int x = 0; x < 12; ++x) {
-              mma_bf16_pair_lo(t_s, q + (x >> 2) * (kQSlab >> 4) + (x & 3) * 2, kDescHi,
-                               k + (x >> 2) * (kKSlab >> 4) + (x & 3) * 2, kDescHi, idesc_s, x ? 1u : 0u);
-              // (the other thread sees its turn about when the rest has been issued)
-              if (x == 8 && j > 0) mbar_arrive(here(misc->turn[1 - s]));
-            }
-            mma_commit_pair(here(misc->s_full[s]), 3);
-            if (j + 1 == tiles) mma_commit_pair(here(misc->q_empty[s]), 3);
-          };
-          auto k_landed = [&](int j) { return wait(misc->k_full[(it + j) % kKvStages], (it + j) / kKvStages); };
-          if (tiles > 0) {
-            ok = wait(misc->q_full[s], units) && k_landed(0);
-            if (!ok) break;
-            tc_fence_after();
-            issue_s(0);
-          }
-          for (int j = 0; j < nt; ++j) {
-            const int st = (it + j) % kKvStages, use = (it + j) / kKvStages;
-            if (j >= tiles) {  // the other sub-tile's alone
-              if (!(ok = wait(misc->turn[s], s == 0 ? turns - 1 : turns))) break;
-              ++turns;
-              mbar_arrive(here(misc->turn[1 - s]));
-              continue;
-            }
-            // Everything but P first: a thread that tests a barrier waits until the instructions that it has queued are
-            // dispatched, and a commit costs as much as one or two of them, so neither stands between P's arrival, PV and
-            // the next S (the softmax warps pass on the stages, which their own barriers say have been read).
-            ok = wait(misc->v_full[st], use);
-            if (ok && j + 1 < tiles) ok = k_landed(j + 1);
-            if (ok && j == 0 && units > 0) ok = wait(misc->o_free[s], units - 1);
-            if (ok) ok = wait(misc->p_full[2 * s], scores);
-            if (ok) ok = wait(misc->turn[s], s == 0 ? turns - 1 : turns);
-            if (!ok) break;
-            ++turns;
-            tc_fence_after();
-            const uint32_t v = v0 + st * (kVBytes >> 4);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              mma_bf16_pair_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), kDescHi, idesc_o, (j | x) ? 1u : 0u);
-            if (!(ok = wait(misc->p_full[2 * s + 1], scores))) break;
-            tc_fence_after();
-#pragma unroll
-            for (int x = 4; x < 8; ++x)
-              mma_bf16_pair_ts_lo(t_o, t_s + 8 * x, v + x * (2048 >> 4), kDescHi, idesc_o, 1u);
-            ++scores;
-            if (j + 1 < tiles) {
-              issue_s(j + 1);
-            } else {
-              mma_commit_pair(here(misc->o_full[s]), 3);
-              mbar_arrive(here(misc->turn[1 - s]));
-            }
-          }
-          it += nt;
-          units += tiles > 0;
-        }
-        mma_commit_pair(here(misc->last), 1);
-        mbar_wait_drain_cluster(here(misc->last), 0);
-      };
-      if (warp == 1) issuer(std::integral_constant<int, 0>());
-      else issuer(std::integral_constant<int, 1>());
+      if (!mixed) {
+        if (warp == 1) chunk_issue<0, false>(C);
+        else chunk_issue<1, false>(C);
+      } else {
+        if (warp == 1) chunk_issue<0, true>(C);
+        else chunk_issue<1, true>(C);
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    const int s = (warp - 4) >> 2, quarter = warp & 3;
-    const int mine = 256 * s + 128 * rank + 32 * quarter + lane;  // row of the unit
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t t_s = tmem + lane_off + s * 128, t_o = tmem + lane_off + 256 + s * 128;
-    const uint32_t p_bar[2] = {lead(misc->p_full[2 * s]), lead(misc->p_full[2 * s + 1])};
-    int scores = 0, units = 0, it = 0;
-    bool ok = true;
-    for (int i = item0; i < item1 && ok; ++i) {
-      const Unit u = read_unit(P, i);
-      if (u.head >= P.group_heads) continue;
-      const int tiles = u.tiles[s], others = u.tiles[1 - s];
-      const int lim = row_limit(P.causal, u.len, u.n, u.q0 + mine) - u.tb * 128;  // rows that this query sees, from tb on
-      // The stage of K or V of tile j has been read by this sub-tile's products, and by the other's if it has none there:
-      // each of two arrivals says so for one of them.
-      auto pass_on = [&](uint64_t (&empty)[kKvStages], int j) {
-        if (quarter == 0 && lane == 0) {
-          const uint32_t b = here(empty[(it + j) % kKvStages]);
-          mbar_arrive(b);
-          if (j >= others) mbar_arrive(b);
-        }
-        __syncwarp();
-      };
-      // Weights are 2^(score + e - ref) with e the exponent of their 32 rows' values and ref such that they stay below 2^15;
-      // the sum takes e back out.
-      float ref = -INFINITY, l_run = 0.f;
-      const float4* exps = reinterpret_cast<const float4*>(P.value_exp + static_cast<int64_t>(u.head) * (P.kv_rows >> 5) +
-                                                           (u.kv_start >> 5)) + u.tb;
-      float4 e_next = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (tiles > 0) e_next = exps[0];
-      for (int j = 0; j < tiles; ++j) {
-        const float e[4] = {e_next.x, e_next.y, e_next.z, e_next.w};
-        if (!wait(misc->s_full[s], scores)) {
-          ok = false;
-          break;
-        }
-        ++scores;
-        tc_fence_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(t_s + 32 * k, x + 32 * k);
-        tmem_wait_ld();
-        if (j + 1 < tiles) e_next = exps[j + 1];  // (not before: the wait would be for this load too)
-        const int nv = lim - j * 128;  // columns that this row sees
-        if (__any_sync(0xffffffffu, nv < 128)) {
-#pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if (k >= nv) x[k] = 0xFF800000u;
-        }
-        float top = -INFINITY;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float m = -INFINITY;
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            m = max3(m, __uint_as_float(x[32 * g + 2 * k]), __uint_as_float(x[32 * g + 2 * k + 1]));
-          top = fmaxf(top, fmaf(m, P.scale_log2, e[g]));
-        }
-        const bool raise = top > ref + kWeightMaxLog2;
-        if (__any_sync(0xffffffffu, raise)) {
-          const float a = raise ? fast_exp2(ref - (top - kWeightLog2)) : 1.f;  // (0 for the first rows that a query sees)
-          l_run *= a;
-          if (raise) ref = top - kWeightLog2;
-          if (j > 0) {
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k) {  // (16 columns: the scores fill the registers)
-              uint32_t o[16];
-              tmem_ld16(t_o + 16 * k, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * a);
-              tmem_st16(t_o + 16 * k, o);
-            }
-          }
-        }
-        const float ref_use = ref == -INFINITY ? 0.f : ref;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int gg = 0; gg < 2; ++gg) {
-            const int g = 2 * h + gg;
-            uint32_t p[16];
-            const float off = e[g] - ref_use;
-            const float2 off2 = make_float2(off, off);
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 v = fma2(make_float2(__uint_as_float(x[32 * g + 2 * k]), __uint_as_float(x[32 * g + 2 * k + 1])),
-                                    P.scale_log2, off2);
-              const float2 w = make_float2(fast_exp2(v.x), fast_exp2(v.y));
-              sum[k & 1] = add2(sum[k & 1], w);
-              p[k] = f32x2_to_f16x2(w.x, w.y);
-            }
-            const float2 t = add2(sum[0], sum[1]);
-            l_run = fmaf(t.x + t.y, fast_exp2(-e[g]), l_run);
-            tmem_st16(t_s + 16 * g, p);
-          }
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(p_bar[h]);
-          __syncwarp();
-        }
-        pass_on(misc->k_empty, j);  // (only now: P is waited for, the stages have two tiles' time)
-        if (j > 0) pass_on(misc->v_empty, j - 1);
-      }
-      if (!ok) break;
-      // Out, 32 bytes a store. A row that sees nothing is zeros with an lse of -infinity; a NaN sum stays NaN.
-      const bool empty = l_run == 0.f;
-      const float inv = empty ? 0.f : 1.0f / l_run;
-      const float lse = empty ? -INFINITY : (ref + log2f(l_run)) * 0.6931471805599453f;
-      const Unit w = read_unit(P, i);  // (again: no register holds it while the scores fill them)
-      const int row = w.q0 + mine;
-      const bool live = row < w.n && w.q_start + row < P.tokens;  // (whatever a schedule says)
-      if (tiles > 0) {
-        if (!wait(misc->o_full[s], units)) break;
-        ++units;
-        pass_on(misc->v_empty, tiles - 1);
-        tc_fence_after();
-      }
-      const int64_t at = static_cast<int64_t>(w.q_start + row) * P.heads + P.head0 + w.head;  // row of out
-      const int64_t part = static_cast<int64_t>(w.slot) + mine;
-      if (live) {
-        if (w.slot >= 0) P.part_lse[part] = lse;
-        else if (P.lse != nullptr) P.lse[at] = lse;
-      }
-#pragma unroll 1
-      for (int k = 0; k < 4; ++k) {
-        uint32_t o[32];
-        __syncwarp();
-        if (tiles > 0) {
-          tmem_ld32(t_o + 32 * k, o);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = empty ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);
-        if (live && w.slot >= 0) {
-          float* dst = P.part_out + part * 128 + 32 * k;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t v[8] = {o[8 * e], o[8 * e + 1], o[8 * e + 2], o[8 * e + 3],
-                                   o[8 * e + 4], o[8 * e + 5], o[8 * e + 6], o[8 * e + 7]};
-            st_global_v8(dst + 8 * e, v);
-          }
-        } else if (live) {
-          uint16_t* dst = P.out + at * 128 + 32 * k;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t v[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-              v[y] = f32x2_to_bf16x2(__uint_as_float(o[16 * e + 2 * y]), __uint_as_float(o[16 * e + 2 * y + 1]));
-            st_global_v8(dst + 16 * e, v);
-          }
-        }
-      }
-      if (tiles > 0) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(lead(misc->o_free[s]));
-      }
-      it += max(w.tiles[0], w.tiles[1]);
-    }
+    if (!mixed) chunk_softmax<false>(C);
+    else chunk_softmax<true>(C);
   }
   tc_fence_before();
   __syncthreads();

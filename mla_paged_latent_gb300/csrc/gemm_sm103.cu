@@ -27,6 +27,9 @@ namespace {
 
 // What the epilogue does: bias and residual; an activation between them; or keys and values of the heads.
 enum { kPlain = 0, kSilu = 1, kGelu = 2, kKeysValues = 3 };
+// of values (kKeysValues): their scale, and the bits of the magnitudes that fp16 takes
+constexpr float kValueScale = 1 << kValueLog2;
+constexpr uint32_t kValueMin = (127u + kValueMinLog2) << 23, kValueMax = (127u + kValueMaxLog2) << 23;
 
 __device__ __forceinline__ float2 mul2(float2 a, float b) { return fma2(a, b, make_float2(0.f, 0.f)); }
 __device__ __forceinline__ float fast_rcp(float x) {
@@ -239,33 +242,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (!wait_bar(smem_addr(&misc->acc_full[buf]), (u >> 1) & 1, abort_flag, status)) break;
       tc_fence_after();
       if (KIND == kKeysValues) {
-        // a tile is one head: 128 columns of its keys, 128 of its values. Values leave as fp16, 32 rows scaled by a power
-        // of two of their own that brings their largest to 2^13 .. 2^14 (three bits more than bf16, whatever the values'
-        // range); an infinity or NaN does not count.
+        // a tile is one head: 128 columns of its keys, 128 of its values. 32 rows of values leave as fp16 (three bits more than
+        // bf16) where their largest is of a size that fp16 holds well, else as bf16, which takes any.
         if (row0 < P.rows) {
           uint32_t acc[128], o[32];
 #pragma unroll
           for (int k = 0; k < 4; ++k) tmem_ld32(src + 128 * half + 32 * k, acc + 32 * k);
           tmem_wait_ld();
-          float scale = 1.f;
+          bool wide = true;  // (keys are bf16)
           if (half == 1) {
-            uint32_t top = 0;  // magnitudes compare as integers
+            float largest = 0.f;
 #pragma unroll
-            for (int k = 0; k < 128; ++k) {
-              const uint32_t v = acc[k] & 0x7FFFFFFFu;
-              top = max(top, v < 0x7F800000u ? v : 0u);
+            for (int k = 0; k < 128; k += 2) {
+              const float a = __uint_as_float(acc[k]), b = __uint_as_float(acc[k + 1]);
+              largest = max3(largest, fabsf(a), fabsf(b));
+              acc[k] = __float_as_uint(a * kValueScale);
+              acc[k + 1] = __float_as_uint(b * kValueScale);
             }
-            top = __reduce_max_sync(0xffffffffu, top);
-            const int e = min(max(static_cast<int>(top >> 23) - 127 - 13, kValueExpMin), kValueExpMax);
-            scale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-            if (lane == 0) P.value_exp[static_cast<int64_t>(n0 >> 8) * P.value_exp_stride + (row0 >> 5)] = static_cast<float>(e);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(largest));  // (as integers)
+            wide = top != 0u && (top < kValueMin || top >= kValueMax);
+            if (lane == 0) {
+              P.value_wide[static_cast<int64_t>(n0 >> 8) * P.value_wide_stride + (row0 >> 5)] = wide;
+              if (wide) *P.any_wide = 1;
+            }
           }
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
               const float a = __uint_as_float(acc[64 * c + 2 * k]), b = __uint_as_float(acc[64 * c + 2 * k + 1]);
-              o[k] = half == 0 ? f32x2_to_bf16x2(a, b) : f32x2_to_f16x2(a * scale, b * scale);
+              o[k] = wide ? f32x2_to_bf16x2(a, b) : f32x2_to_f16x2(a, b);
             }
             slab_free(lane);
 #pragma unroll
@@ -587,7 +593,7 @@ cudaError_t launch_gemm_pair(const GemmParams& p, const CUtensorMap& x_map, cons
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(2 * clusters), dim3(kGemmThreads), kGemmSmem, stream, p, x_map, w_map, y_map);
   };
-  if (p.value_exp != nullptr) return go(gemm_pair_kernel<kKeysValues>);
+  if (p.value_wide != nullptr) return go(gemm_pair_kernel<kKeysValues>);
   return p.act == kPlain ? go(gemm_pair_kernel<kPlain>) : p.act == kSilu ? go(gemm_pair_kernel<kSilu>) : go(gemm_pair_kernel<kGelu>);
 }
 

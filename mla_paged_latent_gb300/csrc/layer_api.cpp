@@ -34,15 +34,16 @@ int rows_map(const char* what, CUtensorMap* map, const void* base, int64_t cols,
 
 // Where the parts of a chunk's workspace begin (bytes).
 struct ChunkSpace {
-  size_t rows, kv, value_exp, part_out, part_lse, end;
+  size_t rows, kv, value_wide, any_wide, part_out, part_lse, end;
 };
-ChunkSpace chunk_space(int64_t kv_rows, int64_t group, int64_t slots) {
+ChunkSpace chunk_space(int64_t kv_rows, int64_t heads, int64_t group, int64_t slots) {
   ChunkSpace s;
   const size_t n = static_cast<size_t>(kv_rows < 128 ? 128 : kv_rows);
   s.rows = MLA_WORKSPACE_HEADER;
   s.kv = s.rows + align256(n * 1152);
-  s.value_exp = s.kv + n * static_cast<size_t>(group) * 512;
-  s.part_out = s.value_exp + align256(n / 32 * static_cast<size_t>(group) * 4);
+  s.value_wide = s.kv + n * static_cast<size_t>(group) * 512;
+  s.any_wide = s.value_wide + align256(n / 32 * static_cast<size_t>(group));
+  s.part_out = s.any_wide + align256(static_cast<size_t>((heads + group - 1) / group) * 4);
   s.part_lse = s.part_out + static_cast<size_t>(slots) * 128 * 4;
   s.end = s.part_lse + static_cast<size_t>(slots) * 4;
   return s;
@@ -102,7 +103,7 @@ int mla_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
     info->slots = p.slots;
     const ChunkSections s = chunk_sections(*info);
     info->sched_words = s.end;
-    info->workspace_bytes = chunk_space(rows, group, p.slots).end;
+    info->workspace_bytes = chunk_space(rows, num_heads, group, p.slots).end;
     if (sched == nullptr) return MLA_OK;
     if (sched_capacity < s.end)
       return fail(MLA_ERR_CAPACITY, "mla_chunk_plan: sched needs %lld words, capacity %lld", static_cast<long long>(s.end),
@@ -151,7 +152,7 @@ int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layou
       !aligned_to(out, 32) || !aligned_to(lse, 4) || !aligned_to(block_table, 4))
     return fail(MLA_ERR_INVALID_ARG, "mla_chunk_attention: q, kv_cache, w_kv and sched must be 16-byte and out 32-byte aligned");
   if (!aligned_to(workspace, 256)) return fail(MLA_ERR_INVALID_ARG, "mla_chunk_attention: workspace must be 256-byte aligned");
-  const ChunkSpace space = chunk_space(I.kv_rows, I.group, I.slots);
+  const ChunkSpace space = chunk_space(I.kv_rows, I.heads, I.group, I.slots);
   if (workspace_bytes < space.end)
     return fail(MLA_ERR_WORKSPACE_TOO_SMALL, "mla_chunk_attention: workspace %zu bytes < %zu needed", workspace_bytes, space.end);
   const int64_t T = I.tokens, N = I.heads;
@@ -178,7 +179,7 @@ int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layou
   p.merges = sched + at.merges;
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;
-  p.value_exp = reinterpret_cast<float*>(ws + space.value_exp);
+  p.value_wide = ws + space.value_wide;
   p.part_out = reinterpret_cast<float*>(ws + space.part_out);
   p.part_lse = reinterpret_cast<float*>(ws + space.part_lse);
   p.status = reinterpret_cast<unsigned int*>(ws);
@@ -212,19 +213,24 @@ int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layou
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
+  int32_t* any_wide = reinterpret_cast<int32_t*>(ws + space.any_wide);  // of each group of heads
   if (I.kv_rows > 0) {
+    p.any_wide = any_wide;
+    p.group_heads = I.group;
     e = mla::launch_chunk_rows(static_cast<int>(layout), p, s);
     if (e != cudaSuccess) return cuda_fail(e, "mla_chunk_attention: rows launch");
   }
-  for (int head0 = 0; head0 < I.heads; head0 += I.group) {
+  for (int head0 = 0; head0 < I.heads; head0 += I.group, ++any_wide) {
     p.head0 = head0;
+    p.any_wide = any_wide;
     p.group_heads = I.heads - head0 < I.group ? I.heads - head0 : I.group;
     if (I.kv_rows > 0) {
       mla::GemmParams g;
       std::memset(&g, 0, sizeof g);
       g.status = p.status;
-      g.value_exp = reinterpret_cast<float*>(ws + space.value_exp);
-      g.value_exp_stride = I.kv_rows / 32;
+      g.value_wide = ws + space.value_wide;
+      g.value_wide_stride = I.kv_rows / 32;
+      g.any_wide = any_wide;
       g.rows = I.kv_rows;
       g.cols = p.group_heads * 256;
       g.k_blocks = 8;

@@ -153,8 +153,9 @@ struct GemmParams {
   uint16_t* out;                  // (most of the pair kernel's output goes through its tensor map)
   int64_t out_stride;
   unsigned int* status;           // or null
-  float* value_exp;               // pair: not null for keys and values of heads, [heads, value_exp_stride]: the power of two
-  int64_t value_exp_stride;       // that each 32 rows of a head's values are scaled down by
+  uint8_t* value_wide;            // pair: not null for keys and values of heads, [heads, value_wide_stride]: 1 for each 32 rows
+  int64_t value_wide_stride;      // of a head whose values are held as bf16, 0 where they are fp16
+  int32_t* any_wide;              // pair: set to 1 if any of those is 1
   int32_t rows, cols, k_blocks;   // k_blocks: steps of 64 in K
   int32_t act;                    // 0 none, 1 silu, 2 gelu
   int32_t m_tiles, n_tiles, band; // pair: tiles of 256 x tile_cols; narrow: n_tiles of 128 columns
@@ -167,8 +168,9 @@ cudaError_t launch_gemm_pair(const GemmParams& p, const CUtensorMap& x_map, cons
 cudaError_t launch_gemm_narrow(int rows_a_cta, const GemmParams& p, const CUtensorMap& x_map, const CUtensorMap& w_map,
                                int grid, cudaStream_t stream);
 
-// Range of a value exponent: 2^(120 - 7) between the weights of two groups of rows is still a normal number.
-constexpr int kValueExpMin = -60, kValueExpMax = 60;
+// Values are held times 2^kValueLog2: 32 rows and a head of them as fp16 where the largest is zero or in [2^kValueMinLog2,
+// 2^kValueMaxLog2), with 11 bits down to 2^-22 then, and as bf16 otherwise.
+constexpr int kValueLog2 = 8, kValueMinLog2 = -8, kValueMaxLog2 = 7;
 
 // Attention of a chunk of new tokens (chunk_sm103.cu).
 struct ChunkParams {
@@ -182,7 +184,8 @@ struct ChunkParams {
   const int32_t* merges;          // [merges, 8]: first token, tokens, head, first slot; pieces
   uint16_t* out;                  // bf16 [T, heads, 128]
   float* lse;                     // [T, heads] or null
-  const float* value_exp;         // [group, kv_rows / 32]: values are held times 2^-e
+  const uint8_t* value_wide;      // [group, kv_rows / 32]: 1 where 32 rows of a head's values are bf16, 0 where they are fp16
+  int32_t* any_wide;              // 0 if none of them is 1 (rows: of each group of heads; attention: of this one)
   float* part_out;                // [slots, 128]: a row a query and piece
   float* part_lse;                // [slots]
   unsigned int* status;
