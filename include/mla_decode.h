@@ -515,8 +515,8 @@ int mla_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
  * values is zero or in [2^-8, 2^7) (a value is then off by 2^-11 of itself or 2^-33 at most, a weight by 2^-11 of itself or 2^-32 of
  * the query's largest), to bf16 otherwise (2^-8 of itself), whatever the size of other rows' values. Sums, maxima and the
  * accumulator are fp32. A score, and so lse, is off by up to 2^-8 of the sum of its terms' magnitudes for K's rounding. |V| must stay
- * below 2^80: larger values may become infinite. A NaN or infinity in a row makes NaN of query rows of the
- * request that do not see it too, if they are computed with its tile of 128 rows.
+ * below 2^80: larger values may become infinite, for query rows computed with their tile of 128 rows too that do not see them. A NaN
+ * or infinity in a cached row makes NaN of out and lse of the query rows that see it, and of no others.
  */
 int mla_chunk_attention(const void* q, const void* kv_cache, mla_kv_layout layout, int64_t num_pages, int32_t page_size,
                         const int32_t* block_table, int32_t max_pages, const void* w_kv, float sm_scale,

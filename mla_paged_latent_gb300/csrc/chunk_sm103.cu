@@ -54,7 +54,14 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
     if (lane < 8) dst[64 + lane] = make_uint4(0, 0, 0, 0);
     return;
   }
-  read_row<LAYOUT>(P.kv + page * P.page_bytes, pos & (P.page_size - 1), P.page_size, lane, dst);
+  const bool bad = read_row<LAYOUT>(P.kv + page * P.page_bytes, pos & (P.page_size - 1), P.page_size, lane, dst);
+  // An infinity or NaN in the latent part would be one in all of V, and 0 times it NaN for queries of the tile that do not see the
+  // row. It goes into the key instead, whose scores are masked: NaN for those that see it.
+  if (__any_sync(0xffffffffu, bad)) {
+    dst[lane] = make_uint4(0, 0, 0, 0);
+    dst[32 + lane] = make_uint4(0, 0, 0, 0);
+    if (lane < 8) dst[64 + lane] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+  }
 }
 
 // ----------------------------------------------------------------------------- attention

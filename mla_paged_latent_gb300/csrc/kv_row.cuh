@@ -236,10 +236,13 @@ __device__ __forceinline__ void norm_rope_row(const uint16_t* x, const uint16_t*
   norm_rope_row_by(x, w, eps, [&](int i, int) { return make_float2(f[2 * i], f[2 * i + 1]); }, width, lane, srow);
 }
 
+// Bits 15 and 31 of the result: whether the bf16 in either half of w is an infinity or NaN.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return (w & 0x7F807F80u) + 0x00800080u; }
+
 // The row at offset `off` of the page pg, decoded to bf16 into dst, by one warp. A lane takes eight elements a step, so
-// loads and stores of a warp are contiguous.
+// loads and stores of a warp are contiguous. Returns whether this lane's part of the NoPE elements has an infinity or NaN.
 template <int LAYOUT>
-__device__ __forceinline__ void read_row(const uint8_t* pg, int off, int page_size, int lane, uint4* dst) {
+__device__ __forceinline__ bool read_row(const uint8_t* pg, int off, int page_size, int lane, uint4* dst) {
   constexpr int kNope = row_nope(LAYOUT), kRowBytes = row_stored_bytes(LAYOUT);
   constexpr int kCodeBytes = LAYOUT == 0 ? 1024 : LAYOUT <= 2 ? kNope : kNope / 2;
   const uint8_t* src = pg + (int64_t)off * kRowBytes;
@@ -264,25 +267,28 @@ __device__ __forceinline__ void read_row(const uint8_t* pg, int off, int page_si
       sb[h] = sc[c >> 2];
     }
   }
+  uint32_t bad = 0;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int c = lane + 32 * h;
     if (8 * c >= kNope) break;
-    if (LAYOUT == 0) {
-      dst[c] = raw[h];
-    } else if (LAYOUT <= 2) {
+    uint4 v = raw[h];
+    if (LAYOUT != 0 && LAYOUT <= 2) {
       const float s = ue8m0_to_f32(sb[h]);
       const float2 a = e4m3x2_to_f32x2(raw[h].x & 0xFFFFu), b = e4m3x2_to_f32x2(raw[h].x >> 16);
       const float2 d = e4m3x2_to_f32x2(raw[h].y & 0xFFFFu), e = e4m3x2_to_f32x2(raw[h].y >> 16);
-      dst[c] = make_uint4(f32x2_to_bf16x2(a.x * s, a.y * s), f32x2_to_bf16x2(b.x * s, b.y * s),
-                          f32x2_to_bf16x2(d.x * s, d.y * s), f32x2_to_bf16x2(e.x * s, e.y * s));
-    } else {
+      v = make_uint4(f32x2_to_bf16x2(a.x * s, a.y * s), f32x2_to_bf16x2(b.x * s, b.y * s),
+                     f32x2_to_bf16x2(d.x * s, d.y * s), f32x2_to_bf16x2(e.x * s, e.y * s));
+    } else if (LAYOUT > 2) {
       uint32_t o[4];
       fp4x8_to_bf16(raw[h].x, fp4_scale(sb[h]), o);
-      dst[c] = make_uint4(o[0], o[1], o[2], o[3]);
+      v = make_uint4(o[0], o[1], o[2], o[3]);
     }
+    dst[c] = v;
+    bad |= not_finite2(v.x) | not_finite2(v.y) | not_finite2(v.z) | not_finite2(v.w);
   }
   if (lane < 8) dst[kNope / 8 + lane] = pe;
+  return (bad & 0x80008000u) != 0u;
 }
 
 }  // namespace mla
