@@ -72,11 +72,12 @@ int mla_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
   if (!q_lens || !kv_lens || !info) return fail(MLA_ERR_INVALID_ARG, "mla_chunk_plan: NULL argument");
   if (batch < 1 || num_heads < 1 || num_sms < 2)
     return fail(MLA_ERR_INVALID_ARG, "mla_chunk_plan: batch=%d heads=%d num_sms=%d out of range", batch, num_heads, num_sms);
-  int64_t tokens = 0, rows = 0;
+  int64_t tokens = 0, rows = 0, tiles = 0;
   for (int b = 0; b < batch; ++b) {
     if (q_lens[b] < 0 || kv_lens[b] < 0)
       return fail(MLA_ERR_INVALID_ARG, "mla_chunk_plan: lengths of request %d are %d and %d", b, q_lens[b], kv_lens[b]);
     tokens += q_lens[b];
+    tiles += (static_cast<int64_t>(q_lens[b]) + 511) / 512;
     if (q_lens[b] > 0) rows += (static_cast<int64_t>(kv_lens[b]) + 127) / 128 * 128;
   }
   if (num_heads > 4096 || tokens * num_heads >= (1ll << 31) - 512 || rows >= (1ll << 31) - 512)
@@ -88,6 +89,9 @@ int mla_chunk_plan(const int32_t* q_lens, const int32_t* kv_lens, int32_t batch,
   group = group < 1 ? 1 : group > num_heads ? num_heads : group;
   const int64_t groups = (num_heads + group - 1) / group;
   group = (num_heads + groups - 1) / groups;
+  if (tiles * group > (1ll << 27))  // (words of the schedule are found by 32-bit indices, 12 of them a unit)
+    return fail(MLA_ERR_UNSUPPORTED, "mla_chunk_plan: %lld query tiles of %lld heads at once are too many units",
+                static_cast<long long>(tiles), static_cast<long long>(group));
   try {
     const mla::ChunkPlan p = mla::make_chunk_plan(q_lens, kv_lens, batch, num_heads, causal != 0, static_cast<int>(group), num_sms);
     std::memset(info, 0, sizeof *info);
