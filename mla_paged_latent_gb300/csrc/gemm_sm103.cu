@@ -368,7 +368,7 @@ struct NarrowMisc {
   unsigned int status;
 };
 
-// NT rows of x a CTA. Stages fill 96 KB, so that two CTAs share an SM and one's first loads run under the other's last
+// Up to NT rows of x, all of them in each CTA. Stages fill 96 KB, so that two CTAs share an SM and one's first loads run under the other's last
 // sums.
 template <int NT>
 struct Narrow {
@@ -417,8 +417,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
   pdl_trigger();
   pdl_wait();
   const uint32_t tmem = misc->tmem_base;
-  const int tile = static_cast<int>(blockIdx.x) / PARTS;
-  const int f0 = (tile % P.n_tiles) * 128, t0 = (tile / P.n_tiles) * NT;
+  const int f0 = static_cast<int>(blockIdx.x) / PARTS * 128;  // (all rows of x are one tile)
   const int k0 = static_cast<int>(static_cast<int64_t>(P.k_blocks) * rank / PARTS);
   const int k1 = static_cast<int>(static_cast<int64_t>(P.k_blocks) * (rank + 1) / PARTS);
 
@@ -432,7 +431,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
         const uint32_t full = smem_addr(&misc->full[s]);
         mbar_arrive_expect_tx(full, C::kStage);
         tma_load_2d(sb + s * C::kStage, &w_map, 64 * k, f0, full);
-        tma_load_2d(sb + s * C::kStage + C::kW, &x_map, 64 * k, t0, full);
+        tma_load_2d(sb + s * C::kStage + C::kW, &x_map, 64 * k, 0, full);
       }
       if (*abort_flag)
         for (int k = 1; k <= C::kStages && it - k >= 0; ++k)
@@ -493,16 +492,15 @@ __global__ void __launch_bounds__(kNarrowThreads)
     bias[2] = __uint_as_float(b.y << 16);
     bias[3] = __uint_as_float(b.y & 0xFFFF0000u);
   }
-  const int rows = min(NT, P.rows - t0);
-  for (int i0 = warp * PARTS + rank; i0 < rows; i0 += kAtOnce * kWarps * PARTS) {
+  for (int i0 = warp * PARTS + rank; i0 < P.rows; i0 += kAtOnce * kWarps * PARTS) {
     float4 y[kAtOnce];
     uint2 res[kAtOnce];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int i = i0 + u * kWarps * PARTS;
       res[u] = make_uint2(0, 0);
-      if (P.residual != nullptr && i < rows && inside)
-        res[u] = *reinterpret_cast<const uint2*>(P.residual + (t0 + i) * P.residual_stride + f0 + f);
+      if (P.residual != nullptr && i < P.rows && inside)
+        res[u] = *reinterpret_cast<const uint2*>(P.residual + i * P.residual_stride + f0 + f);
     }
     float4 v[PARTS][kAtOnce];
 #pragma unroll
@@ -511,7 +509,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
         const int i = i0 + u * kWarps * PARTS;
-        v[p][u] = i < rows ? ld_shared_cluster_v4(peer + i * 512) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[p][u] = i < P.rows ? ld_shared_cluster_v4(peer + i * 512) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     }
 #pragma unroll
@@ -528,7 +526,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const int i = i0 + u * kWarps * PARTS;
-      if (i >= rows || !inside) continue;
+      if (i >= P.rows || !inside) continue;
       float v[4] = {y[u].x + bias[0], y[u].y + bias[1], y[u].z + bias[2], y[u].w + bias[3]};
       if (P.act != kPlain) {
 #pragma unroll
@@ -545,7 +543,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
         v[2] += __uint_as_float(res[u].y << 16);
         v[3] += __uint_as_float(res[u].y & 0xFFFF0000u);
       }
-      *reinterpret_cast<uint2*>(P.out + (t0 + i) * P.out_stride + f0 + f) =
+      *reinterpret_cast<uint2*>(P.out + i * P.out_stride + f0 + f) =
           make_uint2(f32x2_to_bf16x2(v[0], v[1]), f32x2_to_bf16x2(v[2], v[3]));
     }
   }

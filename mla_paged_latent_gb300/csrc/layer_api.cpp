@@ -314,13 +314,12 @@ int mla_linear(const void* x, int64_t x_stride, const void* weight, const void* 
     const int nt = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
     if (int rc = rows_map("mla_linear: x", &x_map, x, inner, rows, x_stride, 64, nt)) return rc;
     if (int rc = rows_map("mla_linear: weight", &w_map, weight, inner, outer, inner, 64, 128)) return rc;
-    g.n_tiles = (outer + 127) / 128;
-    g.m_tiles = 1;
+    const int n_tiles = (outer + 127) / 128;
     g.split = 1;
-    // CTAs enough for the SMs (two fit one), with eight steps of K each at least: 1 x 16384 x 8192 in 72, 49, 42 and 46 us at 1,
+    // CTAs enough for the SMs (two fit one), with four steps of K each at least: 1 x 16384 x 8192 in 72, 49, 42 and 46 us at 1,
     // 2, 4 and 8
-    while (g.split < 8 && static_cast<int64_t>(g.n_tiles) * g.split < num_sms && g.k_blocks >= 8 * g.split) g.split *= 2;
-    e = mla::launch_gemm_narrow(nt, g, x_map, w_map, g.n_tiles * g.split, s);
+    while (g.split < 8 && static_cast<int64_t>(n_tiles) * g.split < num_sms && g.k_blocks >= 8 * g.split) g.split *= 2;
+    e = mla::launch_gemm_narrow(nt, g, x_map, w_map, n_tiles * g.split, s);
   } else {
     if (int rc = rows_map("mla_linear: x", &x_map, x, inner, rows, x_stride, 64, 128)) return rc;
     if (int rc = rows_map("mla_linear: out", &y_map, out, outer, rows, out_stride, 64, 32)) return rc;

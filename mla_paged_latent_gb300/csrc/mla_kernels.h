@@ -158,7 +158,7 @@ struct GemmParams {
   int32_t* any_wide;              // pair: set to 1 if any of those is 1
   int32_t rows, cols, k_blocks;   // k_blocks: steps of 64 in K
   int32_t act;                    // 0 none, 1 silu, 2 gelu
-  int32_t m_tiles, n_tiles, band; // pair: tiles of 256 x tile_cols; narrow: n_tiles of 128 columns
+  int32_t m_tiles, n_tiles, band; // pair: tiles of 256 x tile_cols (narrow: not read, the grid has a CTA for 128 columns and part)
   int32_t tile_cols;              // pair: 128 to 256, a multiple of 32 (its half: rows of W in a box of w_map)
   int32_t w_row0;                 // pair: first row of W
   int32_t split;                  // narrow: CTAs that share a tile's K
