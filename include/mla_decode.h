@@ -484,7 +484,8 @@ int mla_qkv_norm_rope_axes(const void* q_nope, int64_t q_nope_token_stride, int6
  *  info            what mla_chunk_attention needs beside sched, passed on as it is.
  * Rule: the queries of a request and head are cut into tiles of 512; each is a unit for one pair of SMs, handed out head by
  * head, longest first, to the pair that is free first by a cost of their KV tiles of 128 rows. Where that leaves pairs idle for
- * longer than a merge takes, the units are cut over the KV tiles into equal shares and the partial results merged. More than 2^27
+ * longer than a merge takes, the units are cut over the KV tiles into equal shares and the partial results merged; but only up to
+ * three units a pair, or eight where no request has more than 512 queries or K and V of the heads expanded at once are at most 96 MB. More than 2^27
  * units of the heads that are expanded at once are refused (MLA_ERR_UNSUPPORTED).
  */
 typedef struct {

@@ -15,7 +15,7 @@ namespace mla {
 namespace {
 
 // Costs in tenths of what two sub-tiles (of 256 queries) take for a KV tile, measured in SM cycles: two sub-tiles whose products
-// and softmax run under each other take 3090 (1.6 us), one alone 2780. What a unit costs besides (loads of Q, the first scores,
+// and softmax run under each other take 3250 (1.7 us), one alone 2880. What a unit costs besides (loads of Q, the first scores,
 // the epilogue; about 5 us). What a merge costs, and one more for so many rows of partial results (516 bytes, written and read).
 constexpr int64_t kBoth = 10, kAlone = 9;
 constexpr int64_t kUnitCost = 30;

@@ -7,14 +7,13 @@
 // (row, head) once. Three steps on one stream, and a fourth where the rows are few:
 //   chunk_rows_kernel  the requests' rows, in order, as bf16 [rows, 576]; each request starts at a multiple of 128 and the
 //                      rows up to the next are zeros, so that a masked row is never what memory happened to hold;
-//   the product of the latent part with W (gemm_pair_kernel), K (bf16) and V (fp16 or bf16) of a group of heads [rows, heads, 256]
-//                      (operands of the tensor cores; the sums are fp32), which attention then reads many times;
+//   the product of the latent part with W (gemm_pair_kernel), K (bf16) and V (fp16 or bf16) of a group of heads
+//                      [rows, heads, 256] (operands of the tensor cores; the sums are fp32), which attention then reads many times;
 //   chunk_attention_kernel;
 //   chunk_merge_kernel where a query tile was split over the rows.
-// One after the other on 2048 queries after 32768 bf16 rows at 128 heads: 13, 735 and 3168 us (1.79 PFLOP/s of 640 operations a
-// query, row and head; in a loop the power limit makes 4.3 ms of the three).
+// One after the other on 2048 queries after 32768 bf16 rows at 128 heads: 13, 742 and 3150 us (1.80 PFLOP/s of 640 operations a
+// query, row and head; in a loop the power limit makes 4.3 to 4.4 ms of the three).
 #include <cstdint>
-#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "decode_common.cuh"
@@ -75,9 +74,10 @@ __global__ void __launch_bounds__(256) chunk_rows_kernel(const __grid_constant__
 // TMEM: S of the two sub-tiles (128 columns each; P as fp16 pairs takes the first 64 once S has been read) and O (128 each).
 // A thread for each sub-tile issues PV(j) S(j+1) in turn: S(j+1) follows the PV(j) that reads P from the same columns, and
 // its completion says that O holds tile j, so a rescale of O needs no barrier of its own.
-// Bound by the tensor cores in the end: 2 x 1280 cycles of products a KV tile and unit, 3090 traced. One issuing thread took
-// 4790 (its barrier tests and commits stood between the products), two that run freely 5040 (both softmaxes at once); turns
-// 3730, stages passed on by the softmax warps 3560, P in halves and nothing spilled 3090.
+// Bound by the tensor cores in the end: 2 x 1280 cycles of products a KV tile and unit. One issuing thread took 4790 (its barrier
+// tests and commits stood between the products), two that run freely 5040 (both softmaxes at once); turns 3730, stages passed on by
+// the softmax warps 3560, P in halves and nothing spilled 3090 (traced again, at other clocks: 3250, with values in bf16 3430; one
+// sub-tile alone 2880 and 3050).
 // P and V are fp16 where the values of 32 rows are of a size that fp16 holds well, and bf16 where they are not (an instruction has
 // 16 rows, so its type may differ from the next one's): a scale of V for every 32 rows, which P makes good, would cost the weights of
 // rows whose values are smaller by far their bits. P is kept below 2^15 by a reference that moves (and O is rescaled) only

@@ -7,14 +7,15 @@
 // gemm_pair_kernel: many rows. Two SMs work as one tensor-core pair (tcgen05 .cta_group::2) on a tile of 256 rows x 256
 // columns (or fewer, a multiple of 32): each holds its 128 rows of x and half of W's 256 rows of a slab, 32 KB a step of
 // 64 in K for 2 x 256 x 256 x 64 operations, half of what two single SMs would move. Sums lie in TMEM twice, so that one
-// tile's epilogue runs under the next one's products. Bound by the tensor cores: 4096 x 16384 x 8192 in 600 us, 1.83
-// PFLOP/s, at the power limit (cuBLAS 638 beside it); 4096 x 4096 x 4096 in 79 us. Six stages of one slab (three of two:
+// tile's epilogue runs under the next one's products. Bound by the tensor cores: 4096 x 16384 x 8192 in 573 us
+// for a few calls (1.92 PFLOP/s), in a loop 600 to 690 by what the power limit leaves (cuBLAS likewise: 568, and in turn in a loop
+// 642 to 669 beside 651 to 657); 4096 x 4096 x 4096 in 79 us. Six stages of one slab (three of two:
 // 83.6 us against 80.1 of the last; five: 82.2); one staging slab a warp makes room for the sixth.
 //
 // gemm_narrow_kernel: few rows. Bound by W's bytes, so W takes the M side of the instruction (128 of its rows a CTA) and
 // the rows of x the N side (16 to 128), and K is split over the CTAs of a cluster, whose sums meet through distributed
 // shared memory in the order of their ranks: no workspace, no atomics, the same result every time. 1 x 16384 x 8192 in
-// 42.5 us (6.3 TB/s, 93 % of a copy's), 64 rows 46; what the wider x costs is mostly the exchange of sums.
+// 42.4 us (6.3 TB/s, 93 % of a copy's), 64 rows 45; what the wider x costs is mostly the exchange of sums.
 #include <cstdint>
 #include <cuda_runtime.h>
 
