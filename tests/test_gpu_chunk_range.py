@@ -95,3 +95,42 @@ def test_cut_units_of_values_apart(causal):
     new, lens = [70, 300], [6000, 4000]
     q, cache, w = split_values(6, new, lens, 2, lambda at: torch.where(at // 32 % 7 == 2, 30, 0))
     assert check(q, cache, new, w, causal).slots > 0
+
+
+@pytest.mark.parametrize("head", [0, 3, 6])
+def test_one_head_of_a_group_of_heads(head):
+    """Values of one head out of fp16's range, heads expanded two at a time: every head to its own accuracy."""
+    new, lens = [300, 7], [900, 333]
+    q, cache, w = split_values(7, new, lens, 7, lambda at: torch.zeros_like(at))
+    w[head, 128:192] *= 2.0 ** 45
+    rows = sum(-(-n // 128) * 128 for n in lens)
+    assert check(q, cache, new, w, kv_budget=2 * rows * 512).group == 2
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_one_workspace_for_calls_of_either_kind(graph):
+    """Values in fp16's range, out of it and in it again, in the same buffers: each call as in buffers of its own."""
+    new, lens, heads = [300, 7], [900, 333], 3
+    q, cache, small = split_values(8, new, lens, heads, lambda at: torch.zeros_like(at))
+    large = small.clone()
+    large[1, 128:] *= 2.0 ** 30
+    want = [run_chunk(q, cache, new, w, SCALE)[:2] for w in (small, large)]
+    plan = mla.mla_chunk_plan(new, lens, heads)
+    sched, ws = torch.from_numpy(plan.sched).cuda(), mla.alloc_workspace(plan.workspace_bytes)
+    w, out, lse = small.clone(), torch.empty_like(want[0][0]), torch.empty_like(want[0][1])
+
+    def run():
+        mla.mla_chunk_attention(q, cache.data, 0, PAGE, cache.table, w, SCALE, plan, sched, ws, out, lse)
+    if graph:
+        run()
+        torch.cuda.synchronize()
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            run()
+        run = captured.replay
+    for k in (0, 1, 0, 1, 1, 0, 0):
+        w.copy_((small, large)[k])
+        run()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[k][0]) and torch.equal(lse, want[k][1])
+    assert not torch.equal(want[0][0], want[1][0])
