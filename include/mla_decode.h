@@ -476,7 +476,7 @@ int mla_qkv_norm_rope_axes(const void* q_nope, int64_t q_nope_token_stride, int6
  * no row gives zeros and an lse of -infinity.
  *
  * mla_chunk_plan (host): the schedule of a batch, for any number of calls (layers) with these lengths.
- *  q_lens, kv_lens host int32 [batch].
+ *  q_lens, kv_lens host int32 [batch]. num_heads is 1 to 4096; tokens times heads, and rows, end at 2^31 - 512.
  *  kv_budget       bytes for K and V of the heads that are expanded at once: 512 a row (each request's rows rounded up to 128)
  *                  and head. Where not all heads fit they go in groups, one after another; one head always goes.
  *  num_sms         SMs of the device.

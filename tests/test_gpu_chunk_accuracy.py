@@ -44,12 +44,15 @@ def test_norm_of_the_error(keys, limit, layout, new, lens):
 
 
 @pytest.mark.parametrize("length", [1, 2, 3, 5, 8])
-def test_every_element_of_few_rows(length):
+@pytest.mark.parametrize("small", [0, 18, 30])
+def test_every_element_of_few_rows(length, small):
     """Scores without a rounding of K: a weight is off by 2^-11, V by 2^-11 of itself or 2^-33, the exponential and the sum by
     2^-18, the result by 2^-8; sums of 64 products by 2^-17 of their magnitudes in a score of at most 2^5. V's own sum of 512
-    products in fp32, taken off by 512 2^-23 of their magnitudes, is what the rows below are measured against."""
+    products in fp32, taken off by 512 2^-23 of their magnitudes, is what the rows below are measured against. Half of the dims are
+    smaller by 2^small."""
     new, lens = [1] * 40, [length] * 40
     q, cache, w = make(2, new, lens, 8, 0, keys=False)
+    w[:, 128:192] *= 2.0 ** -small
     out, _, _, ws = run_chunk(q, cache, new, w, SCALE)
     assert mla.mla_read_status(ws) == 0
     scale = torch.tensor(SCALE, dtype=torch.float32).double().item()

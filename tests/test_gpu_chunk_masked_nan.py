@@ -64,6 +64,7 @@ def test_a_row_larger_than_all_others_by_far(new, lens, at):
     cache = Cache(g, lens, 0, 16)
     q, w = normal(g, sum(new), 2, 192), normal(g, 2, 256, 512, scale=512 ** -0.5)
     w[:, 128:, 9] = w[:, 128:, 9].clamp(-0.25, 0.25)
+    want = run_chunk(q, cache, new, w, SCALE)[0]
     row = normal(generator(5), 1, 576)
     row[0, 9] = 2.0 ** 120
     mla.mla_kv_write(row, torch.tensor([slot_of(cache, 0, at)], dtype=torch.int32, device="cuda"), cache.data, 0, 16)
@@ -73,3 +74,4 @@ def test_a_row_larger_than_all_others_by_far(new, lens, at):
     sees[:new[0]] = lens[0] - new[0] + torch.arange(new[0], device="cuda") >= at
     assert ((out.double() - ref).abs() <= bound)[~sees].all()
     assert ((lse.double() - ref_lse).abs() <= lse_bound)[~sees].all()
+    assert torch.equal(out[new[0]:], want[new[0]:])  # the other request's
